@@ -16,6 +16,17 @@ calls raise.
 Layer edges (fused into the kernels, off by default): norm_k=True
 L2-normalises every key row where it is loaded (dk comes back with respect to
 the raw keys); D [H] fp32 adds the skip term o_t += D[h] v_t (bwd returns dD).
+
+The latent-attention layers of the hybrid stack, and their paged cache
+(latent.py):
+
+    o, lse    = mla_fwd(q, k, v, k_rope, lens)                 # expanded heads, causal
+    grads     = mla_bwd(q, k, v, o, lse, do, k_rope, lens)
+    o         = LatentAttention.apply(q, k, v, k_rope, lens, scale)
+    y         = norm_rope(x, weight, positions, freqs)         # per-head norm and rotation
+    plan      = page_plan(lens, new_lens, block_table, free_pages, n_free, page_size, max_tokens)
+    cache     = mla_write(c, k_rope, plan["slots"], cache, weight, plan["positions"], freqs)
+    o, lse    = mla_step(q, cache, block_table, plan["lens"], dl, scale=scale)
 """
 from __future__ import annotations
 
@@ -26,13 +37,16 @@ import torch
 
 __all__ = ["fwd", "fwd_noalloc", "bwd", "step", "step_tokens", "GatedDeltaRule", "GdnError", "lib", "EXPORTS",
            "LIB_PATH", "context_size", "context_states", "fwd_workspace_size", "bwd_workspace_size",
-           "LaunchTimer", "NOALLOC_SCRATCH_BYTES"]
+           "LaunchTimer", "NOALLOC_SCRATCH_BYTES", "mla_fwd", "mla_bwd", "LatentAttention", "mla_step", "norm_rope",
+           "norm_rope_bwd", "NormRope", "mla_write", "page_plan"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn.so")
 EXPORTS = ["gdn_fwd", "gdn_bwd", "gdn_step", "gdn_step_tokens", "gdn_fwd_workspace_size", "gdn_bwd_workspace_size",
            "gdn_fwd_context_size", "gdn_time_launches", "gdn_launch_kind", "gdn_status_string",
-           "gdn_last_error_detail", "gdn_fwd_noalloc"]
+           "gdn_last_error_detail", "gdn_fwd_noalloc", "gdn_mla_fwd", "gdn_mla_bwd", "gdn_mla_bwd_workspace_size",
+           "gdn_mla_step", "gdn_mla_step_workspace_size", "gdn_norm_rope", "gdn_norm_rope_bwd",
+           "gdn_norm_rope_bwd_workspace_size", "gdn_mla_write", "gdn_page_plan"]
 
 GDN_F32, GDN_BF16 = 0, 1
 NOALLOC_SCRATCH_BYTES = 64 << 20  # GDN_NOALLOC_SCRATCH_BYTES of include/gdn.h
@@ -55,6 +69,16 @@ class Shape(ctypes.Structure):
                 ("chunk", ctypes.c_int32), ("flags", ctypes.c_uint32)]
 
 
+class MlaShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "Tq", "Tk", "H", "Hk", "Hr", "dn", "dr", "dv", "dtype")] + [
+        ("scale", ctypes.c_float)]
+
+
+class MlaStepShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("N", "S", "H", "dl", "dr", "dtype", "pages", "page_size",
+                                              "max_pages")] + [("scale", ctypes.c_float)]
+
+
 def lib():
     """Load libgdn.so (raises if it has not been built)."""
     global _lib
@@ -74,6 +98,23 @@ def lib():
             f.restype = ctypes.c_int
         for f in (L.gdn_fwd_workspace_size, L.gdn_bwd_workspace_size, L.gdn_fwd_context_size):
             f.argtypes = [S]
+            f.restype = Z
+        I64, F = ctypes.c_int64, ctypes.c_float
+        A, D = ctypes.POINTER(MlaShape), ctypes.POINTER(MlaStepShape)
+        L.gdn_mla_fwd.argtypes = [A, P, P, P, P, P, P, P, P]
+        L.gdn_mla_bwd.argtypes = [A, P, P, P, P, P, P, P, P, P, P, P, P, P, Z, P]
+        L.gdn_mla_step.argtypes = [D, P, P, P, P, P, P, P, Z, P]
+        L.gdn_norm_rope.argtypes = [I64, I32, I32, I32, I32, U32, F, P, P, P, P, P, P]
+        L.gdn_norm_rope_bwd.argtypes = [I64, I32, I32, I32, I32, U32, F, P, P, P, P, P, P, P, P, Z, P]
+        L.gdn_mla_write.argtypes = [I64, I32, I32, I32, U32, F, P, P, P, P, P, P, P, I64, P]
+        L.gdn_page_plan.argtypes = [I32, I32, I32, I32, I32] + [P] * 12
+        for f in (L.gdn_mla_fwd, L.gdn_mla_bwd, L.gdn_mla_step, L.gdn_norm_rope, L.gdn_norm_rope_bwd,
+                  L.gdn_mla_write, L.gdn_page_plan):
+            f.restype = ctypes.c_int
+        L.gdn_mla_bwd_workspace_size.argtypes = [A]
+        L.gdn_mla_step_workspace_size.argtypes = [D]
+        L.gdn_norm_rope_bwd_workspace_size.argtypes = [I64, I32, I32]
+        for f in (L.gdn_mla_bwd_workspace_size, L.gdn_mla_step_workspace_size, L.gdn_norm_rope_bwd_workspace_size):
             f.restype = Z
         L.gdn_time_launches.argtypes = [P, I32]
         L.gdn_time_launches.restype = I32
@@ -373,7 +414,9 @@ class LaunchTimer:
         n = min(self.count, len(self.events) // 2)
         return [self.events[2 * i].elapsed_time(self.events[2 * i + 1]) for i in range(n)]
 
-    KINDS = ("fwd_prep", "fwd_chain", "bwd_chain", "bwd_local", "dA_reduce", "step", "fwd_scan", "bwd_scan")
+    KINDS = ("fwd_prep", "fwd_chain", "bwd_chain", "bwd_local", "dA_reduce", "step", "fwd_scan", "bwd_scan",
+             "mla_fwd", "mla_bwd_q", "mla_bwd_k", "mla_rope_sum", "mla_step", "mla_join", "norm_rope",
+             "norm_rope_bwd", "norm_sum", "mla_write", "page_plan", "page_fill")
 
     def kinds(self):
         """Kernel name of every bracketed launch, in launch order."""
@@ -406,3 +449,7 @@ class GatedDeltaRule(torch.autograd.Function):
                 want_dD=D is not None and ctx.needs_input_grad[10], want_dh0=h0 is not None)
         return (r["dq"], r["dk"], r["dv"], r["dg"], r["dbeta"], r["dA_log"], r["dh0"], None, None, None,
                 r["dD"])
+
+
+from .latent import (LatentAttention, NormRope, mla_bwd, mla_fwd, mla_step, mla_write, norm_rope,  # noqa: E402
+                     norm_rope_bwd, page_plan)

@@ -14,7 +14,9 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libgdn.so")
 OBJDIR = os.path.join(HERE, "_build")
-SOURCES = ["gdn_fwd.hip", "gdn_bwd.hip", "gdn_bwd128.hip", "gdn_step.hip", "gdn_util.hip", "gdn_noalloc.hip", "gdn_api.cpp"]
+SOURCES = ["gdn_fwd.hip", "gdn_bwd.hip", "gdn_bwd128.hip", "gdn_step.hip", "gdn_util.hip", "gdn_noalloc.hip", "gdn_api.cpp",
+           "gdn_mla_fwd_bf16.hip", "gdn_mla_fwd_f32.hip", "gdn_mla_bwd_q_bf16.hip", "gdn_mla_bwd_k_bf16.hip",
+           "gdn_mla_bwd_f32.hip", "gdn_mla_step.hip", "gdn_norm_rope.hip", "gdn_pages.hip", "gdn_mla_api.cpp"]
 ARCH = "gfx950"
 
 FLAGS = [

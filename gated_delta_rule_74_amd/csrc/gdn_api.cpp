@@ -10,6 +10,7 @@
 #include <string.h>
 
 #include "gdn_launch.hpp"
+#include "gdn_mla.hpp"
 
 namespace {
 
@@ -138,21 +139,9 @@ thread_local int g_kind_n = 0; // launches logged by the last bracketing period
 enum Kind { K_FWD_PREP = 0, K_FWD_CHAIN, K_BWD_CHAIN, K_BWD_LOCAL, K_DA_REDUCE, K_STEP, K_FWD_SCAN, K_BWD_SCAN };
 
 template <class F> hipError_t timed(Kind kind, F &&launch, hipStream_t st) {
-    const int i = g_launch;
-    if (g_events && i < KIND_LOG) g_kinds[i] = (int8_t)kind;
-    const bool on = g_events && 2 * i + 1 < g_nevents;
-    if (on) {
-        const hipError_t e = hipEventRecord((hipEvent_t)g_events[2 * i], st);
-        if (e != hipSuccess) return e;
-    }
-    const hipError_t e = launch();
-    if (e != hipSuccess) return e;
-    if (on) {
-        const hipError_t e2 = hipEventRecord((hipEvent_t)g_events[2 * i + 1], st);
-        if (e2 != hipSuccess) return e2;
-    }
-    if (g_events) ++g_launch;
-    return hipSuccess;
+    hipError_t e = gdn::bracket_begin(kind, st);
+    if (e == hipSuccess) e = launch();
+    return e == hipSuccess ? gdn::bracket_end(st) : e;
 }
 
 gdn_status_t hip_status(hipError_t e, const char *what) {
@@ -161,6 +150,24 @@ gdn_status_t hip_status(hipError_t e, const char *what) {
 }
 
 } // namespace
+
+namespace gdn {
+
+// The event pair of the calling thread's next launch, while bracketing is on.
+static bool bracket_on() { return g_events && 2 * g_launch + 1 < g_nevents; }
+
+hipError_t bracket_begin(int kind, hipStream_t st) {
+    if (g_events && g_launch < KIND_LOG) g_kinds[g_launch] = (int8_t)kind;
+    return bracket_on() ? hipEventRecord((hipEvent_t)g_events[2 * g_launch], st) : hipSuccess;
+}
+
+hipError_t bracket_end(hipStream_t st) {
+    const hipError_t e = bracket_on() ? hipEventRecord((hipEvent_t)g_events[2 * g_launch + 1], st) : hipSuccess;
+    if (g_events && e == hipSuccess) ++g_launch;
+    return e;
+}
+
+} // namespace gdn
 
 extern "C" {
 

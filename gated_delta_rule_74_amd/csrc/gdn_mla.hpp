@@ -1,0 +1,274 @@
+// Latent attention and the paged latent cache: argument blocks, launch
+// interface and device building blocks shared by their kernels (gfx950).
+#pragma once
+
+#include "gdn_common.hpp"
+#include "gdn_launch.hpp"
+
+namespace gdn {
+
+// bracketed(): runs `launch`, between two of the caller's timing events while
+// gdn_time_launches has them on (kinds as listed at gdn_launch_kind).
+enum MlaKind {
+    K_MLA_FWD = 8,
+    K_MLA_BWD_Q,
+    K_MLA_BWD_K,
+    K_MLA_ROPE_SUM,
+    K_MLA_STEP,
+    K_MLA_JOIN,
+    K_NORM_ROPE,
+    K_NORM_ROPE_BWD,
+    K_NORM_SUM,
+    K_MLA_WRITE,
+    K_PAGE_PLAN,
+    K_PAGE_FILL
+};
+hipError_t bracket_begin(int kind, hipStream_t st);
+hipError_t bracket_end(hipStream_t st);
+template <class F> hipError_t bracketed(int kind, F &&launch, hipStream_t st) {
+    hipError_t e = bracket_begin(kind, st);
+    if (e == hipSuccess) e = launch();
+    return e == hipSuccess ? bracket_end(st) : e;
+}
+
+// Expanded heads: q [B,Tq,H,dn+dr], k [B,Tk,Hk,dn], kr [B,Tk,Hr,dr], v [B,Tk,Hk,dv].
+struct MlaArgs {
+    const void *q, *k, *kr, *v;
+    const int *lens; // [B] keys of each sequence, or null (Tk)
+    int B, Tq, Tk, H, Hk, Hr, dn, dr, dv;
+    float scale;
+};
+struct MlaFwdArgs {
+    MlaArgs s;
+    void *o;
+    float *lse; // [B,Tq,H], may be null
+};
+struct MlaBwdArgs {
+    MlaArgs s;
+    const void *o, *dout;
+    const float *lse;
+    float *delta; // workspace [B,H,Tq]: sum of do * o
+    void *dq, *dk, *dv, *dkr;
+    float *dkr_part; // workspace [B,Tk,Hk,dr] when Hr < Hk, else null
+};
+
+// Absorbed heads over the paged cache: q [N,S,H,dl+dr], cache [pages,page,dl+dr].
+struct MlaStepArgs {
+    const void *q, *cache;
+    const int *table, *lens;
+    void *o;
+    float *lse; // may be null
+    int N, S, H, dl, dr, pages, page, cols;
+    float scale;
+    int mt, nsplit; // blocks of 16 rows per workgroup; parts a sequence may be split into
+    float *part;    // workspace [N][S * H][nsplit][dl] when nsplit > 1
+    float *part_ml; // workspace [N][S * H][nsplit][2]
+};
+
+struct NormRopeArgs {
+    const void *x, *dy;
+    const float *w;
+    const int *pos;
+    const double *freqs;
+    void *y; // y (forward) or dx (backward)
+    float *dw, *dw_part;
+    long long M; // tokens
+    int H, d, r, norm, inter;
+    float eps;
+    int nblk; // workgroups of the backward (rows of dw_part)
+};
+
+struct MlaWriteArgs {
+    const void *c, *kr;
+    const float *w;
+    const int *pos, *slots;
+    const double *freqs;
+    void *cache;
+    long long n_slots;
+    int n, dl, dr, norm, inter;
+    float eps;
+};
+
+struct PagePlanArgs {
+    const int *lens, *fresh;
+    int *table, *stack;
+    const int *n_free;
+    int *lens_out, *n_free_out, *granted, *starts, *slots, *positions;
+    int N, cols, F, page, cap;
+};
+
+int mla_dq_pad(int d);  // padded query/key width the kernels are built for
+int mla_dv_pad(int d);  // padded value width
+void mla_step_plan(MlaStepArgs &a, bool bf16, int cus); // sets mt and nsplit from the sizes
+
+// workgroups of the backward of norm_rope: one row of dw partial sums each
+constexpr int MLA_SPLIT_MAX = 512; // parts of one sequence, at most
+
+int norm_rope_blocks(long long rows, int d);
+
+hipError_t launch_mla_fwd_bf16(const MlaFwdArgs &a, hipStream_t st);
+hipError_t launch_mla_fwd_f32(const MlaFwdArgs &a, hipStream_t st);
+hipError_t launch_mla_bwd_q_bf16(const MlaBwdArgs &a, hipStream_t st);
+hipError_t launch_mla_bwd_q_f32(const MlaBwdArgs &a, hipStream_t st);
+hipError_t launch_mla_bwd_k_bf16(const MlaBwdArgs &a, hipStream_t st);
+hipError_t launch_mla_bwd_k_f32(const MlaBwdArgs &a, hipStream_t st);
+hipError_t launch_mla_rope_sum(const MlaBwdArgs &a, bool bf16, hipStream_t st);
+hipError_t launch_mla_step(const MlaStepArgs &a, bool bf16, hipStream_t st);
+hipError_t launch_mla_join(const MlaStepArgs &a, bool bf16, hipStream_t st);
+hipError_t launch_norm_rope(const NormRopeArgs &a, bool bf16, hipStream_t st);
+hipError_t launch_norm_rope_bwd(const NormRopeArgs &a, bool bf16, hipStream_t st);
+hipError_t launch_norm_sum(const NormRopeArgs &a, hipStream_t st);
+hipError_t launch_mla_write(const MlaWriteArgs &a, bool bf16, hipStream_t st);
+hipError_t launch_page_plan(const PagePlanArgs &a, hipStream_t st);
+hipError_t launch_page_fill(const PagePlanArgs &a, hipStream_t st);
+bool page_fill_separate(int cap); // the slots are filled by a launch of their own
+
+// ---------------------------------------------------------------- device code
+
+// Eight consecutive K values of one row (or column) of a 16-wide MFMA
+// operand: lane 16g + r holds row r, K = 8g .. 8g + 7. One bf16 MFMA takes
+// all 32 K values at once; in fp32 eight 16x16x4 MFMAs take value j of every
+// lane in turn (K = {j, 8 + j, 16 + j, 24 + j}), which sums the same products
+// as long as both operands are held this way.
+template <bool BF> struct Frag;
+template <> struct Frag<true> {
+    bf16x8 v;
+};
+template <> struct Frag<false> {
+    f32x4 lo, hi;
+};
+__device__ __forceinline__ f32x4 mma8(const Frag<true> &a, const Frag<true> &b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.v, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mma8(const Frag<false> &a, const Frag<false> &b, f32x4 c) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.lo[j], b.lo[j], c, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.hi[j], b.hi[j], c, 0, 0, 0);
+    return c;
+}
+// eight values stored one after the other (LDS or global, 16-byte aligned)
+__device__ __forceinline__ Frag<true> row8(const u16 *p) { return {*reinterpret_cast<const bf16x8 *>(p)}; }
+__device__ __forceinline__ Frag<false> row8(const float *p) {
+    return {*reinterpret_cast<const f32x4 *>(p), *reinterpret_cast<const f32x4 *>(p + 4)};
+}
+template <bool BF> __device__ __forceinline__ Frag<BF> zero8();
+template <> __device__ __forceinline__ Frag<true> zero8<true>() {
+    return {__builtin_bit_cast(bf16x8, uint4{0u, 0u, 0u, 0u})};
+}
+template <> __device__ __forceinline__ Frag<false> zero8<false>() { return {zero4(), zero4()}; }
+
+// sum of the eight products, in fp32
+__device__ __forceinline__ float dot8(const Frag<true> &a, const Frag<true> &b) {
+    float x = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x = fmaf((float)a.v[e], (float)b.v[e], x);
+    return x;
+}
+__device__ __forceinline__ float dot8(const Frag<false> &a, const Frag<false> &b) {
+    float x = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x = fmaf(a.lo[e], b.lo[e], x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x = fmaf(a.hi[e], b.hi[e], x);
+    return x;
+}
+
+// Operand column m0 + lane % 16 of an LDS matrix X[k][m] over the 32 rows from
+// k0, in the K order of two accumulator tiles (acc8): lane group g takes rows
+// k0 + 4g + e, then k0 + 16 + 4g + e.
+__device__ __forceinline__ Frag<true> col8(const u16 *X, int ld, int k0, int m0, int lane) {
+    return {join8(operand_tr4(X, ld, k0, m0, lane), operand_tr4(X, ld, k0 + 16, m0, lane))};
+}
+__device__ __forceinline__ Frag<false> col8(const float *X, int ld, int k0, int m0, int lane) {
+    const float *p = X + (k0 + 4 * (lane >> 4)) * ld + m0 + (lane & 15);
+    Frag<false> f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        f.lo[e] = p[e * ld];
+        f.hi[e] = p[(16 + e) * ld];
+    }
+    return f;
+}
+// Two 16x16 accumulator tiles (rows k0 .. and k0 + 16 .. of one column block)
+// as the other operand of such a product. In bf16 the values are rounded to
+// nearest even here: it is what lets the product run on bf16 MFMAs.
+template <bool BF> __device__ __forceinline__ Frag<BF> acc8(f32x4 t0, f32x4 t1);
+template <> __device__ __forceinline__ Frag<true> acc8<true>(f32x4 t0, f32x4 t1) {
+    return {join8(pack4(t0), pack4(t1))};
+}
+template <> __device__ __forceinline__ Frag<false> acc8<false>(f32x4 t0, f32x4 t1) { return {t0, t1}; }
+
+// x of the three lanes 16, 32 and 48 away folded in: every lane of a column
+// (lane % 16) gets the maximum (sum) over its four lane groups.
+__device__ __forceinline__ float max4g(float x) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float sum4g(float x) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// Four consecutive output values.
+__device__ __forceinline__ void store4(u16 *p, f32x4 x) {
+    uint2 w;
+    w.x = f2bf2(x[0], x[1]);
+    w.y = f2bf2(x[2], x[3]);
+    *reinterpret_cast<uint2 *>(p) = w;
+}
+__device__ __forceinline__ void store4(float *p, f32x4 x) { *reinterpret_cast<f32x4 *>(p) = x; }
+
+// Workgroup barrier that waits for this wave's LDS accesses only: global
+// loads already in flight into registers stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Rows of a sequence, NR at a time, from global memory over registers into an
+// LDS tile [NR][ld]: columns 0 .. d0 - 1 from x0, d0 .. d0 + d1 - 1 from x1
+// (both multiples of 8), zeros up to DP and for rows past `n`. fetch() only
+// issues the loads (from clamped addresses inside the tensors), stash()
+// masks and writes, so the loads stay in flight in between.
+template <bool BF, int DP, int NR, int NT> struct RowTile {
+    using S = typename Op<BF>::S;
+    static constexpr int V = Op<BF>::VEC;
+    static constexpr int NG = DP / V;
+    static constexpr int NIT = (NR * NG + NT - 1) / NT;
+    static constexpr bool FULL = (NR * NG) % NT == 0;
+    uint4 r[NIT];
+    __device__ __forceinline__ void fetch(const S *__restrict__ x0, size_t rs0, int d0, const S *__restrict__ x1,
+                                          size_t rs1, int d1, int row0, int n, int tid) {
+#pragma unroll
+        for (int m = 0; m < NIT; ++m) {
+            const int it = tid + m * NT;
+            const int j = min(row0 + it / NG, n - 1), c = (it % NG) * V;
+            const S *p = c < d0 ? x0 + (size_t)j * rs0 + c : x0;
+            if (d1 > 0 && c >= d0) p = x1 + (size_t)j * rs1 + min(c - d0, d1 - V);
+            r[m] = *reinterpret_cast<const uint4 *>(p);
+        }
+    }
+    __device__ __forceinline__ void stash(S *dst, int ld, int d, int row0, int n, int tid) const {
+#pragma unroll
+        for (int m = 0; m < NIT; ++m) {
+            const int it = tid + m * NT;
+            const int j = it / NG, c = (it % NG) * V;
+            if (!FULL && j >= NR) continue;
+            const bool in = row0 + j < n && c < d;
+            *reinterpret_cast<uint4 *>(dst + j * ld + c) = in ? r[m] : uint4{0u, 0u, 0u, 0u};
+        }
+    }
+};
+
+// Workgroup -> logical index so that each XCD (workgroups go round robin over
+// the 8) works on a contiguous range of them, for any number of workgroups.
+__device__ __forceinline__ int xcd_range(int bid, int n) {
+    const int q = n / 8, rem = n % 8, x = bid % 8, i = bid / 8;
+    return x * q + min(x, rem) + i;
+}
+
+} // namespace gdn

@@ -1,0 +1,366 @@
+// Causal attention of expanded latent-attention heads, backward.
+//
+//   P_ij = exp(z_ij - lse_i),  delta_i = do_i . o_i,  dS_ij = P_ij (do_i . v_j - delta_i)
+//   dq_i = scale sum_j dS_ij [k_j | kr_j],   [dk_j | dkr_j] = scale sum_i dS_ij q_i,   dv_j = sum_i P_ij do_i
+//
+// The probabilities are formed again from the saved lse. Two kernels, so that
+// every sum has one owner and a fixed order (no atomics):
+//  * mla_bwd_q: a wave holds QT * 16 queries (q, do, and dq in accumulators)
+//    and walks the keys; it also forms delta, which it leaves for the other;
+//  * mla_bwd_k: a wave holds KT * 16 keys (k, v, and dk, dv in accumulators)
+//    and walks the queries of every head that shares them, so a shared head's
+//    gradient is summed in registers. Only the rotary key is shared by more
+//    heads than that: each key head leaves its part in fp32 and mla_rope_sum
+//    adds them up.
+// In both, S and dP are formed with the walked rows as accumulator rows, so P
+// and dS are at once the operand of the next product (as in the forward), and
+// the walked tiles are read row by row for the first two products and by
+// transposing reads for the last. The sums P and dS enter in bf16 (rounded to
+// nearest even) when the tensors are bf16; everything else is fp32.
+#pragma once
+
+#include "gdn_mla.hpp"
+
+namespace gdn {
+
+constexpr int MLA_BT = 64; // walked rows per tile
+
+template <bool BF, int DP, int DVP, int NW, int QT>
+__global__ __launch_bounds__(NW * 64) void mla_bwd_q_kernel(MlaBwdArgs a) {
+    using S = typename Op<BF>::S;
+    constexpr int LDK = DP + Op<BF>::PAD, LDV = DVP + Op<BF>::PAD, NT = NW * 64, KS = DP / 32, VS = DVP / 32,
+                  MD = DP / 16;
+    __shared__ __align__(16) S Ks[MLA_BT * LDK];
+    __shared__ __align__(16) S Vs[MLA_BT * LDV];
+    const MlaArgs &s = a.s;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
+    constexpr int QB = NW * QT * 16;
+    const int nqb = (s.Tq + QB - 1) / QB;
+    const int id = xcd_range(blockIdx.x, gridDim.x);
+    const int bh = id / nqb, qb = nqb - 1 - id % nqb;
+    const int b = bh / s.H, h = bh % s.H, hk = h / (s.H / s.Hk);
+    const int hr = s.Hr > 0 ? h / (s.H / s.Hr) : 0;
+    const int D = s.dn + s.dr, off = s.Tk - s.Tq;
+    const int n = s.lens ? min(max(s.lens[b], 0), s.Tk) : s.Tk;
+    const int q0 = qb * QB + wave * QT * 16;
+    const size_t rq = (size_t)s.H * D, rk = (size_t)s.Hk * s.dn, rr = (size_t)s.Hr * s.dr, rv = (size_t)s.Hk * s.dv,
+                 ro = (size_t)s.H * s.dv;
+    const S *kp = (const S *)s.k + (size_t)b * s.Tk * rk + (size_t)hk * s.dn;
+    const S *krp = s.dr > 0 ? (const S *)s.kr + (size_t)b * s.Tk * rr + (size_t)hr * s.dr : kp;
+    const S *vp = (const S *)s.v + (size_t)b * s.Tk * rv + (size_t)hk * s.dv;
+    const int last = min(min(qb * QB + QB, s.Tq) - 1 + off, n - 1);
+    const int nt = qb * QB + off < n ? last / MLA_BT + 1 : 0;
+
+    RowTile<BF, DP, MLA_BT, NT> kt;
+    RowTile<BF, DVP, MLA_BT, NT> vt;
+    if (nt > 0) {
+        kt.fetch(kp, rk, s.dn, krp, rr, s.dr, 0, n, tid);
+        vt.fetch(vp, rv, s.dv, vp, 0, 0, 0, n, tid);
+    }
+    Frag<BF> Q[QT][KS], G[QT][VS]; // q and do as operand columns
+    float lse2[QT], delta[QT];
+    const S *qp = (const S *)s.q + (size_t)b * s.Tq * rq + (size_t)h * D;
+    const S *gp = (const S *)a.dout + (size_t)b * s.Tq * ro + (size_t)h * s.dv;
+    const S *op = (const S *)a.o + (size_t)b * s.Tq * ro + (size_t)h * s.dv;
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        const int i = q0 + 16 * t + r;
+        const bool live = i < s.Tq && i + off < n;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            const int c = 32 * k + 8 * g;
+            Q[t][k] = (live && c < D) ? row8(qp + (size_t)i * rq + c) : zero8<BF>();
+        }
+        float d = 0.f;
+#pragma unroll
+        for (int k = 0; k < VS; ++k) {
+            const int c = 32 * k + 8 * g;
+            G[t][k] = zero8<BF>();
+            if (live && c < s.dv) {
+                G[t][k] = row8(gp + (size_t)i * ro + c);
+                const Frag<BF> o = row8(op + (size_t)i * ro + c);
+                d += dot8(G[t][k], o);
+            }
+        }
+        delta[t] = sum4g(d);
+        const float ls = live ? a.lse[((size_t)b * s.Tq + i) * s.H + h] : -INFINITY;
+        // a row without keys: every probability is exp2(z - inf) = 0
+        lse2[t] = ls == -INFINITY ? INFINITY : ls * (float)LOG2E;
+        if (g == 0 && i < s.Tq) a.delta[((size_t)b * s.H + h) * s.Tq + i] = delta[t];
+    }
+    f32x4 dQ[QT][MD];
+#pragma unroll
+    for (int t = 0; t < QT; ++t)
+#pragma unroll
+        for (int v = 0; v < MD; ++v) dQ[t][v] = zero4();
+    const float c2 = s.scale * (float)LOG2E;
+    const int wlast = min(q0 + QT * 16 - 1 + off, n - 1), wfirst = q0 + off;
+    for (int kb = 0; kb < nt; ++kb) {
+        const int key0 = kb * MLA_BT;
+        lds_barrier(); // the previous tile's readers are done
+        kt.stash(Ks, LDK, D, key0, n, tid);
+        vt.stash(Vs, LDV, s.dv, key0, n, tid);
+        if (kb + 1 < nt) {
+            kt.fetch(kp, rk, s.dn, krp, rr, s.dr, key0 + MLA_BT, n, tid);
+            vt.fetch(vp, rv, s.dv, vp, 0, 0, key0 + MLA_BT, n, tid);
+        }
+        lds_barrier();
+        if (key0 > wlast || wfirst >= n) continue;
+        const bool mask = key0 + MLA_BT - 1 > wfirst || key0 + MLA_BT > n;
+#pragma unroll
+        for (int u = 0; u < MLA_BT / 32; ++u) {
+            f32x4 P[QT][2], dP[QT][2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int t = 0; t < QT; ++t) P[t][j] = dP[t][j] = zero4();
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    const Frag<BF> kf = row8(Ks + (32 * u + 16 * j + r) * LDK + 32 * k + 8 * g);
+#pragma unroll
+                    for (int t = 0; t < QT; ++t) P[t][j] = mma8(kf, Q[t][k], P[t][j]);
+                }
+#pragma unroll
+                for (int k = 0; k < VS; ++k) {
+                    const Frag<BF> vf = row8(Vs + (32 * u + 16 * j + r) * LDV + 32 * k + 8 * g);
+#pragma unroll
+                    for (int t = 0; t < QT; ++t) dP[t][j] = mma8(vf, G[t][k], dP[t][j]);
+                }
+            }
+            Frag<BF> ds[QT];
+#pragma unroll
+            for (int t = 0; t < QT; ++t) {
+                const int lim = min(q0 + 16 * t + r + off, n - 1) - key0 - 32 * u - 4 * g;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float x = exp2_fast(fmaf(P[t][j][e], c2, -lse2[t])) * (dP[t][j][e] - delta[t]);
+                        P[t][j][e] = (!mask || 16 * j + e <= lim) ? x : 0.f;
+                    }
+                ds[t] = acc8<BF>(P[t][0], P[t][1]);
+            }
+#pragma unroll
+            for (int v = 0; v < MD; ++v) {
+                const Frag<BF> kf = col8(Ks, LDK, 32 * u, 16 * v, lane);
+#pragma unroll
+                for (int t = 0; t < QT; ++t) dQ[t][v] = mma8(kf, ds[t], dQ[t][v]);
+            }
+        }
+    }
+    S *dqp = (S *)a.dq + (size_t)b * s.Tq * rq + (size_t)h * D;
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        const int i = q0 + 16 * t + r;
+        if (i >= s.Tq) continue;
+#pragma unroll
+        for (int v = 0; v < MD; ++v) {
+            const int c = 16 * v + 4 * g;
+            if (c < D) store4(dqp + (size_t)i * rq + c, dQ[t][v] * s.scale);
+        }
+    }
+}
+
+template <bool BF, int DP, int DVP, int NW, int KT>
+__global__ __launch_bounds__(NW * 64) void mla_bwd_k_kernel(MlaBwdArgs a) {
+    using S = typename Op<BF>::S;
+    constexpr int LDQ = DP + Op<BF>::PAD, LDG = DVP + Op<BF>::PAD, NT = NW * 64, KS = DP / 32, VS = DVP / 32,
+                  MD = DP / 16, MV = DVP / 16;
+    __shared__ __align__(16) S Qs[MLA_BT * LDQ];
+    __shared__ __align__(16) S Gs[MLA_BT * LDG];
+    __shared__ __align__(16) float Ls[MLA_BT], Ds[MLA_BT];
+    const MlaArgs &s = a.s;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
+    constexpr int KB = NW * KT * 16;
+    const int nkb = (s.Tk + KB - 1) / KB;
+    // the longest walks (first keys) first
+    const int id = xcd_range(blockIdx.x, gridDim.x);
+    const int bh = id / nkb, kb = id % nkb;
+    const int b = bh / s.Hk, hk = bh % s.Hk, per = s.H / s.Hk;
+    const int hr = s.Hr > 0 ? hk / (s.Hk / s.Hr) : 0;
+    const int D = s.dn + s.dr, off = s.Tk - s.Tq;
+    const int n = s.lens ? min(max(s.lens[b], 0), s.Tk) : s.Tk;
+    const int key0 = kb * KB, w0 = key0 + wave * KT * 16; // first key of the workgroup, of the wave
+    const size_t rq = (size_t)s.H * D, rk = (size_t)s.Hk * s.dn, rr = (size_t)s.Hr * s.dr, rv = (size_t)s.Hk * s.dv,
+                 ro = (size_t)s.H * s.dv;
+    // queries that see a key of this workgroup: q_lo .. nq - 1, a tile-aligned walk of each head
+    const int nq = min(s.Tq, n - off);
+    const int t_lo = max(key0 - off, 0) / MLA_BT;
+    const int tiles = key0 < n && nq > t_lo * MLA_BT ? (nq + MLA_BT - 1) / MLA_BT - t_lo : 0;
+    const int total = tiles * per;
+
+    RowTile<BF, DP, MLA_BT, NT> qt;
+    RowTile<BF, DVP, MLA_BT, NT> gt;
+    float lreg = 0.f, dreg = 0.f;
+    auto fetch = [&](int x) {
+        const int h = hk * per + x / tiles, row0 = (t_lo + x % tiles) * MLA_BT;
+        const S *qp = (const S *)s.q + (size_t)b * s.Tq * rq + (size_t)h * D;
+        const S *gp = (const S *)a.dout + (size_t)b * s.Tq * ro + (size_t)h * s.dv;
+        qt.fetch(qp, rq, D, qp, 0, 0, row0, nq, tid);
+        gt.fetch(gp, ro, s.dv, gp, 0, 0, row0, nq, tid);
+        if (tid < MLA_BT) {
+            const int i = min(row0 + tid, nq - 1);
+            lreg = a.lse[((size_t)b * s.Tq + i) * s.H + h];
+            dreg = a.delta[((size_t)b * s.H + h) * s.Tq + i];
+        }
+    };
+    if (total > 0) fetch(0);
+    Frag<BF> K[KT][KS], V[KT][VS]; // keys and values as operand columns
+    const S *kp = (const S *)s.k + (size_t)b * s.Tk * rk + (size_t)hk * s.dn;
+    const S *krp = s.dr > 0 ? (const S *)s.kr + (size_t)b * s.Tk * rr + (size_t)hr * s.dr : kp;
+    const S *vp = (const S *)s.v + (size_t)b * s.Tk * rv + (size_t)hk * s.dv;
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+        const int j = w0 + 16 * t + r;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            const int c = 32 * k + 8 * g;
+            K[t][k] = zero8<BF>();
+            if (j < n && c < D) K[t][k] = row8(c < s.dn ? kp + (size_t)j * rk + c : krp + (size_t)j * rr + (c - s.dn));
+        }
+#pragma unroll
+        for (int k = 0; k < VS; ++k) {
+            const int c = 32 * k + 8 * g;
+            V[t][k] = (j < n && c < s.dv) ? row8(vp + (size_t)j * rv + c) : zero8<BF>();
+        }
+    }
+    f32x4 dK[KT][MD], dV[KT][MV];
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+#pragma unroll
+        for (int v = 0; v < MD; ++v) dK[t][v] = zero4();
+#pragma unroll
+        for (int v = 0; v < MV; ++v) dV[t][v] = zero4();
+    }
+    const float c2 = s.scale * (float)LOG2E;
+    for (int x = 0; x < total; ++x) {
+        const int row0 = (t_lo + x % tiles) * MLA_BT;
+        lds_barrier();
+        qt.stash(Qs, LDQ, D, row0, nq, tid);
+        gt.stash(Gs, LDG, s.dv, row0, nq, tid);
+        if (tid < MLA_BT) {
+            Ls[tid] = lreg == -INFINITY ? INFINITY : lreg * (float)LOG2E;
+            Ds[tid] = dreg;
+        }
+        if (x + 1 < total) fetch(x + 1);
+        lds_barrier();
+        // no query of the tile sees a key of this wave
+        if (row0 + MLA_BT - 1 + off < w0 || w0 >= n) continue;
+        const bool mask = row0 + off < w0 + KT * 16 - 1 || row0 + MLA_BT > nq || w0 + KT * 16 > n;
+#pragma unroll
+        for (int u = 0; u < MLA_BT / 32; ++u) {
+            f32x4 P[KT][2], dP[KT][2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int t = 0; t < KT; ++t) P[t][j] = dP[t][j] = zero4();
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    const Frag<BF> qf = row8(Qs + (32 * u + 16 * j + r) * LDQ + 32 * k + 8 * g);
+#pragma unroll
+                    for (int t = 0; t < KT; ++t) P[t][j] = mma8(qf, K[t][k], P[t][j]);
+                }
+#pragma unroll
+                for (int k = 0; k < VS; ++k) {
+                    const Frag<BF> gf = row8(Gs + (32 * u + 16 * j + r) * LDG + 32 * k + 8 * g);
+#pragma unroll
+                    for (int t = 0; t < KT; ++t) dP[t][j] = mma8(gf, V[t][k], dP[t][j]);
+                }
+            }
+            Frag<BF> pf[KT], sf[KT];
+#pragma unroll
+            for (int t = 0; t < KT; ++t) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int i0 = 32 * u + 16 * j + 4 * g; // first of this lane's four rows
+                    const f32x4 ls = *reinterpret_cast<const f32x4 *>(Ls + i0);
+                    const f32x4 dl = *reinterpret_cast<const f32x4 *>(Ds + i0);
+                    // row e sees this lane's key from row w0 + 16 t + r - off on; no key at or past n
+                    const int j_at = w0 + 16 * t + r, lo = j_at - off - row0 - i0, hi = nq - row0 - i0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float p = exp2_fast(fmaf(P[t][j][e], c2, -ls[e]));
+                        float d = p * (dP[t][j][e] - dl[e]);
+                        const bool in = !mask || (e >= lo && e < hi && j_at < n);
+                        P[t][j][e] = in ? p : 0.f;
+                        dP[t][j][e] = in ? d : 0.f;
+                    }
+                }
+                pf[t] = acc8<BF>(P[t][0], P[t][1]);
+                sf[t] = acc8<BF>(dP[t][0], dP[t][1]);
+            }
+#pragma unroll
+            for (int v = 0; v < MV; ++v) {
+                const Frag<BF> gf = col8(Gs, LDG, 32 * u, 16 * v, lane);
+#pragma unroll
+                for (int t = 0; t < KT; ++t) dV[t][v] = mma8(gf, pf[t], dV[t][v]);
+            }
+#pragma unroll
+            for (int v = 0; v < MD; ++v) {
+                const Frag<BF> qf = col8(Qs, LDQ, 32 * u, 16 * v, lane);
+#pragma unroll
+                for (int t = 0; t < KT; ++t) dK[t][v] = mma8(qf, sf[t], dK[t][v]);
+            }
+        }
+    }
+    S *dkp = (S *)a.dk + (size_t)b * s.Tk * rk + (size_t)hk * s.dn;
+    S *dvp = (S *)a.dv + (size_t)b * s.Tk * rv + (size_t)hk * s.dv;
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+        const int j = w0 + 16 * t + r;
+        if (j >= s.Tk) continue;
+#pragma unroll
+        for (int v = 0; v < MV; ++v) {
+            const int c = 16 * v + 4 * g;
+            if (c < s.dv) store4(dvp + (size_t)j * rv + c, dV[t][v]);
+        }
+#pragma unroll
+        for (int v = 0; v < MD; ++v) {
+            const int c = 16 * v + 4 * g;
+            const f32x4 x = dK[t][v] * s.scale;
+            if (c < s.dn) {
+                store4(dkp + (size_t)j * rk + c, x);
+            } else if (c < D) {
+                if (a.dkr_part)
+                    store4(a.dkr_part + (((size_t)b * s.Tk + j) * s.Hk + hk) * s.dr + (c - s.dn), x);
+                else
+                    store4((S *)a.dkr + ((size_t)b * s.Tk + j) * rr + (size_t)hr * s.dr + (c - s.dn), x);
+            }
+        }
+    }
+}
+
+template <bool BF, int DP, int DVP> hipError_t mla_bwd_q_run(const MlaBwdArgs &a, hipStream_t st) {
+    constexpr int NW = 4, QT = BF && DP <= 128 ? 2 : 1;
+    const long long nqb = (a.s.Tq + NW * QT * 16 - 1) / (NW * QT * 16);
+    hipLaunchKernelGGL((mla_bwd_q_kernel<BF, DP, DVP, NW, QT>), dim3((unsigned)(nqb * a.s.B * a.s.H)), dim3(NW * 64),
+                       0, st, a);
+    return hipGetLastError();
+}
+template <bool BF, int DP, int DVP> hipError_t mla_bwd_k_run(const MlaBwdArgs &a, hipStream_t st) {
+    constexpr int NW = 4, KT = BF ? 2 : 1;
+    const long long nkb = (a.s.Tk + NW * KT * 16 - 1) / (NW * KT * 16);
+    hipLaunchKernelGGL((mla_bwd_k_kernel<BF, DP, DVP, NW, KT>), dim3((unsigned)(nkb * a.s.B * a.s.Hk)), dim3(NW * 64),
+                       0, st, a);
+    return hipGetLastError();
+}
+
+template <bool BF, bool Q, int DP, int DVP> hipError_t mla_bwd_run(const MlaBwdArgs &a, hipStream_t st) {
+    if constexpr (Q) return mla_bwd_q_run<BF, DP, DVP>(a, st);
+    else return mla_bwd_k_run<BF, DP, DVP>(a, st);
+}
+template <bool BF, bool Q> hipError_t mla_bwd_launch(const MlaBwdArgs &a, hipStream_t st) {
+    const int D = mla_dq_pad(a.s.dn + a.s.dr);
+    if (mla_dv_pad(a.s.dv) == 64) {
+        if (D == 64) return mla_bwd_run<BF, Q, 64, 64>(a, st);
+        if (D == 96) return mla_bwd_run<BF, Q, 96, 64>(a, st);
+        if (D == 128) return mla_bwd_run<BF, Q, 128, 64>(a, st);
+        return mla_bwd_run<BF, Q, 192, 64>(a, st);
+    }
+    if (D == 64) return mla_bwd_run<BF, Q, 64, 128>(a, st);
+    if (D == 96) return mla_bwd_run<BF, Q, 96, 128>(a, st);
+    if (D == 128) return mla_bwd_run<BF, Q, 128, 128>(a, st);
+    return mla_bwd_run<BF, Q, 192, 128>(a, st);
+}
+
+} // namespace gdn

@@ -1,0 +1,6 @@
+// The bf16 instances of the attention backward: key and value gradients.
+#include "gdn_mla_bwd.hpp"
+
+namespace gdn {
+hipError_t launch_mla_bwd_k_bf16(const MlaBwdArgs &a, hipStream_t st) { return mla_bwd_launch<true, false>(a, st); }
+} // namespace gdn

@@ -1,0 +1,223 @@
+// Causal attention of expanded latent-attention heads, forward.
+//
+//   z_ij = scale (q_i[:dn] . k_j + q_i[dn:] . kr_j),  o_i = sum_j softmax(z_i)_j v_j,
+//   lse_i = log sum_j exp z_ij   over the keys j <= i + Tk - Tq, j < len_b
+//
+// in one pass over the keys with the running maximum and sum of the softmax.
+// A workgroup takes NW * QT * 16 queries of one head and walks the keys in
+// tiles of 64 that all its waves share in LDS; a wave holds its QT * 16
+// queries in registers for the whole walk. The products are formed
+// transposed, S^T = K Q^T and O^T = V^T P^T: then a lane owns one query
+// (column), the maximum and the rescaling are per-lane scalars, and the
+// probabilities leave the first product in exactly the lanes and K order that
+// the second one wants its operand in, so they never pass through LDS; V is
+// read from its row-major tile by transposing LDS reads.
+// The running maximum is only moved when a score exceeds it by more than
+// RAISE (in powers of two): until then the probabilities are merely up to
+// 2^RAISE too large, in P, in the sum and in O alike, which fp32 holds without
+// loss; this keeps the cross-lane maximum and the rescaling of O out of almost
+// every tile.
+#pragma once
+
+#include "gdn_mla.hpp"
+
+namespace gdn {
+
+constexpr int MLA_KT = 64;      // keys per tile
+constexpr float MLA_RAISE = 8.f; // see above
+
+template <bool BF, int DP, int DVP, int NW, int QT>
+__global__ __launch_bounds__(NW * 64) void mla_fwd_kernel(MlaFwdArgs a) {
+    using S = typename Op<BF>::S;
+    constexpr int LDK = DP + Op<BF>::PAD, LDV = DVP + Op<BF>::PAD, NT = NW * 64, KS = DP / 32, MV = DVP / 16;
+    // two tiles in bf16; one in fp32, where two of the widest pass 160 KB
+    constexpr int NB = BF ? 2 : 1;
+    __shared__ __align__(16) S Ks[NB][MLA_KT * LDK];
+    __shared__ __align__(16) S Vs[NB][MLA_KT * LDV];
+    const MlaArgs &s = a.s;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
+    constexpr int QB = NW * QT * 16;
+    const int nqb = (s.Tq + QB - 1) / QB;
+    // the longest walks (last queries) of a head first, heads of one XCD together
+    const int id = xcd_range(blockIdx.x, gridDim.x);
+    const int bh = id / nqb, qb = nqb - 1 - id % nqb;
+    const int b = bh / s.H, h = bh % s.H, hk = h / (s.H / s.Hk);
+    const int hr = s.Hr > 0 ? h / (s.H / s.Hr) : 0;
+    const int D = s.dn + s.dr, off = s.Tk - s.Tq;
+    const int n = s.lens ? min(max(s.lens[b], 0), s.Tk) : s.Tk;
+    const int q0 = qb * QB + wave * QT * 16; // first query of this wave
+    const size_t rq = (size_t)s.H * D, rk = (size_t)s.Hk * s.dn, rr = (size_t)s.Hr * s.dr, rv = (size_t)s.Hk * s.dv;
+    const S *kp = (const S *)s.k + (size_t)b * s.Tk * rk + (size_t)hk * s.dn;
+    const S *krp = s.dr > 0 ? (const S *)s.kr + (size_t)b * s.Tk * rr + (size_t)hr * s.dr : kp;
+    const S *vp = (const S *)s.v + (size_t)b * s.Tk * rv + (size_t)hk * s.dv;
+
+    // keys the workgroup has to see: those of its last query that is not padding
+    const int last = min(min(qb * QB + QB, s.Tq) - 1 + off, n - 1);
+    const int first = qb * QB + off; // position of its first query
+    const int nt = first < n ? last / MLA_KT + 1 : 0;
+
+    RowTile<BF, DP, MLA_KT, NT> kt;
+    RowTile<BF, DVP, MLA_KT, NT> vt;
+    if (nt > 0) {
+        kt.fetch(kp, rk, s.dn, krp, rr, s.dr, 0, n, tid);
+        vt.fetch(vp, rv, s.dv, vp, 0, 0, 0, n, tid);
+    }
+    // queries as operand columns; rows past the sequence read as zero
+    Frag<BF> Q[QT][KS];
+    const S *qp = (const S *)s.q + (size_t)b * s.Tq * rq + (size_t)h * D;
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        const int i = q0 + 16 * t + r;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            const int c = 32 * k + 8 * g;
+            Q[t][k] = (i < s.Tq && c < D) ? row8(qp + (size_t)i * rq + c) : zero8<BF>();
+        }
+    }
+    f32x4 O[QT][MV];
+    float m[QT], l[QT];
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        m[t] = -INFINITY;
+        l[t] = 0.f;
+#pragma unroll
+        for (int v = 0; v < MV; ++v) O[t][v] = zero4();
+    }
+    const float c2 = s.scale * (float)LOG2E;
+    if (nt > 0) {
+        kt.stash(Ks[0], LDK, D, 0, n, tid);
+        vt.stash(Vs[0], LDV, s.dv, 0, n, tid);
+        lds_barrier();
+    }
+    const int wlast = min(q0 + QT * 16 - 1 + off, n - 1), wfirst = q0 + off;
+    for (int kb = 0; kb < nt; ++kb) {
+        const int key0 = kb * MLA_KT;
+        if (kb + 1 < nt) {
+            kt.fetch(kp, rk, s.dn, krp, rr, s.dr, key0 + MLA_KT, n, tid);
+            vt.fetch(vp, rv, s.dv, vp, 0, 0, key0 + MLA_KT, n, tid);
+        }
+        if (key0 <= wlast && wfirst < n) {
+            const S *K = Ks[kb % NB], *V = Vs[kb % NB];
+            f32x4 P[QT][4];
+#pragma unroll
+            for (int t = 0; t < QT; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) P[t][j] = zero4();
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const Frag<BF> kf = row8(K + (16 * j + r) * LDK + 32 * k + 8 * g);
+#pragma unroll
+                    for (int t = 0; t < QT; ++t) P[t][j] = mma8(kf, Q[t][k], P[t][j]);
+                }
+            // the mask, where this tile reaches past a query or the sequence
+            if (key0 + MLA_KT - 1 > wfirst || key0 + MLA_KT > n) {
+#pragma unroll
+                for (int t = 0; t < QT; ++t) {
+                    const int lim = min(q0 + 16 * t + r + off, n - 1) - key0 - 4 * g; // last key seen
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) P[t][j][e] = 16 * j + e <= lim ? P[t][j][e] : -INFINITY;
+                }
+            }
+            float mx[QT];
+            bool raise = false;
+#pragma unroll
+            for (int t = 0; t < QT; ++t) {
+                float x = P[t][0][0];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x = fmaxf(x, P[t][j][e]);
+                mx[t] = x * c2;
+                raise |= mx[t] > m[t] + MLA_RAISE;
+            }
+            if (__any(raise)) {
+#pragma unroll
+                for (int t = 0; t < QT; ++t) {
+                    const float mn = fmaxf(m[t], max4g(mx[t]));
+                    const float f = mn == -INFINITY ? 1.f : exp2_fast(m[t] - mn);
+                    m[t] = mn;
+                    l[t] *= f;
+#pragma unroll
+                    for (int v = 0; v < MV; ++v) O[t][v] *= f;
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < QT; ++t) {
+                const float mt = m[t] == -INFINITY ? 0.f : m[t];
+                f32x4 sum = zero4();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) P[t][j][e] = exp2_fast(fmaf(P[t][j][e], c2, -mt));
+                    sum += P[t][j];
+                }
+                l[t] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                Frag<BF> pf[QT];
+#pragma unroll
+                for (int t = 0; t < QT; ++t) pf[t] = acc8<BF>(P[t][2 * k], P[t][2 * k + 1]);
+#pragma unroll
+                for (int v = 0; v < MV; ++v) {
+                    const Frag<BF> vf = col8(V, LDV, 32 * k, 16 * v, lane);
+#pragma unroll
+                    for (int t = 0; t < QT; ++t) O[t][v] = mma8(vf, pf[t], O[t][v]);
+                }
+            }
+        }
+        if (kb + 1 < nt) {
+            // with two buffers the other one's last readers passed the previous barrier
+            if (NB == 1) lds_barrier();
+            kt.stash(Ks[(kb + 1) % NB], LDK, D, key0 + MLA_KT, n, tid);
+            vt.stash(Vs[(kb + 1) % NB], LDV, s.dv, key0 + MLA_KT, n, tid);
+            lds_barrier();
+        }
+    }
+    S *op = (S *)a.o + (size_t)b * s.Tq * s.H * s.dv + (size_t)h * s.dv;
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        const int i = q0 + 16 * t + r;
+        const float lt = sum4g(l[t]);
+        const bool some = i + off < n; // (a query at or past the length has no key)
+        const float inv = some && lt != 0.f ? 1.f / lt : 0.f; // (every score -inf: o = 0)
+        if (i >= s.Tq) continue;
+#pragma unroll
+        for (int v = 0; v < MV; ++v) {
+            const int c = 16 * v + 4 * g;
+            const f32x4 x = some ? O[t][v] * inv : zero4();
+            if (c < s.dv) store4(op + (size_t)i * s.H * s.dv + c, x);
+        }
+        if (a.lse && g == 0)
+            a.lse[((size_t)b * s.Tq + i) * s.H + h] =
+                some ? (m[t] + __builtin_amdgcn_logf(lt)) * 0.69314718055994531f : -INFINITY;
+    }
+}
+
+template <bool BF, int DP, int DVP> hipError_t mla_fwd_run(const MlaFwdArgs &a, hipStream_t st) {
+    constexpr int NW = 4, QT = BF ? 2 : 1;
+    const long long nqb = (a.s.Tq + NW * QT * 16 - 1) / (NW * QT * 16);
+    hipLaunchKernelGGL((mla_fwd_kernel<BF, DP, DVP, NW, QT>), dim3((unsigned)(nqb * a.s.B * a.s.H)), dim3(NW * 64), 0,
+                       st, a);
+    return hipGetLastError();
+}
+
+template <bool BF> hipError_t mla_fwd_launch(const MlaFwdArgs &a, hipStream_t st) {
+    const int D = mla_dq_pad(a.s.dn + a.s.dr);
+    if (mla_dv_pad(a.s.dv) == 64) {
+        if (D == 64) return mla_fwd_run<BF, 64, 64>(a, st);
+        if (D == 96) return mla_fwd_run<BF, 96, 64>(a, st);
+        if (D == 128) return mla_fwd_run<BF, 128, 64>(a, st);
+        return mla_fwd_run<BF, 192, 64>(a, st);
+    }
+    if (D == 64) return mla_fwd_run<BF, 64, 128>(a, st);
+    if (D == 96) return mla_fwd_run<BF, 96, 128>(a, st);
+    if (D == 128) return mla_fwd_run<BF, 128, 128>(a, st);
+    return mla_fwd_run<BF, 192, 128>(a, st);
+}
+
+} // namespace gdn

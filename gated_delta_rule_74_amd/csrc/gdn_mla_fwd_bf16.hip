@@ -1,0 +1,9 @@
+// The bf16 instances of the attention forward (a translation unit of their
+// own, so that the instances compile side by side).
+#include "gdn_mla_fwd.hpp"
+
+namespace gdn {
+int mla_dq_pad(int d) { return d <= 64 ? 64 : d <= 96 ? 96 : d <= 128 ? 128 : 192; }
+int mla_dv_pad(int d) { return d <= 64 ? 64 : 128; }
+hipError_t launch_mla_fwd_bf16(const MlaFwdArgs &a, hipStream_t st) { return mla_fwd_launch<true>(a, st); }
+} // namespace gdn

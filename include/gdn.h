@@ -220,6 +220,137 @@ gdn_status_t gdn_step_tokens(int32_t N, int32_t S, int32_t H, int32_t dk, int32_
                              const float *g, const float *beta, const float *A_log, const float *D,
                              const float *h_in, float *h_out, void *o, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Latent attention and its paged cache: the softmax-attention layers that sit
+ * between GDN layers in the hybrid stack ("HyMo-434M documentation portal",
+ * MLA: one latent and one rotary key a token, shared by the heads). The
+ * projections are the caller's. Two forms:
+ *
+ *   expanded (gdn_mla_fwd, gdn_mla_bwd; training and prompts): every head has
+ *   keys k and values v made from the latent, and a rotary key k_rope that
+ *   heads share;
+ *   absorbed (gdn_mla_step; new tokens): the key and value maps are folded
+ *   into q and the output projection, so every head attends to the cached
+ *   rows [latent | rotary key] themselves.
+ *
+ * The rules at the top of this file hold (ownership, streams, errors, no
+ * allocation, bitwise reproducible results). Tensors are contiguous; q, k, v,
+ * o, c, x, cache and their gradients are fp32 or bf16 as the call's dtype
+ * says, sums and softmax statistics fp32. NaN/Inf in rows that take part
+ * propagate (and within a tile of 64 keys may reach queries before them);
+ * rows at or past a length, and cache rows no table entry in use names, are
+ * not read.
+ */
+
+/* q [B,Tq,H,dn+dr], k [B,Tk,Hk,dn], k_rope [B,Tk,Hr,dr], v [B,Tk,Hk,dv],
+ * o [B,Tq,H,dv], lse [B,Tq,H] fp32. Head h uses key head h / (H / Hk) and
+ * rotary head h / (H / Hr); Hk divides H and Hr divides Hk. dr = 0: no rotary
+ * part (k_rope may be NULL, Hr is not read). dn, dv: multiples of 8 up to
+ * 128; dr: one up to 64 (GDN_EUNSUPPORTED else). scale > 0. Tk >= Tq: the
+ * queries are the last Tq of the Tk positions (a chunk after cached ones). */
+typedef struct {
+    int32_t B, Tq, Tk, H, Hk, Hr, dn, dr, dv, dtype;
+    float scale;
+} gdn_mla_shape_t;
+
+/* Causal attention, forward: query i of sequence b sees the keys
+ * j <= i + Tk - Tq with j < lens[b] (lens NULL: Tk; values outside [0, Tk]
+ * are clamped).
+ *   z_ij = scale (q_i[:dn] . k_j + q_i[dn:] . k_rope_j)
+ *   o_i = sum_j softmax(z_i)_j v_j,  lse_i = log sum_j exp z_ij
+ * A query at a position >= lens[b] (padding) gets o = 0 and lse = -inf.
+ * lse may be NULL; gdn_mla_bwd needs it. Tq = 0 does nothing. */
+gdn_status_t gdn_mla_fwd(const gdn_mla_shape_t *s, const void *q, const void *k, const void *k_rope, const void *v,
+                         const int32_t *lens, void *o, float *lse, void *stream);
+
+/* Its backward: the gradients of sum(do * o) with respect to q, k, k_rope and
+ * v, summed over the heads that share a row; zero for padding. o and lse are
+ * the forward's. ws: gdn_mla_bwd_workspace_size() bytes, 256-byte aligned. */
+size_t gdn_mla_bwd_workspace_size(const gdn_mla_shape_t *s);
+gdn_status_t gdn_mla_bwd(const gdn_mla_shape_t *s, const void *q, const void *k, const void *k_rope, const void *v,
+                         const int32_t *lens, const void *o, const float *lse, const void *dout, void *dq, void *dk,
+                         void *dk_rope, void *dv, void *ws, size_t ws_bytes, void *stream);
+
+/* q [N,S,H,dl+dr], cache [pages,page_size,dl+dr], block_table [N,max_pages]
+ * int32 (page of each page_size tokens of a sequence), lens [N] int32 (cached
+ * tokens, the S new ones included), o [N,S,H,dl], lse [N,S,H] fp32. dl: a
+ * multiple of 16 up to 512; dr: one of 8 up to 64. pages * page_size and
+ * max_pages * page_size stay below 2^31 (the cache itself may be larger than
+ * 2^32 bytes). */
+typedef struct {
+    int32_t N, S, H, dl, dr, dtype, pages, page_size, max_pages;
+    float scale;
+} gdn_mla_step_shape_t;
+
+/* S new tokens for each of N sequences against their cached rows (which hold
+ * the new tokens' rows already, see gdn_mla_write): token s sees the rows
+ * j <= lens[n] - S + s.
+ *   z_j = scale q . row_j,  o = sum_j softmax(z)_j row_j[:dl],  lse = log sum_j exp z_j
+ * A token that sees no row gets o = 0 and lse = -inf. lens is clamped to
+ * [0, max_pages * page_size]; a table entry outside [0, pages) masks its
+ * rows. lse may be NULL. N = 0 or S = 0 does nothing. ws:
+ * gdn_mla_step_workspace_size() bytes, 256-byte aligned (it depends on the
+ * shape alone, not on the lengths). */
+size_t gdn_mla_step_workspace_size(const gdn_mla_step_shape_t *s);
+gdn_status_t gdn_mla_step(const gdn_mla_step_shape_t *s, const void *q, const void *cache, const int32_t *block_table,
+                          const int32_t *lens, void *o, float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/* Flags of gdn_norm_rope, gdn_norm_rope_bwd and gdn_mla_write. */
+#define GDN_ROPE_NORM 1u        /* RMS norm of every row (times w, when given) */
+#define GDN_ROPE_INTERLEAVED 2u /* pairs (2i, 2i + 1) instead of (i, i + r/2) */
+
+/* Norm and position rotation of every head's row in one pass, x, y [M,H,d]:
+ *   z = x / sqrt(mean(x^2) + eps) * w  (GDN_ROPE_NORM; w [d] fp32 or NULL = 1)
+ *   y = z with its last r columns turned pairwise, (a, b) ->
+ *       (a cos t - b sin t, b cos t + a sin t), t = positions[m] * freqs[i]
+ * positions [M] int32, freqs [r/2] fp64 (the angle is formed in fp64); both
+ * may be NULL with r = 0. 1 <= d <= 512, r even, 0 <= r <= d. y may be x. */
+gdn_status_t gdn_norm_rope(int64_t M, int32_t H, int32_t d, int32_t r, int32_t dtype, uint32_t flags, float eps,
+                           const void *x, const float *w, const int32_t *positions, const double *freqs, void *y,
+                           void *stream);
+
+/* Its backward: dx, and dw [d] fp32 (NULL: not wanted; overwritten). x may be
+ * NULL without GDN_ROPE_NORM. ws: gdn_norm_rope_bwd_workspace_size() bytes,
+ * 256-byte aligned, needed with dw. */
+size_t gdn_norm_rope_bwd_workspace_size(int64_t M, int32_t H, int32_t d);
+gdn_status_t gdn_norm_rope_bwd(int64_t M, int32_t H, int32_t d, int32_t r, int32_t dtype, uint32_t flags, float eps,
+                               const void *dy, const void *x, const float *w, const int32_t *positions,
+                               const double *freqs, void *dx, float *dw, void *ws, size_t ws_bytes, void *stream);
+
+/* Rows of n new tokens into the paged cache [n_slots,dl+dr]: row slots[i] =
+ * [norm(c_i) | turned k_rope_i], norm as above with GDN_ROPE_NORM (w [dl] fp32
+ * or NULL), the turn by positions[i] * freqs (freqs NULL: k_rope as it is).
+ * c [n,dl], k_rope [n,dr]. Slots outside [0, n_slots) are skipped; slots have
+ * to differ from each other (a row named twice holds a mixture). Rows no slot
+ * names stay as they are. dl: a multiple of 8 up to 512; dr: one up to 64. */
+gdn_status_t gdn_mla_write(int64_t n, int32_t dl, int32_t dr, int32_t dtype, uint32_t flags, float eps, const void *c,
+                           const void *k_rope, const float *w, const int32_t *positions, const double *freqs,
+                           const int32_t *slots, void *cache, int64_t n_slots, void *stream);
+
+/* Pages, slots and positions of the next step's tokens, on the GPU. Each of N
+ * sequences holds lens[i] cached tokens in the pages of its block_table row
+ * and asks for new_lens[i] more; new_lens[i] < 0 ends it: its pages go back on
+ * the stack of free pages (free_pages [n_pages], n_free of them, the last one
+ * on top) before any are taken, and its length becomes 0.
+ * In order, a sequence is granted what it asks for when its table row has
+ * room, the tokens asked for so far (by sequences with room) are at most
+ * max_tokens, and the pages asked for so far are at most those free (or it
+ * needs no new page); else it is granted nothing and stays as it is. New pages
+ * are popped from the stack's top into the sequence's row.
+ *   granted [N]        new tokens granted
+ *   starts [N+1]       their prefix sums: where a sequence's new tokens begin
+ *   slots [max_tokens] page * page_size + offset of every new token; -1 past
+ *                      the last one
+ *   positions [max_tokens]  its position in its sequence; 0 past the last one
+ *   lens_out [N]       lengths afterwards (may be lens)
+ *   n_free_out [1]     free pages afterwards (may be n_free)
+ * block_table and free_pages are updated in place; with separate lens_out and
+ * n_free_out the same call again gives the same result. All int32. */
+gdn_status_t gdn_page_plan(int32_t N, int32_t max_pages, int32_t n_pages, int32_t page_size, int32_t max_tokens,
+                           const int32_t *lens, const int32_t *new_lens, int32_t *block_table, int32_t *free_pages,
+                           const int32_t *n_free, int32_t *lens_out, int32_t *n_free_out, int32_t *granted,
+                           int32_t *starts, int32_t *slots, int32_t *positions, void *stream);
+
 /* Timing aid for benchmarks (no effect on results). While `events` is
  * non-NULL, every kernel the library launches from this thread is bracketed
  * by hipEventRecord calls on the launch's stream: events[2i] before launch i
@@ -233,11 +364,16 @@ int32_t gdn_time_launches(void *const *events, int32_t n);
  * off, the last) bracketing period was: 0 forward prep, 1 forward serial
  * pass, 2 backward serial pass, 3 backward local gradients, 4 dA_log (or
  * dD) reduction, 5 decode step, 6 forward scan over chunk ranges, 7 backward
- * scan; -1 when i is out of range. A forward call may launch its two kernels
- * several times each, over consecutive chunk ranges (prep of the next range
- * runs on a second stream while the serial pass works on the current one),
- * and a serial pass run as a parallel scan launches twice (the ranges' maps,
- * then every range from its start). */
+ * scan, 8 attention forward, 9 and 10 attention backward (query gradients;
+ * key and value gradients), 11 sum of the shared rotary key's gradient, 12
+ * attention against the paged cache, 13 join of its parts, 14 norm and
+ * rotation, 15 their backward, 16 sum of the norm weight's gradient, 17 cache
+ * write, 18 page plan, 19 slots of a page plan; -1 when i is out of range. A
+ * forward call may launch its two kernels several times each, over
+ * consecutive chunk ranges (prep of the next range runs on a second stream
+ * while the serial pass works on the current one), and a serial pass run as a
+ * parallel scan launches twice (the ranges' maps, then every range from its
+ * start). */
 int32_t gdn_launch_kind(int32_t i);
 
 const char *gdn_status_string(gdn_status_t st);
