@@ -247,7 +247,7 @@ __global__ __launch_bounds__(NW * 64) void mla_bwd_k_kernel(MlaBwdArgs a) {
         // no query of the tile sees a key of this wave
         if (row0 + MLA_BT - 1 + off < w0 || w0 >= n) continue;
         const bool mask = row0 + off < w0 + KT * 16 - 1 || row0 + MLA_BT > nq || w0 + KT * 16 > n;
-#pragma unroll
+#pragma unroll 1
         for (int u = 0; u < MLA_BT / 32; ++u) {
             f32x4 P[KT][2], dP[KT][2];
 #pragma unroll
