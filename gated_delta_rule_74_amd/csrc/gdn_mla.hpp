@@ -229,6 +229,26 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
+// Keeps the compiler from moving instructions across: what is requested before
+// it is in flight during what comes after. Without it the compiler, short of
+// registers, sinks every LDS read to just before its use and waits for it.
+__device__ __forceinline__ void in_flight() { __builtin_amdgcn_sched_barrier(0); }
+
+// N operands along K of the 16 rows at p (row stride ld), for this lane.
+template <bool BF, int N> struct Frags {
+    Frag<BF> f[N];
+    __device__ __forceinline__ void rows(const typename Op<BF>::S *X, int ld, int row0, int lane) {
+        const typename Op<BF>::S *p = X + (row0 + (lane & 15)) * ld + 8 * (lane >> 4);
+#pragma unroll
+        for (int k = 0; k < N; ++k) f[k] = row8(p + 32 * k);
+    }
+    // N operand columns of 16 from column m0 on, over the 32 rows from k0
+    __device__ __forceinline__ void cols(const typename Op<BF>::S *X, int ld, int k0, int m0, int lane) {
+#pragma unroll
+        for (int v = 0; v < N; ++v) f[v] = col8(X, ld, k0, m0 + 16 * v, lane);
+    }
+};
+
 // Rows of a sequence, NR at a time, from global memory over registers into an
 // LDS tile [NR][ld]: columns 0 .. d0 - 1 from x0, d0 .. d0 + d1 - 1 from x1
 // (both multiples of 8), zeros up to DP and for rows past `n`. fetch() only
@@ -264,11 +284,23 @@ template <bool BF, int DP, int NR, int NT> struct RowTile {
     }
 };
 
-// Workgroup -> logical index so that each XCD (workgroups go round robin over
-// the 8) works on a contiguous range of them, for any number of workgroups.
-__device__ __forceinline__ int xcd_range(int bid, int n) {
-    const int q = n / 8, rem = n % 8, x = bid % 8, i = bid / 8;
-    return x * q + min(x, rem) + i;
+// Workgroup -> (batch-head, block of its sequence), longest walks first.
+// Workgroups go round robin over the 8 XCDs: eight heads at a time run side by
+// side, one per XCD, so that a head's rows are read into one L2; what is left
+// over (fewer than eight heads) is dealt out block by block, which keeps the
+// XCDs equally loaded when there are few heads (four heads of 128 causal
+// blocks, two XCDs each: half a head per XCD would give one of the two three
+// times the work of the other).
+__device__ __forceinline__ void head_block(int id, int heads, int blocks, int &bh, int &blk) {
+    const int full = heads / 8 * 8;
+    if (id < full * blocks) {
+        bh = id / (8 * blocks) * 8 + id % 8;
+        blk = id / 8 % blocks;
+    } else {
+        const int i = id - full * blocks;
+        bh = full + i % (heads - full);
+        blk = i / (heads - full);
+    }
 }
 
 } // namespace gdn

@@ -24,9 +24,21 @@
 namespace gdn {
 
 constexpr int MLA_BT = 64; // walked rows per tile
+#ifndef QOCC
+#define QOCC 2
+#endif
+#ifndef KOCC
+#define KOCC (DP + DVP <= 160 ? 2 : 1)
+#endif
+#ifndef QQT
+#define QQT 2
+#endif
+#ifndef KKT
+#define KKT 2
+#endif
 
 template <bool BF, int DP, int DVP, int NW, int QT>
-__global__ __launch_bounds__(NW * 64) void mla_bwd_q_kernel(MlaBwdArgs a) {
+__global__ __launch_bounds__(NW * 64, QOCC) void mla_bwd_q_kernel(MlaBwdArgs a) {
     using S = typename Op<BF>::S;
     constexpr int LDK = DP + Op<BF>::PAD, LDV = DVP + Op<BF>::PAD, NT = NW * 64, KS = DP / 32, VS = DVP / 32,
                   MD = DP / 16;
@@ -36,8 +48,9 @@ __global__ __launch_bounds__(NW * 64) void mla_bwd_q_kernel(MlaBwdArgs a) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
     constexpr int QB = NW * QT * 16;
     const int nqb = (s.Tq + QB - 1) / QB;
-    const int id = xcd_range(blockIdx.x, gridDim.x);
-    const int bh = id / nqb, qb = nqb - 1 - id % nqb;
+    int bh, qb;
+    head_block(blockIdx.x, s.B * s.H, nqb, bh, qb);
+    qb = nqb - 1 - qb; // the last queries walk longest
     const int b = bh / s.H, h = bh % s.H, hk = h / (s.H / s.Hk);
     const int hr = s.Hr > 0 ? h / (s.H / s.Hr) : 0;
     const int D = s.dn + s.dr, off = s.Tk - s.Tq;
@@ -105,10 +118,10 @@ __global__ __launch_bounds__(NW * 64) void mla_bwd_q_kernel(MlaBwdArgs a) {
             vt.fetch(vp, rv, s.dv, vp, 0, 0, key0 + MLA_BT, n, tid);
         }
         lds_barrier();
-        if (key0 > wlast || wfirst >= n) continue;
+        const int nu = key0 > wlast || wfirst >= n ? 0 : MLA_BT / 32; // (0: no query of the wave sees the tile)
         const bool mask = key0 + MLA_BT - 1 > wfirst || key0 + MLA_BT > n;
-#pragma unroll
-        for (int u = 0; u < MLA_BT / 32; ++u) {
+#pragma unroll 1
+        for (int u = 0; u < nu; ++u) {
             f32x4 P[QT][2], dP[QT][2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -162,7 +175,7 @@ __global__ __launch_bounds__(NW * 64) void mla_bwd_q_kernel(MlaBwdArgs a) {
 }
 
 template <bool BF, int DP, int DVP, int NW, int KT>
-__global__ __launch_bounds__(NW * 64) void mla_bwd_k_kernel(MlaBwdArgs a) {
+__global__ __launch_bounds__(NW * 64, KOCC) void mla_bwd_k_kernel(MlaBwdArgs a) {
     using S = typename Op<BF>::S;
     constexpr int LDQ = DP + Op<BF>::PAD, LDG = DVP + Op<BF>::PAD, NT = NW * 64, KS = DP / 32, VS = DVP / 32,
                   MD = DP / 16, MV = DVP / 16;
@@ -173,9 +186,8 @@ __global__ __launch_bounds__(NW * 64) void mla_bwd_k_kernel(MlaBwdArgs a) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
     constexpr int KB = NW * KT * 16;
     const int nkb = (s.Tk + KB - 1) / KB;
-    // the longest walks (first keys) first
-    const int id = xcd_range(blockIdx.x, gridDim.x);
-    const int bh = id / nkb, kb = id % nkb;
+    int bh, kb; // (the first keys walk longest)
+    head_block(blockIdx.x, s.B * s.Hk, nkb, bh, kb);
     const int b = bh / s.Hk, hk = bh % s.Hk, per = s.H / s.Hk;
     const int hr = s.Hr > 0 ? hk / (s.Hk / s.Hr) : 0;
     const int D = s.dn + s.dr, off = s.Tk - s.Tq;
@@ -233,6 +245,19 @@ __global__ __launch_bounds__(NW * 64) void mla_bwd_k_kernel(MlaBwdArgs a) {
         for (int v = 0; v < MV; ++v) dV[t][v] = zero4();
     }
     const float c2 = s.scale * (float)LOG2E;
+    // S and dP of 16 walked rows against the wave's keys
+    auto scores = [&](f32x4 (&P)[KT][2], f32x4 (&dP)[KT][2], int j, const Frags<BF, KS> &q, const Frags<BF, VS> &gr) {
+#pragma unroll
+        for (int t = 0; t < KT; ++t) P[t][j] = dP[t][j] = zero4();
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int t = 0; t < KT; ++t) P[t][j] = mma8(q.f[k], K[t][k], P[t][j]);
+#pragma unroll
+        for (int k = 0; k < VS; ++k)
+#pragma unroll
+            for (int t = 0; t < KT; ++t) dP[t][j] = mma8(gr.f[k], V[t][k], dP[t][j]);
+    };
     for (int x = 0; x < total; ++x) {
         const int row0 = (t_lo + x % tiles) * MLA_BT;
         lds_barrier();
@@ -244,29 +269,27 @@ __global__ __launch_bounds__(NW * 64) void mla_bwd_k_kernel(MlaBwdArgs a) {
         }
         if (x + 1 < total) fetch(x + 1);
         lds_barrier();
-        // no query of the tile sees a key of this wave
-        if (row0 + MLA_BT - 1 + off < w0 || w0 >= n) continue;
+        // (0: no query of the tile sees a key of this wave)
+        const int nu = row0 + MLA_BT - 1 + off < w0 || w0 >= n ? 0 : MLA_BT / 32;
         const bool mask = row0 + off < w0 + KT * 16 - 1 || row0 + MLA_BT > nq || w0 + KT * 16 > n;
 #pragma unroll 1
-        for (int u = 0; u < MLA_BT / 32; ++u) {
+        for (int u = 0; u < nu; ++u) {
             f32x4 P[KT][2], dP[KT][2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-#pragma unroll
-                for (int t = 0; t < KT; ++t) P[t][j] = dP[t][j] = zero4();
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    const Frag<BF> qf = row8(Qs + (32 * u + 16 * j + r) * LDQ + 32 * k + 8 * g);
-#pragma unroll
-                    for (int t = 0; t < KT; ++t) P[t][j] = mma8(qf, K[t][k], P[t][j]);
-                }
-#pragma unroll
-                for (int k = 0; k < VS; ++k) {
-                    const Frag<BF> gf = row8(Gs + (32 * u + 16 * j + r) * LDG + 32 * k + 8 * g);
-#pragma unroll
-                    for (int t = 0; t < KT; ++t) dP[t][j] = mma8(gf, V[t][k], dP[t][j]);
-                }
-            }
+            Frags<BF, KS> qa, qb;
+            Frags<BF, VS> ga, gb;
+            qa.rows(Qs, LDQ, 32 * u, lane);
+            ga.rows(Gs, LDG, 32 * u, lane);
+            in_flight();
+            qb.rows(Qs, LDQ, 32 * u + 16, lane);
+            gb.rows(Gs, LDG, 32 * u + 16, lane);
+            in_flight();
+            scores(P, dP, 0, qa, ga);
+            in_flight();
+            constexpr int CV = MV < 4 ? MV : 4, CK = MD % 4 == 0 ? 4 : 3; // operands requested at a time
+            Frags<BF, CV> vc;
+            vc.cols(Gs, LDG, 32 * u, 0, lane);
+            in_flight();
+            scores(P, dP, 1, qb, gb);
             Frag<BF> pf[KT], sf[KT];
 #pragma unroll
             for (int t = 0; t < KT; ++t) {
@@ -275,31 +298,48 @@ __global__ __launch_bounds__(NW * 64) void mla_bwd_k_kernel(MlaBwdArgs a) {
                     const int i0 = 32 * u + 16 * j + 4 * g; // first of this lane's four rows
                     const f32x4 ls = *reinterpret_cast<const f32x4 *>(Ls + i0);
                     const f32x4 dl = *reinterpret_cast<const f32x4 *>(Ds + i0);
-                    // row e sees this lane's key from row w0 + 16 t + r - off on; no key at or past n
-                    const int j_at = w0 + 16 * t + r, lo = j_at - off - row0 - i0, hi = nq - row0 - i0;
+                    if (mask) {
+                        // row e sees this lane's key from row j_at - off on; no key at or past n
+                        const int j_at = w0 + 16 * t + r, lo = j_at - off - row0 - i0, hi = nq - row0 - i0;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            P[t][j][e] = e >= lo && e < hi && j_at < n ? P[t][j][e] : -INFINITY;
+                    }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float p = exp2_fast(fmaf(P[t][j][e], c2, -ls[e]));
-                        float d = p * (dP[t][j][e] - dl[e]);
-                        const bool in = !mask || (e >= lo && e < hi && j_at < n);
-                        P[t][j][e] = in ? p : 0.f;
-                        dP[t][j][e] = in ? d : 0.f;
+                        P[t][j][e] = exp2_fast(fmaf(P[t][j][e], c2, -ls[e]));
+                        dP[t][j][e] = P[t][j][e] * (dP[t][j][e] - dl[e]);
                     }
                 }
                 pf[t] = acc8<BF>(P[t][0], P[t][1]);
                 sf[t] = acc8<BF>(dP[t][0], dP[t][1]);
             }
+            // the next group of operands is requested before the products of the one at hand
+            Frags<BF, CK> kc;
 #pragma unroll
-            for (int v = 0; v < MV; ++v) {
-                const Frag<BF> gf = col8(Gs, LDG, 32 * u, 16 * v, lane);
+            for (int v0 = 0; v0 < MV; v0 += CV) {
+                Frags<BF, CV> nv;
+                in_flight();
+                if (v0 + CV < MV) nv.cols(Gs, LDG, 32 * u, 16 * (v0 + CV), lane);
+                else kc.cols(Qs, LDQ, 32 * u, 0, lane);
+                in_flight();
 #pragma unroll
-                for (int t = 0; t < KT; ++t) dV[t][v] = mma8(gf, pf[t], dV[t][v]);
+                for (int v = 0; v < CV; ++v)
+#pragma unroll
+                    for (int t = 0; t < KT; ++t) dV[t][v0 + v] = mma8(vc.f[v], pf[t], dV[t][v0 + v]);
+                vc = nv;
             }
 #pragma unroll
-            for (int v = 0; v < MD; ++v) {
-                const Frag<BF> qf = col8(Qs, LDQ, 32 * u, 16 * v, lane);
+            for (int v0 = 0; v0 < MD; v0 += CK) {
+                Frags<BF, CK> nk;
+                in_flight();
+                if (v0 + CK < MD) nk.cols(Qs, LDQ, 32 * u, 16 * (v0 + CK), lane);
+                in_flight();
 #pragma unroll
-                for (int t = 0; t < KT; ++t) dK[t][v] = mma8(qf, sf[t], dK[t][v]);
+                for (int v = 0; v < CK; ++v)
+#pragma unroll
+                    for (int t = 0; t < KT; ++t) dK[t][v0 + v] = mma8(kc.f[v], sf[t], dK[t][v0 + v]);
+                kc = nk;
             }
         }
     }
@@ -331,14 +371,14 @@ __global__ __launch_bounds__(NW * 64) void mla_bwd_k_kernel(MlaBwdArgs a) {
 }
 
 template <bool BF, int DP, int DVP> hipError_t mla_bwd_q_run(const MlaBwdArgs &a, hipStream_t st) {
-    constexpr int NW = 4, QT = BF && DP <= 128 ? 2 : 1;
+    constexpr int NW = 4, QT = BF && DP <= 128 ? QQT : 1;
     const long long nqb = (a.s.Tq + NW * QT * 16 - 1) / (NW * QT * 16);
     hipLaunchKernelGGL((mla_bwd_q_kernel<BF, DP, DVP, NW, QT>), dim3((unsigned)(nqb * a.s.B * a.s.H)), dim3(NW * 64),
                        0, st, a);
     return hipGetLastError();
 }
 template <bool BF, int DP, int DVP> hipError_t mla_bwd_k_run(const MlaBwdArgs &a, hipStream_t st) {
-    constexpr int NW = 4, KT = BF ? 2 : 1;
+    constexpr int NW = 4, KT = BF ? KKT : 1;
     const long long nkb = (a.s.Tk + NW * KT * 16 - 1) / (NW * KT * 16);
     hipLaunchKernelGGL((mla_bwd_k_kernel<BF, DP, DVP, NW, KT>), dim3((unsigned)(nkb * a.s.B * a.s.Hk)), dim3(NW * 64),
                        0, st, a);

@@ -26,21 +26,27 @@ namespace gdn {
 constexpr int MLA_KT = 64;      // keys per tile
 constexpr float MLA_RAISE = 8.f; // see above
 
+#ifndef FOCC
+#define FOCC 2
+#endif
+#ifndef FQT
+#define FQT 2
+#endif
 template <bool BF, int DP, int DVP, int NW, int QT>
-__global__ __launch_bounds__(NW * 64) void mla_fwd_kernel(MlaFwdArgs a) {
+__global__ __launch_bounds__(NW * 64, FOCC) void mla_fwd_kernel(MlaFwdArgs a) {
     using S = typename Op<BF>::S;
     constexpr int LDK = DP + Op<BF>::PAD, LDV = DVP + Op<BF>::PAD, NT = NW * 64, KS = DP / 32, MV = DVP / 16;
-    // two tiles in bf16; one in fp32, where two of the widest pass 160 KB
-    constexpr int NB = BF ? 2 : 1;
+    // two tiles where a second workgroup still fits the CU's 160 KB beside them
+    constexpr int NB = 2 * MLA_KT * (LDK + LDV) * (int)sizeof(S) <= 80 * 1024 ? 2 : 1;
     __shared__ __align__(16) S Ks[NB][MLA_KT * LDK];
     __shared__ __align__(16) S Vs[NB][MLA_KT * LDV];
     const MlaArgs &s = a.s;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
     constexpr int QB = NW * QT * 16;
     const int nqb = (s.Tq + QB - 1) / QB;
-    // the longest walks (last queries) of a head first, heads of one XCD together
-    const int id = xcd_range(blockIdx.x, gridDim.x);
-    const int bh = id / nqb, qb = nqb - 1 - id % nqb;
+    int bh, qb;
+    head_block(blockIdx.x, s.B * s.H, nqb, bh, qb);
+    qb = nqb - 1 - qb; // the last queries walk longest
     const int b = bh / s.H, h = bh % s.H, hk = h / (s.H / s.Hk);
     const int hr = s.Hr > 0 ? h / (s.H / s.Hr) : 0;
     const int D = s.dn + s.dr, off = s.Tk - s.Tq;
@@ -98,73 +104,69 @@ __global__ __launch_bounds__(NW * 64) void mla_fwd_kernel(MlaFwdArgs a) {
         }
         if (key0 <= wlast && wfirst < n) {
             const S *K = Ks[kb % NB], *V = Vs[kb % NB];
-            f32x4 P[QT][4];
+            const bool mask = key0 + MLA_KT - 1 > wfirst || key0 + MLA_KT > n;
+#pragma unroll 1
+            for (int u = 0; u < MLA_KT / 32; ++u) {
+                f32x4 P[QT][2];
 #pragma unroll
-            for (int t = 0; t < QT; ++t)
+                for (int t = 0; t < QT; ++t) P[t][0] = P[t][1] = zero4();
 #pragma unroll
-                for (int j = 0; j < 4; ++j) P[t][j] = zero4();
+                for (int k = 0; k < KS; ++k)
 #pragma unroll
-            for (int k = 0; k < KS; ++k)
+                    for (int j = 0; j < 2; ++j) {
+                        const Frag<BF> kf = row8(K + (32 * u + 16 * j + r) * LDK + 32 * k + 8 * g);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const Frag<BF> kf = row8(K + (16 * j + r) * LDK + 32 * k + 8 * g);
+                        for (int t = 0; t < QT; ++t) P[t][j] = mma8(kf, Q[t][k], P[t][j]);
+                    }
+                // the mask, where this tile reaches past a query or the sequence
+                if (mask) {
 #pragma unroll
-                    for (int t = 0; t < QT; ++t) P[t][j] = mma8(kf, Q[t][k], P[t][j]);
+                    for (int t = 0; t < QT; ++t) {
+                        const int lim = min(q0 + 16 * t + r + off, n - 1) - key0 - 32 * u - 4 * g; // last key seen
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) P[t][j][e] = 16 * j + e <= lim ? P[t][j][e] : -INFINITY;
+                    }
                 }
-            // the mask, where this tile reaches past a query or the sequence
-            if (key0 + MLA_KT - 1 > wfirst || key0 + MLA_KT > n) {
+                float mx[QT];
+                bool raise = false;
 #pragma unroll
                 for (int t = 0; t < QT; ++t) {
-                    const int lim = min(q0 + 16 * t + r + off, n - 1) - key0 - 4 * g; // last key seen
+                    float x = P[t][0][0];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < 2; ++j)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) P[t][j][e] = 16 * j + e <= lim ? P[t][j][e] : -INFINITY;
+                        for (int e = 0; e < 4; ++e) x = fmaxf(x, P[t][j][e]);
+                    mx[t] = x * c2;
+                    raise |= mx[t] > m[t] + MLA_RAISE;
                 }
-            }
-            float mx[QT];
-            bool raise = false;
+                if (__any(raise)) {
 #pragma unroll
-            for (int t = 0; t < QT; ++t) {
-                float x = P[t][0][0];
+                    for (int t = 0; t < QT; ++t) {
+                        const float mn = fmaxf(m[t], max4g(mx[t]));
+                        const float f = mn == -INFINITY ? 1.f : exp2_fast(m[t] - mn);
+                        m[t] = mn;
+                        l[t] *= f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x = fmaxf(x, P[t][j][e]);
-                mx[t] = x * c2;
-                raise |= mx[t] > m[t] + MLA_RAISE;
-            }
-            if (__any(raise)) {
-#pragma unroll
-                for (int t = 0; t < QT; ++t) {
-                    const float mn = fmaxf(m[t], max4g(mx[t]));
-                    const float f = mn == -INFINITY ? 1.f : exp2_fast(m[t] - mn);
-                    m[t] = mn;
-                    l[t] *= f;
-#pragma unroll
-                    for (int v = 0; v < MV; ++v) O[t][v] *= f;
+                        for (int v = 0; v < MV; ++v) O[t][v] *= f;
+                    }
                 }
-            }
-#pragma unroll
-            for (int t = 0; t < QT; ++t) {
-                const float mt = m[t] == -INFINITY ? 0.f : m[t];
-                f32x4 sum = zero4();
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) P[t][j][e] = exp2_fast(fmaf(P[t][j][e], c2, -mt));
-                    sum += P[t][j];
-                }
-                l[t] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
                 Frag<BF> pf[QT];
 #pragma unroll
-                for (int t = 0; t < QT; ++t) pf[t] = acc8<BF>(P[t][2 * k], P[t][2 * k + 1]);
+                for (int t = 0; t < QT; ++t) {
+                    const float mt = m[t] == -INFINITY ? 0.f : m[t];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) P[t][j][e] = exp2_fast(fmaf(P[t][j][e], c2, -mt));
+                    const f32x4 sum = P[t][0] + P[t][1];
+                    l[t] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    pf[t] = acc8<BF>(P[t][0], P[t][1]);
+                }
 #pragma unroll
                 for (int v = 0; v < MV; ++v) {
-                    const Frag<BF> vf = col8(V, LDV, 32 * k, 16 * v, lane);
+                    const Frag<BF> vf = col8(V, LDV, 32 * u, 16 * v, lane);
 #pragma unroll
                     for (int t = 0; t < QT; ++t) O[t][v] = mma8(vf, pf[t], O[t][v]);
                 }
@@ -199,7 +201,7 @@ __global__ __launch_bounds__(NW * 64) void mla_fwd_kernel(MlaFwdArgs a) {
 }
 
 template <bool BF, int DP, int DVP> hipError_t mla_fwd_run(const MlaFwdArgs &a, hipStream_t st) {
-    constexpr int NW = 4, QT = BF ? 2 : 1;
+    constexpr int NW = 4, QT = BF ? FQT : 1;
     const long long nqb = (a.s.Tq + NW * QT * 16 - 1) / (NW * QT * 16);
     hipLaunchKernelGGL((mla_fwd_kernel<BF, DP, DVP, NW, QT>), dim3((unsigned)(nqb * a.s.B * a.s.H)), dim3(NW * 64), 0,
                        st, a);
