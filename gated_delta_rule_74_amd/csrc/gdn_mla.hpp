@@ -249,38 +249,48 @@ template <bool BF, int N> struct Frags {
     }
 };
 
+// sixteen bytes of zeros: where a tile's padding columns are loaded from
+__device__ const uint4 mla_zeros = {0u, 0u, 0u, 0u};
+
 // Rows of a sequence, NR at a time, from global memory over registers into an
 // LDS tile [NR][ld]: columns 0 .. d0 - 1 from x0, d0 .. d0 + d1 - 1 from x1
-// (both multiples of 8), zeros up to DP and for rows past `n`. fetch() only
-// issues the loads (from clamped addresses inside the tensors), stash()
-// masks and writes, so the loads stay in flight in between.
+// (both multiples of 8), zeros up to DP and for rows past the end. A thread
+// has one 16-byte column of every RP-th row, so its source and row stride are
+// fixed (padding columns: the zeros above, with stride 0). fetch() only issues
+// the loads (rows past the end read the last one), without a branch that would
+// have them waited for; stash() masks and writes.
 template <bool BF, int DP, int NR, int NT> struct RowTile {
     using S = typename Op<BF>::S;
     static constexpr int V = Op<BF>::VEC;
     static constexpr int NG = DP / V;
-    static constexpr int NIT = (NR * NG + NT - 1) / NT;
-    static constexpr bool FULL = (NR * NG) % NT == 0;
+    static constexpr int RP = NT / NG, NIT = (NR + RP - 1) / RP;
     uint4 r[NIT];
-    __device__ __forceinline__ void fetch(const S *__restrict__ x0, size_t rs0, int d0, const S *__restrict__ x1,
-                                          size_t rs1, int d1, int row0, int n, int tid) {
-#pragma unroll
-        for (int m = 0; m < NIT; ++m) {
-            const int it = tid + m * NT;
-            const int j = min(row0 + it / NG, n - 1), c = (it % NG) * V;
-            const S *p = c < d0 ? x0 + (size_t)j * rs0 + c : x0;
-            if (d1 > 0 && c >= d0) p = x1 + (size_t)j * rs1 + min(c - d0, d1 - V);
-            r[m] = *reinterpret_cast<const uint4 *>(p);
-        }
+    const S *p;
+    unsigned rs;
+    int j0, c;
+    __device__ __forceinline__ void init(const S *x0, size_t rs0, int d0, const S *x1, size_t rs1, int d1, int tid) {
+        c = (tid % NG) * V;
+        j0 = tid < RP * NG ? tid / NG : NR; // (the threads left over write nothing)
+        p = c < d0 ? x0 + c : c < d0 + d1 ? x1 + (c - d0) : (const S *)&mla_zeros;
+        rs = c < d0 ? (unsigned)rs0 : c < d0 + d1 ? (unsigned)rs1 : 0u;
     }
-    __device__ __forceinline__ void stash(S *dst, int ld, int d, int row0, int n, int tid) const {
+    // from row row0 on, of n rows (n >= 1), `shift` elements further (another head)
+    __device__ __forceinline__ void fetch(int row0, int n, size_t shift = 0) {
+        const S *q = p + (rs ? shift : 0);
 #pragma unroll
-        for (int m = 0; m < NIT; ++m) {
-            const int it = tid + m * NT;
-            const int j = it / NG, c = (it % NG) * V;
-            if (!FULL && j >= NR) continue;
-            const bool in = row0 + j < n && c < d;
-            *reinterpret_cast<uint4 *>(dst + j * ld + c) = in ? r[m] : uint4{0u, 0u, 0u, 0u};
+        for (int m = 0; m < NIT; ++m)
+            r[m] = *reinterpret_cast<const uint4 *>(q + (size_t)(unsigned)min(row0 + j0 + m * RP, n - 1) * rs);
+    }
+    __device__ __forceinline__ void stash(S *dst, int ld, int row0, int n) {
+        S *q = dst + j0 * ld + c;
+        if (row0 + NR > n) { // (the last tile)
+#pragma unroll
+            for (int m = 0; m < NIT; ++m)
+                if (row0 + j0 + m * RP >= n) r[m] = uint4{0u, 0u, 0u, 0u};
         }
+#pragma unroll
+        for (int m = 0; m < NIT; ++m)
+            if (j0 + m * RP < NR) *reinterpret_cast<uint4 *>(q + m * RP * ld) = r[m];
     }
 };
 

@@ -45,7 +45,7 @@ __global__ __launch_bounds__(NW * 64, QOCC) void mla_bwd_q_kernel(MlaBwdArgs a) 
     __shared__ __align__(16) S Ks[MLA_BT * LDK];
     __shared__ __align__(16) S Vs[MLA_BT * LDV];
     const MlaArgs &s = a.s;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
     constexpr int QB = NW * QT * 16;
     const int nqb = (s.Tq + QB - 1) / QB;
     int bh, qb;
@@ -66,9 +66,11 @@ __global__ __launch_bounds__(NW * 64, QOCC) void mla_bwd_q_kernel(MlaBwdArgs a) 
 
     RowTile<BF, DP, MLA_BT, NT> kt;
     RowTile<BF, DVP, MLA_BT, NT> vt;
+    kt.init(kp, rk, s.dn, krp, rr, s.dr, tid);
+    vt.init(vp, rv, s.dv, vp, 0, 0, tid);
     if (nt > 0) {
-        kt.fetch(kp, rk, s.dn, krp, rr, s.dr, 0, n, tid);
-        vt.fetch(vp, rv, s.dv, vp, 0, 0, 0, n, tid);
+        kt.fetch(0, n);
+        vt.fetch(0, n);
     }
     Frag<BF> Q[QT][KS], G[QT][VS]; // q and do as operand columns
     float lse2[QT], delta[QT];
@@ -108,14 +110,15 @@ __global__ __launch_bounds__(NW * 64, QOCC) void mla_bwd_q_kernel(MlaBwdArgs a) 
         for (int v = 0; v < MD; ++v) dQ[t][v] = zero4();
     const float c2 = s.scale * (float)LOG2E;
     const int wlast = min(q0 + QT * 16 - 1 + off, n - 1), wfirst = q0 + off;
+    wait_vmem(); // (what is held is there: else its first use in the loop waits for the tile in flight)
     for (int kb = 0; kb < nt; ++kb) {
         const int key0 = kb * MLA_BT;
         lds_barrier(); // the previous tile's readers are done
-        kt.stash(Ks, LDK, D, key0, n, tid);
-        vt.stash(Vs, LDV, s.dv, key0, n, tid);
+        kt.stash(Ks, LDK, key0, n);
+        vt.stash(Vs, LDV, key0, n);
         if (kb + 1 < nt) {
-            kt.fetch(kp, rk, s.dn, krp, rr, s.dr, key0 + MLA_BT, n, tid);
-            vt.fetch(vp, rv, s.dv, vp, 0, 0, key0 + MLA_BT, n, tid);
+            kt.fetch(key0 + MLA_BT, n);
+            vt.fetch(key0 + MLA_BT, n);
         }
         lds_barrier();
         const int nu = key0 > wlast || wfirst >= n ? 0 : MLA_BT / 32; // (0: no query of the wave sees the tile)
@@ -143,14 +146,18 @@ __global__ __launch_bounds__(NW * 64, QOCC) void mla_bwd_q_kernel(MlaBwdArgs a) 
             Frag<BF> ds[QT];
 #pragma unroll
             for (int t = 0; t < QT; ++t) {
-                const int lim = min(q0 + 16 * t + r + off, n - 1) - key0 - 32 * u - 4 * g;
+                if (mask) {
+                    const int lim = min(q0 + 16 * t + r + off, n - 1) - key0 - 32 * u - 4 * g;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) P[t][j][e] = 16 * j + e <= lim ? P[t][j][e] : -INFINITY;
+                }
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float x = exp2_fast(fmaf(P[t][j][e], c2, -lse2[t])) * (dP[t][j][e] - delta[t]);
-                        P[t][j][e] = (!mask || 16 * j + e <= lim) ? x : 0.f;
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        P[t][j][e] = exp2_fast(fmaf(P[t][j][e], c2, -lse2[t])) * (dP[t][j][e] - delta[t]);
                 ds[t] = acc8<BF>(P[t][0], P[t][1]);
             }
 #pragma unroll
@@ -183,7 +190,7 @@ __global__ __launch_bounds__(NW * 64, KOCC) void mla_bwd_k_kernel(MlaBwdArgs a) 
     __shared__ __align__(16) S Gs[MLA_BT * LDG];
     __shared__ __align__(16) float Ls[MLA_BT], Ds[MLA_BT];
     const MlaArgs &s = a.s;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
     constexpr int KB = NW * KT * 16;
     const int nkb = (s.Tk + KB - 1) / KB;
     int bh, kb; // (the first keys walk longest)
@@ -203,13 +210,15 @@ __global__ __launch_bounds__(NW * 64, KOCC) void mla_bwd_k_kernel(MlaBwdArgs a) 
 
     RowTile<BF, DP, MLA_BT, NT> qt;
     RowTile<BF, DVP, MLA_BT, NT> gt;
+    const S *qp = (const S *)s.q + (size_t)b * s.Tq * rq + (size_t)hk * per * D; // first of the heads
+    const S *gp = (const S *)a.dout + (size_t)b * s.Tq * ro + (size_t)hk * per * s.dv;
+    qt.init(qp, rq, D, qp, 0, 0, tid);
+    gt.init(gp, ro, s.dv, gp, 0, 0, tid);
     float lreg = 0.f, dreg = 0.f;
     auto fetch = [&](int x) {
         const int h = hk * per + x / tiles, row0 = (t_lo + x % tiles) * MLA_BT;
-        const S *qp = (const S *)s.q + (size_t)b * s.Tq * rq + (size_t)h * D;
-        const S *gp = (const S *)a.dout + (size_t)b * s.Tq * ro + (size_t)h * s.dv;
-        qt.fetch(qp, rq, D, qp, 0, 0, row0, nq, tid);
-        gt.fetch(gp, ro, s.dv, gp, 0, 0, row0, nq, tid);
+        qt.fetch(row0, nq, (size_t)(x / tiles) * D);
+        gt.fetch(row0, nq, (size_t)(x / tiles) * s.dv);
         if (tid < MLA_BT) {
             const int i = min(row0 + tid, nq - 1);
             lreg = a.lse[((size_t)b * s.Tq + i) * s.H + h];
@@ -258,11 +267,12 @@ __global__ __launch_bounds__(NW * 64, KOCC) void mla_bwd_k_kernel(MlaBwdArgs a) 
 #pragma unroll
             for (int t = 0; t < KT; ++t) dP[t][j] = mma8(gr.f[k], V[t][k], dP[t][j]);
     };
+    wait_vmem(); // (as above)
     for (int x = 0; x < total; ++x) {
         const int row0 = (t_lo + x % tiles) * MLA_BT;
         lds_barrier();
-        qt.stash(Qs, LDQ, D, row0, nq, tid);
-        gt.stash(Gs, LDG, s.dv, row0, nq, tid);
+        qt.stash(Qs, LDQ, row0, nq);
+        gt.stash(Gs, LDG, row0, nq);
         if (tid < MLA_BT) {
             Ls[tid] = lreg == -INFINITY ? INFINITY : lreg * (float)LOG2E;
             Ds[tid] = dreg;

@@ -41,7 +41,7 @@ __global__ __launch_bounds__(NW * 64, FOCC) void mla_fwd_kernel(MlaFwdArgs a) {
     __shared__ __align__(16) S Ks[NB][MLA_KT * LDK];
     __shared__ __align__(16) S Vs[NB][MLA_KT * LDV];
     const MlaArgs &s = a.s;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
     constexpr int QB = NW * QT * 16;
     const int nqb = (s.Tq + QB - 1) / QB;
     int bh, qb;
@@ -64,9 +64,11 @@ __global__ __launch_bounds__(NW * 64, FOCC) void mla_fwd_kernel(MlaFwdArgs a) {
 
     RowTile<BF, DP, MLA_KT, NT> kt;
     RowTile<BF, DVP, MLA_KT, NT> vt;
+    kt.init(kp, rk, s.dn, krp, rr, s.dr, tid);
+    vt.init(vp, rv, s.dv, vp, 0, 0, tid);
     if (nt > 0) {
-        kt.fetch(kp, rk, s.dn, krp, rr, s.dr, 0, n, tid);
-        vt.fetch(vp, rv, s.dv, vp, 0, 0, 0, n, tid);
+        kt.fetch(0, n);
+        vt.fetch(0, n);
     }
     // queries as operand columns; rows past the sequence read as zero
     Frag<BF> Q[QT][KS];
@@ -91,16 +93,17 @@ __global__ __launch_bounds__(NW * 64, FOCC) void mla_fwd_kernel(MlaFwdArgs a) {
     }
     const float c2 = s.scale * (float)LOG2E;
     if (nt > 0) {
-        kt.stash(Ks[0], LDK, D, 0, n, tid);
-        vt.stash(Vs[0], LDV, s.dv, 0, n, tid);
+        kt.stash(Ks[0], LDK, 0, n);
+        vt.stash(Vs[0], LDV, 0, n);
         lds_barrier();
     }
+    wait_vmem(); // (Q is there: else its first use in the loop waits for the tile in flight)
     const int wlast = min(q0 + QT * 16 - 1 + off, n - 1), wfirst = q0 + off;
     for (int kb = 0; kb < nt; ++kb) {
         const int key0 = kb * MLA_KT;
         if (kb + 1 < nt) {
-            kt.fetch(kp, rk, s.dn, krp, rr, s.dr, key0 + MLA_KT, n, tid);
-            vt.fetch(vp, rv, s.dv, vp, 0, 0, key0 + MLA_KT, n, tid);
+            kt.fetch(key0 + MLA_KT, n);
+            vt.fetch(key0 + MLA_KT, n);
         }
         if (key0 <= wlast && wfirst < n) {
             const S *K = Ks[kb % NB], *V = Vs[kb % NB];
@@ -175,8 +178,8 @@ __global__ __launch_bounds__(NW * 64, FOCC) void mla_fwd_kernel(MlaFwdArgs a) {
         if (kb + 1 < nt) {
             // with two buffers the other one's last readers passed the previous barrier
             if (NB == 1) lds_barrier();
-            kt.stash(Ks[(kb + 1) % NB], LDK, D, key0 + MLA_KT, n, tid);
-            vt.stash(Vs[(kb + 1) % NB], LDV, s.dv, key0 + MLA_KT, n, tid);
+            kt.stash(Ks[(kb + 1) % NB], LDK, key0 + MLA_KT, n);
+            vt.stash(Vs[(kb + 1) % NB], LDV, key0 + MLA_KT, n);
             lds_barrier();
         }
     }

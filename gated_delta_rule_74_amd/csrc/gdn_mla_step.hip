@@ -46,7 +46,7 @@ __global__ __launch_bounds__(256, (DLP <= 256 && MT == 1 ? 2 : 1)) void mla_step
     __shared__ __align__(16) float bias[P::KT];
     __shared__ float Ms[WK][MT * 16], Ss[WK][MT * 16];
     S *T = (S *)smem;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
     const int kw = wave % WK, wr = wave / WK;
     const int rows = a.S * a.H, rb = (rows + MT * 16 - 1) / (MT * 16);
     // eight units (sequence, part) side by side on the eight XCDs, then the
@@ -127,6 +127,7 @@ __global__ __launch_bounds__(256, (DLP <= 256 && MT == 1 ? 2 : 1)) void mla_step
     for (int e = tid; e < P::KT * (P::LD - d); e += P::NT) T[(e / (P::LD - d)) * P::LD + d + e % (P::LD - d)] = S(0);
     const float c2 = a.scale * (float)LOG2E;
     const int all_see = n - a.S + 1; // keys below this are seen by every query
+    wait_vmem(); // (q is there: else its first use in the loop waits for the tile in flight)
     for (int t0 = k0; t0 < k1; t0 += P::KT) {
         lds_barrier();
 #pragma unroll
