@@ -36,6 +36,7 @@ struct MlaArgs {
     const void *q, *k, *kr, *v;
     const int *lens; // [B] keys of each sequence, or null (Tk)
     int B, Tq, Tk, H, Hk, Hr, dn, dr, dv;
+    int pair; // a workgroup takes a long and a short block instead of one
     float scale;
 };
 struct MlaFwdArgs {

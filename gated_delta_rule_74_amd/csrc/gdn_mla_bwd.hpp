@@ -33,24 +33,24 @@ constexpr int MLA_BT = 64; // walked rows per tile
 #ifndef QQT
 #define QQT 2
 #endif
+#ifndef QNW
+#define QNW 8
+#endif
+#ifndef KNW
+#define KNW 4
+#endif
 #ifndef KKT
 #define KKT 2
 #endif
 
-template <bool BF, int DP, int DVP, int NW, int QT>
-__global__ __launch_bounds__(NW * 64, QOCC) void mla_bwd_q_kernel(MlaBwdArgs a) {
-    using S = typename Op<BF>::S;
+// dq of block qb of the queries of head bh, and their delta.
+template <bool BF, int DP, int DVP, int NW, int QT, class S>
+__device__ __forceinline__ void mla_bwd_q_block(const MlaBwdArgs a, int bh, int qb, S *Ks, S *Vs) {
     constexpr int LDK = DP + Op<BF>::PAD, LDV = DVP + Op<BF>::PAD, NT = NW * 64, KS = DP / 32, VS = DVP / 32,
                   MD = DP / 16;
-    __shared__ __align__(16) S Ks[MLA_BT * LDK];
-    __shared__ __align__(16) S Vs[MLA_BT * LDV];
-    const MlaArgs &s = a.s;
+    const MlaArgs s = a.s;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
     constexpr int QB = NW * QT * 16;
-    const int nqb = (s.Tq + QB - 1) / QB;
-    int bh, qb;
-    head_block(blockIdx.x, s.B * s.H, nqb, bh, qb);
-    qb = nqb - 1 - qb; // the last queries walk longest
     const int b = bh / s.H, h = bh % s.H, hk = h / (s.H / s.Hk);
     const int hr = s.Hr > 0 ? h / (s.H / s.Hr) : 0;
     const int D = s.dn + s.dr, off = s.Tk - s.Tq;
@@ -181,20 +181,39 @@ __global__ __launch_bounds__(NW * 64, QOCC) void mla_bwd_q_kernel(MlaBwdArgs a) 
     }
 }
 
-template <bool BF, int DP, int DVP, int NW, int KT>
-__global__ __launch_bounds__(NW * 64, KOCC) void mla_bwd_k_kernel(MlaBwdArgs a) {
+template <bool BF, int DP, int DVP, int NW, int QT>
+__global__ __launch_bounds__(NW * 64, QOCC) void mla_bwd_q_kernel(MlaBwdArgs a) {
     using S = typename Op<BF>::S;
+    __shared__ __align__(16) S Ks[MLA_BT * (DP + Op<BF>::PAD)];
+    __shared__ __align__(16) S Vs[MLA_BT * (DVP + Op<BF>::PAD)];
+    constexpr int QB = NW * QT * 16;
+    const int nqb = (a.s.Tq + QB - 1) / QB, work = a.s.pair ? (nqb + 1) / 2 : nqb;
+    int bh, i;
+    head_block(blockIdx.x, a.s.B * a.s.H, work, bh, i);
+    // the last queries walk longest (a block begins with a barrier, so the tiles may be reused)
+    const int parts = a.s.pair && i < nqb - 1 - i ? 2 : 1;
+#pragma unroll 1
+    for (int p = 0; p < parts; ++p) mla_bwd_q_block<BF, DP, DVP, NW, QT>(a, bh, p ? i : nqb - 1 - i, Ks, Vs);
+}
+
+// x[t][j] += the products of N walked operands with the held ones of tile t.
+template <int N, bool BF, int T>
+__device__ __forceinline__ void times(f32x4 (&x)[T][2], int j, const Frags<BF, N> &f, const Frag<BF> (&held)[T][N]) {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int t = 0; t < T; ++t) x[t][j] = mma8(f.f[k], held[t][k], x[t][j]);
+}
+
+// dk, dkr and dv of block kb of the keys of key head bh.
+template <bool BF, int DP, int DVP, int NW, int KT, class S>
+__device__ __forceinline__ void mla_bwd_k_block(const MlaBwdArgs a, int bh, int kb, S *Qs, S *Gs, float *Ls,
+                                                float *Ds) {
     constexpr int LDQ = DP + Op<BF>::PAD, LDG = DVP + Op<BF>::PAD, NT = NW * 64, KS = DP / 32, VS = DVP / 32,
                   MD = DP / 16, MV = DVP / 16;
-    __shared__ __align__(16) S Qs[MLA_BT * LDQ];
-    __shared__ __align__(16) S Gs[MLA_BT * LDG];
-    __shared__ __align__(16) float Ls[MLA_BT], Ds[MLA_BT];
-    const MlaArgs &s = a.s;
+    const MlaArgs s = a.s;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
     constexpr int KB = NW * KT * 16;
-    const int nkb = (s.Tk + KB - 1) / KB;
-    int bh, kb; // (the first keys walk longest)
-    head_block(blockIdx.x, s.B * s.Hk, nkb, bh, kb);
     const int b = bh / s.Hk, hk = bh % s.Hk, per = s.H / s.Hk;
     const int hr = s.Hr > 0 ? hk / (s.Hk / s.Hr) : 0;
     const int D = s.dn + s.dr, off = s.Tk - s.Tq;
@@ -254,19 +273,6 @@ __global__ __launch_bounds__(NW * 64, KOCC) void mla_bwd_k_kernel(MlaBwdArgs a) 
         for (int v = 0; v < MV; ++v) dV[t][v] = zero4();
     }
     const float c2 = s.scale * (float)LOG2E;
-    // S and dP of 16 walked rows against the wave's keys
-    auto scores = [&](f32x4 (&P)[KT][2], f32x4 (&dP)[KT][2], int j, const Frags<BF, KS> &q, const Frags<BF, VS> &gr) {
-#pragma unroll
-        for (int t = 0; t < KT; ++t) P[t][j] = dP[t][j] = zero4();
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int t = 0; t < KT; ++t) P[t][j] = mma8(q.f[k], K[t][k], P[t][j]);
-#pragma unroll
-        for (int k = 0; k < VS; ++k)
-#pragma unroll
-            for (int t = 0; t < KT; ++t) dP[t][j] = mma8(gr.f[k], V[t][k], dP[t][j]);
-    };
     wait_vmem(); // (as above)
     for (int x = 0; x < total; ++x) {
         const int row0 = (t_lo + x % tiles) * MLA_BT;
@@ -285,21 +291,30 @@ __global__ __launch_bounds__(NW * 64, KOCC) void mla_bwd_k_kernel(MlaBwdArgs a) 
 #pragma unroll 1
         for (int u = 0; u < nu; ++u) {
             f32x4 P[KT][2], dP[KT][2];
+            // operands are requested one group ahead of the products that use them
             Frags<BF, KS> qa, qb;
             Frags<BF, VS> ga, gb;
+#pragma unroll
+            for (int t = 0; t < KT; ++t) P[t][0] = P[t][1] = dP[t][0] = dP[t][1] = zero4();
             qa.rows(Qs, LDQ, 32 * u, lane);
+            in_flight();
             ga.rows(Gs, LDG, 32 * u, lane);
             in_flight();
+            times<KS>(P, 0, qa, K);
+            in_flight();
             qb.rows(Qs, LDQ, 32 * u + 16, lane);
+            in_flight();
+            times<VS>(dP, 0, ga, V);
+            in_flight();
             gb.rows(Gs, LDG, 32 * u + 16, lane);
             in_flight();
-            scores(P, dP, 0, qa, ga);
+            times<KS>(P, 1, qb, K);
             in_flight();
-            constexpr int CV = MV < 4 ? MV : 4, CK = MD % 4 == 0 ? 4 : 3; // operands requested at a time
+            constexpr int CV = 4, CK = MD % 4 == 0 ? 4 : 3; // operands requested at a time
             Frags<BF, CV> vc;
             vc.cols(Gs, LDG, 32 * u, 0, lane);
             in_flight();
-            scores(P, dP, 1, qb, gb);
+            times<VS>(dP, 1, gb, V);
             Frag<BF> pf[KT], sf[KT];
 #pragma unroll
             for (int t = 0; t < KT; ++t) {
@@ -380,17 +395,33 @@ __global__ __launch_bounds__(NW * 64, KOCC) void mla_bwd_k_kernel(MlaBwdArgs a) 
     }
 }
 
+template <bool BF, int DP, int DVP, int NW, int KT>
+__global__ __launch_bounds__(NW * 64, KOCC) void mla_bwd_k_kernel(MlaBwdArgs a) {
+    using S = typename Op<BF>::S;
+    __shared__ __align__(16) S Qs[MLA_BT * (DP + Op<BF>::PAD)];
+    __shared__ __align__(16) S Gs[MLA_BT * (DVP + Op<BF>::PAD)];
+    __shared__ __align__(16) float Ls[MLA_BT], Ds[MLA_BT];
+    constexpr int KB = NW * KT * 16;
+    const int nkb = (a.s.Tk + KB - 1) / KB, work = a.s.pair ? (nkb + 1) / 2 : nkb;
+    int bh, i;
+    head_block(blockIdx.x, a.s.B * a.s.Hk, work, bh, i);
+    // the first keys are seen by the most queries
+    const int parts = a.s.pair && i < nkb - 1 - i ? 2 : 1;
+#pragma unroll 1
+    for (int p = 0; p < parts; ++p) mla_bwd_k_block<BF, DP, DVP, NW, KT>(a, bh, p ? nkb - 1 - i : i, Qs, Gs, Ls, Ds);
+}
+
 template <bool BF, int DP, int DVP> hipError_t mla_bwd_q_run(const MlaBwdArgs &a, hipStream_t st) {
-    constexpr int NW = 4, QT = BF && DP <= 128 ? QQT : 1;
-    const long long nqb = (a.s.Tq + NW * QT * 16 - 1) / (NW * QT * 16);
-    hipLaunchKernelGGL((mla_bwd_q_kernel<BF, DP, DVP, NW, QT>), dim3((unsigned)(nqb * a.s.B * a.s.H)), dim3(NW * 64),
+    constexpr int NW = DP + DVP > 224 ? QNW : 4, QT = BF ? QQT : 1;
+    const long long nqb = (a.s.Tq + NW * QT * 16 - 1) / (NW * QT * 16), work = a.s.pair ? (nqb + 1) / 2 : nqb;
+    hipLaunchKernelGGL((mla_bwd_q_kernel<BF, DP, DVP, NW, QT>), dim3((unsigned)(work * a.s.B * a.s.H)), dim3(NW * 64),
                        0, st, a);
     return hipGetLastError();
 }
 template <bool BF, int DP, int DVP> hipError_t mla_bwd_k_run(const MlaBwdArgs &a, hipStream_t st) {
-    constexpr int NW = 4, KT = BF ? KKT : 1;
-    const long long nkb = (a.s.Tk + NW * KT * 16 - 1) / (NW * KT * 16);
-    hipLaunchKernelGGL((mla_bwd_k_kernel<BF, DP, DVP, NW, KT>), dim3((unsigned)(nkb * a.s.B * a.s.Hk)), dim3(NW * 64),
+    constexpr int NW = DP + DVP > 224 ? KNW : 4, KT = BF ? (DP + DVP > 224 ? KKT : 2) : 1;
+    const long long nkb = (a.s.Tk + NW * KT * 16 - 1) / (NW * KT * 16), work = a.s.pair ? (nkb + 1) / 2 : nkb;
+    hipLaunchKernelGGL((mla_bwd_k_kernel<BF, DP, DVP, NW, KT>), dim3((unsigned)(work * a.s.B * a.s.Hk)), dim3(NW * 64),
                        0, st, a);
     return hipGetLastError();
 }

@@ -29,24 +29,31 @@ constexpr float MLA_RAISE = 8.f; // see above
 #ifndef FOCC
 #define FOCC 2
 #endif
+#ifndef FNW
+#define FNW 8
+#endif
+#ifndef FLDS
+#define FLDS 80
+#endif
 #ifndef FQT
 #define FQT 2
 #endif
-template <bool BF, int DP, int DVP, int NW, int QT>
-__global__ __launch_bounds__(NW * 64, FOCC) void mla_fwd_kernel(MlaFwdArgs a) {
+template <bool BF, int DP, int DVP, int NW, int QT> struct MlaFwdShape {
     using S = typename Op<BF>::S;
-    constexpr int LDK = DP + Op<BF>::PAD, LDV = DVP + Op<BF>::PAD, NT = NW * 64, KS = DP / 32, MV = DVP / 16;
+    static constexpr int LDK = DP + Op<BF>::PAD, LDV = DVP + Op<BF>::PAD, QB = NW * QT * 16;
     // two tiles where a second workgroup still fits the CU's 160 KB beside them
-    constexpr int NB = 2 * MLA_KT * (LDK + LDV) * (int)sizeof(S) <= 80 * 1024 ? 2 : 1;
-    __shared__ __align__(16) S Ks[NB][MLA_KT * LDK];
-    __shared__ __align__(16) S Vs[NB][MLA_KT * LDV];
-    const MlaArgs &s = a.s;
+    static constexpr int NB = 2 * MLA_KT * (LDK + LDV) * (int)sizeof(S) <= (NW == 8 ? FLDS : 80) * 1024 ? 2 : 1;
+
+};
+
+// Block qb of the queries of head bh.
+template <bool BF, int DP, int DVP, int NW, int QT, class S>
+__device__ __forceinline__ void mla_fwd_block(const MlaFwdArgs a, int bh, int qb, S *Kst, S *Vst) {
+    using H = MlaFwdShape<BF, DP, DVP, NW, QT>;
+    constexpr int LDK = H::LDK, LDV = H::LDV, NB = H::NB, NT = NW * 64, KS = DP / 32, MV = DVP / 16;
+    const MlaArgs s = a.s;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
-    constexpr int QB = NW * QT * 16;
-    const int nqb = (s.Tq + QB - 1) / QB;
-    int bh, qb;
-    head_block(blockIdx.x, s.B * s.H, nqb, bh, qb);
-    qb = nqb - 1 - qb; // the last queries walk longest
+    constexpr int QB = H::QB;
     const int b = bh / s.H, h = bh % s.H, hk = h / (s.H / s.Hk);
     const int hr = s.Hr > 0 ? h / (s.H / s.Hr) : 0;
     const int D = s.dn + s.dr, off = s.Tk - s.Tq;
@@ -93,8 +100,8 @@ __global__ __launch_bounds__(NW * 64, FOCC) void mla_fwd_kernel(MlaFwdArgs a) {
     }
     const float c2 = s.scale * (float)LOG2E;
     if (nt > 0) {
-        kt.stash(Ks[0], LDK, 0, n);
-        vt.stash(Vs[0], LDV, 0, n);
+        kt.stash(Kst, LDK, 0, n);
+        vt.stash(Vst, LDV, 0, n);
         lds_barrier();
     }
     wait_vmem(); // (Q is there: else its first use in the loop waits for the tile in flight)
@@ -106,7 +113,7 @@ __global__ __launch_bounds__(NW * 64, FOCC) void mla_fwd_kernel(MlaFwdArgs a) {
             vt.fetch(key0 + MLA_KT, n);
         }
         if (key0 <= wlast && wfirst < n) {
-            const S *K = Ks[kb % NB], *V = Vs[kb % NB];
+            const S *K = Kst + kb % NB * (MLA_KT * LDK), *V = Vst + kb % NB * (MLA_KT * LDV);
             const bool mask = key0 + MLA_KT - 1 > wfirst || key0 + MLA_KT > n;
 #pragma unroll 1
             for (int u = 0; u < MLA_KT / 32; ++u) {
@@ -178,8 +185,8 @@ __global__ __launch_bounds__(NW * 64, FOCC) void mla_fwd_kernel(MlaFwdArgs a) {
         if (kb + 1 < nt) {
             // with two buffers the other one's last readers passed the previous barrier
             if (NB == 1) lds_barrier();
-            kt.stash(Ks[(kb + 1) % NB], LDK, key0 + MLA_KT, n);
-            vt.stash(Vs[(kb + 1) % NB], LDV, key0 + MLA_KT, n);
+            kt.stash(Kst + (kb + 1) % NB * (MLA_KT * LDK), LDK, key0 + MLA_KT, n);
+            vt.stash(Vst + (kb + 1) % NB * (MLA_KT * LDV), LDV, key0 + MLA_KT, n);
             lds_barrier();
         }
     }
@@ -203,10 +210,27 @@ __global__ __launch_bounds__(NW * 64, FOCC) void mla_fwd_kernel(MlaFwdArgs a) {
     }
 }
 
+template <bool BF, int DP, int DVP, int NW, int QT>
+__global__ __launch_bounds__(NW * 64, FOCC) void mla_fwd_kernel(MlaFwdArgs a) {
+    using H = MlaFwdShape<BF, DP, DVP, NW, QT>;
+    __shared__ __align__(16) typename H::S Ks[H::NB * MLA_KT * H::LDK];
+    __shared__ __align__(16) typename H::S Vs[H::NB * MLA_KT * H::LDV];
+    const int nqb = (a.s.Tq + H::QB - 1) / H::QB, work = a.s.pair ? (nqb + 1) / 2 : nqb;
+    int bh, i;
+    head_block(blockIdx.x, a.s.B * a.s.H, work, bh, i);
+    // the last queries walk longest: they come first; in pairs, a long walk with a short one
+    const int parts = a.s.pair && i < nqb - 1 - i ? 2 : 1;
+#pragma unroll 1
+    for (int p = 0; p < parts; ++p) {
+        if (p) lds_barrier(); // (the first block's readers are done)
+        mla_fwd_block<BF, DP, DVP, NW, QT>(a, bh, p ? i : nqb - 1 - i, Ks, Vs);
+    }
+}
+
 template <bool BF, int DP, int DVP> hipError_t mla_fwd_run(const MlaFwdArgs &a, hipStream_t st) {
-    constexpr int NW = 4, QT = BF ? FQT : 1;
-    const long long nqb = (a.s.Tq + NW * QT * 16 - 1) / (NW * QT * 16);
-    hipLaunchKernelGGL((mla_fwd_kernel<BF, DP, DVP, NW, QT>), dim3((unsigned)(nqb * a.s.B * a.s.H)), dim3(NW * 64), 0,
+    constexpr int NW = DP + DVP > 224 ? FNW : 4, QT = BF ? FQT : 1;
+    const long long nqb = (a.s.Tq + NW * QT * 16 - 1) / (NW * QT * 16), work = a.s.pair ? (nqb + 1) / 2 : nqb;
+    hipLaunchKernelGGL((mla_fwd_kernel<BF, DP, DVP, NW, QT>), dim3((unsigned)(work * a.s.B * a.s.H)), dim3(NW * 64), 0,
                        st, a);
     return hipGetLastError();
 }
