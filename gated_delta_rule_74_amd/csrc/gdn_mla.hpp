@@ -36,7 +36,7 @@ struct MlaArgs {
     const void *q, *k, *kr, *v;
     const int *lens; // [B] keys of each sequence, or null (Tk)
     int B, Tq, Tk, H, Hk, Hr, dn, dr, dv;
-    int pair; // a workgroup takes a long and a short block instead of one
+    int pair; // a workgroup takes a long and a short block instead of one (set at the launch)
     float scale;
 };
 struct MlaFwdArgs {
@@ -97,6 +97,32 @@ struct PagePlanArgs {
     int *lens_out, *n_free_out, *granted, *starts, *slots, *positions;
     int N, cols, F, page, cap;
 };
+
+// How the attention launches share out their blocks (MI355X: 256 CUs).
+// A causal walk is as long as its block is late, so two blocks of opposite
+// length make one workgroup (MlaArgs::pair) once that still leaves one for
+// every CU: equal workgroups, no tail (B8 H16 T4096, 56 + 32 | 56: 2.07 ms
+// forward and backward unpaired, 1.94 paired; B2 T512: 60 us unpaired, 66
+// paired). Large blocks (32 rows a wave; eight waves for wide heads) reuse
+// each LDS read twice, small ones (16 rows, four waves) make two to four times
+// as many workgroups: large when, paired, they fill every CU with as many
+// workgroups as it holds (per_cu) (B2 T4096 128 + 64 | 128: 1.04 against
+// 1.28 ms; B1 T2048: 0.43 against 0.27).
+constexpr long long MLA_CUS = 256;
+inline long long mla_blocks(long long n, int rows) { return (n + rows - 1) / rows; }
+inline bool mla_large(long long heads, long long n, int rows, int per_cu) {
+    return heads * mla_blocks(n, rows) >= 2 * MLA_CUS * per_cu;
+}
+// Waves of a large block: eight share a tile where its registers in flight
+// would not fit beside the operands of four (192 | 128: forward 1.59 ms with
+// four, 1.46 with eight; query gradients 2.74 and 2.28 ms, T 16384).
+constexpr int mla_waves(int dp, int dvp) { return dp + dvp > 224 ? 8 : 4; }
+// Workgroups of a launch over blocks of `rows`; sets pair.
+inline long long mla_work(MlaArgs &s, long long heads, long long n, int rows) {
+    const long long blocks = mla_blocks(n, rows);
+    s.pair = heads * blocks >= 2 * MLA_CUS;
+    return heads * (s.pair ? (blocks + 1) / 2 : blocks);
+}
 
 int mla_dq_pad(int d);  // padded query/key width the kernels are built for
 int mla_dv_pad(int d);  // padded value width

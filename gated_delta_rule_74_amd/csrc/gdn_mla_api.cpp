@@ -8,7 +8,6 @@
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
-#include <stdlib.h>
 
 #include "gdn_mla.hpp"
 
@@ -98,7 +97,7 @@ gdn::MlaArgs mla_args(const gdn_mla_shape_t *s, const void *q, const void *k, co
     a.dn = s->dn;
     a.dr = s->dr;
     a.dv = s->dv;
-    a.pair = getenv("GDN_PAIR") ? atoi(getenv("GDN_PAIR")) : 0;
+    a.pair = 0;
     a.scale = s->scale;
     return a;
 }

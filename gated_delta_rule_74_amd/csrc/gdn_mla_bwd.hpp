@@ -23,25 +23,8 @@
 
 namespace gdn {
 
-constexpr int MLA_BT = 64; // walked rows per tile
-#ifndef QOCC
-#define QOCC 2
-#endif
-#ifndef KOCC
-#define KOCC (DP + DVP <= 160 ? 2 : 1)
-#endif
-#ifndef QQT
-#define QQT 2
-#endif
-#ifndef QNW
-#define QNW 8
-#endif
-#ifndef KNW
-#define KNW 4
-#endif
-#ifndef KKT
-#define KKT 2
-#endif
+constexpr int MLA_BT = 64;          // walked rows per tile
+constexpr int MLA_EXACT_TILES = 4; // blocks that see at most so many tiles form delta from the products
 
 // dq of block qb of the queries of head bh, and their delta.
 template <bool BF, int DP, int DVP, int NW, int QT, class S>
@@ -101,15 +84,45 @@ __device__ __forceinline__ void mla_bwd_q_block(const MlaBwdArgs a, int bh, int 
         const float ls = live ? a.lse[((size_t)b * s.Tq + i) * s.H + h] : -INFINITY;
         // a row without keys: every probability is exp2(z - inf) = 0
         lse2[t] = ls == -INFINITY ? INFINITY : ls * (float)LOG2E;
-        if (g == 0 && i < s.Tq) a.delta[((size_t)b * s.H + h) * s.Tq + i] = delta[t];
+    }
+    const float c2 = s.scale * (float)LOG2E;
+    const int wlast = min(q0 + QT * 16 - 1 + off, n - 1), wfirst = q0 + off;
+    // Where a row sees few keys, dP - delta cancels, and do . o with o rounded
+    // to bf16 is not near enough: a first walk forms delta = sum_j P_ij dP_ij
+    // from the products themselves.
+    if (BF && nt <= MLA_EXACT_TILES) {
+        float sum[QT] = {};
+        for (int kb = 0; kb < nt; ++kb) {
+            const int key0 = kb * MLA_BT, next = kb + 1 < nt ? key0 + MLA_BT : 0; // (0: for the walk below)
+            lds_barrier();
+            kt.stash(Ks, LDK, key0, n);
+            vt.stash(Vs, LDV, key0, n);
+            kt.fetch(next, n);
+            vt.fetch(next, n);
+            lds_barrier();
+#pragma unroll 1
+            for (int j = 0; j < MLA_BT / 16; ++j)
+#pragma unroll
+                for (int t = 0; t < QT; ++t) {
+                    f32x4 z = zero4(), dp = zero4();
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) z = mma8(row8(Ks + (16 * j + r) * LDK + 32 * k + 8 * g), Q[t][k], z);
+#pragma unroll
+                    for (int k = 0; k < VS; ++k) dp = mma8(row8(Vs + (16 * j + r) * LDV + 32 * k + 8 * g), G[t][k], dp);
+                    const int lim = min(q0 + 16 * t + r + off, n - 1) - key0 - 16 * j - 4 * g;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sum[t] = fmaf(e <= lim ? exp2_fast(fmaf(z[e], c2, -lse2[t])) : 0.f, dp[e], sum[t]);
+                }
+        }
+#pragma unroll
+        for (int t = 0; t < QT; ++t) delta[t] = sum4g(sum[t]);
     }
     f32x4 dQ[QT][MD];
 #pragma unroll
     for (int t = 0; t < QT; ++t)
 #pragma unroll
         for (int v = 0; v < MD; ++v) dQ[t][v] = zero4();
-    const float c2 = s.scale * (float)LOG2E;
-    const int wlast = min(q0 + QT * 16 - 1 + off, n - 1), wfirst = q0 + off;
     wait_vmem(); // (what is held is there: else its first use in the loop waits for the tile in flight)
     for (int kb = 0; kb < nt; ++kb) {
         const int key0 = kb * MLA_BT;
@@ -173,6 +186,7 @@ __device__ __forceinline__ void mla_bwd_q_block(const MlaBwdArgs a, int bh, int 
     for (int t = 0; t < QT; ++t) {
         const int i = q0 + 16 * t + r;
         if (i >= s.Tq) continue;
+        if (g == 0) a.delta[((size_t)b * s.H + h) * s.Tq + i] = delta[t];
 #pragma unroll
         for (int v = 0; v < MD; ++v) {
             const int c = 16 * v + 4 * g;
@@ -182,7 +196,7 @@ __device__ __forceinline__ void mla_bwd_q_block(const MlaBwdArgs a, int bh, int 
 }
 
 template <bool BF, int DP, int DVP, int NW, int QT>
-__global__ __launch_bounds__(NW * 64, QOCC) void mla_bwd_q_kernel(MlaBwdArgs a) {
+__global__ __launch_bounds__(NW * 64, 2) void mla_bwd_q_kernel(MlaBwdArgs a) {
     using S = typename Op<BF>::S;
     __shared__ __align__(16) S Ks[MLA_BT * (DP + Op<BF>::PAD)];
     __shared__ __align__(16) S Vs[MLA_BT * (DVP + Op<BF>::PAD)];
@@ -395,8 +409,14 @@ __device__ __forceinline__ void mla_bwd_k_block(const MlaBwdArgs a, int bh, int 
     }
 }
 
+// Waves per SIMD: two need the operands and both accumulators of a wave in 256
+// registers (96 | 64: 0.87 ms with two, 1.43 with one at the layer shape);
+// wider pairs of key tiles take up to 512 and run one (192 | 128 with one pair
+// per wave: 3.2 ms at T 16384, one tile and two waves 3.8).
+constexpr int mla_bwd_k_waves(int kt, int dp, int dvp) { return kt == 1 || dp + dvp <= 160 ? 2 : 1; }
+
 template <bool BF, int DP, int DVP, int NW, int KT>
-__global__ __launch_bounds__(NW * 64, KOCC) void mla_bwd_k_kernel(MlaBwdArgs a) {
+__global__ __launch_bounds__(NW * 64, mla_bwd_k_waves(KT, DP, DVP)) void mla_bwd_k_kernel(MlaBwdArgs a) {
     using S = typename Op<BF>::S;
     __shared__ __align__(16) S Qs[MLA_BT * (DP + Op<BF>::PAD)];
     __shared__ __align__(16) S Gs[MLA_BT * (DVP + Op<BF>::PAD)];
@@ -411,19 +431,29 @@ __global__ __launch_bounds__(NW * 64, KOCC) void mla_bwd_k_kernel(MlaBwdArgs a) 
     for (int p = 0; p < parts; ++p) mla_bwd_k_block<BF, DP, DVP, NW, KT>(a, bh, p ? nkb - 1 - i : i, Qs, Gs, Ls, Ds);
 }
 
+template <bool BF, int DP, int DVP, int NW, int QT> hipError_t mla_bwd_q_start(MlaBwdArgs a, hipStream_t st) {
+    const long long work = mla_work(a.s, (long long)a.s.B * a.s.H, a.s.Tq, NW * QT * 16);
+    hipLaunchKernelGGL((mla_bwd_q_kernel<BF, DP, DVP, NW, QT>), dim3((unsigned)work), dim3(NW * 64), 0, st, a);
+    return hipGetLastError();
+}
 template <bool BF, int DP, int DVP> hipError_t mla_bwd_q_run(const MlaBwdArgs &a, hipStream_t st) {
-    constexpr int NW = DP + DVP > 224 ? QNW : 4, QT = BF ? QQT : 1;
-    const long long nqb = (a.s.Tq + NW * QT * 16 - 1) / (NW * QT * 16), work = a.s.pair ? (nqb + 1) / 2 : nqb;
-    hipLaunchKernelGGL((mla_bwd_q_kernel<BF, DP, DVP, NW, QT>), dim3((unsigned)(work * a.s.B * a.s.H)), dim3(NW * 64),
-                       0, st, a);
+    if constexpr (BF) {
+        constexpr int NW = mla_waves(DP, DVP);
+        if (mla_large((long long)a.s.B * a.s.H, a.s.Tq, NW * 32, 8 / NW))
+            return mla_bwd_q_start<BF, DP, DVP, NW, 2>(a, st);
+    }
+    return mla_bwd_q_start<BF, DP, DVP, 4, 1>(a, st);
+}
+template <bool BF, int DP, int DVP, int NW, int KT> hipError_t mla_bwd_k_start(MlaBwdArgs a, hipStream_t st) {
+    const long long work = mla_work(a.s, (long long)a.s.B * a.s.Hk, a.s.Tk, NW * KT * 16);
+    hipLaunchKernelGGL((mla_bwd_k_kernel<BF, DP, DVP, NW, KT>), dim3((unsigned)work), dim3(NW * 64), 0, st, a);
     return hipGetLastError();
 }
 template <bool BF, int DP, int DVP> hipError_t mla_bwd_k_run(const MlaBwdArgs &a, hipStream_t st) {
-    constexpr int NW = DP + DVP > 224 ? KNW : 4, KT = BF ? (DP + DVP > 224 ? KKT : 2) : 1;
-    const long long nkb = (a.s.Tk + NW * KT * 16 - 1) / (NW * KT * 16), work = a.s.pair ? (nkb + 1) / 2 : nkb;
-    hipLaunchKernelGGL((mla_bwd_k_kernel<BF, DP, DVP, NW, KT>), dim3((unsigned)(work * a.s.B * a.s.Hk)), dim3(NW * 64),
-                       0, st, a);
-    return hipGetLastError();
+    if constexpr (BF)
+        if (mla_large((long long)a.s.B * a.s.Hk, a.s.Tk, 128, mla_bwd_k_waves(2, DP, DVP)))
+            return mla_bwd_k_start<BF, DP, DVP, 4, 2>(a, st);
+    return mla_bwd_k_start<BF, DP, DVP, 4, 1>(a, st);
 }
 
 template <bool BF, bool Q, int DP, int DVP> hipError_t mla_bwd_run(const MlaBwdArgs &a, hipStream_t st) {

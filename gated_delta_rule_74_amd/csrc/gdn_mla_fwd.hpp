@@ -26,24 +26,11 @@ namespace gdn {
 constexpr int MLA_KT = 64;      // keys per tile
 constexpr float MLA_RAISE = 8.f; // see above
 
-#ifndef FOCC
-#define FOCC 2
-#endif
-#ifndef FNW
-#define FNW 8
-#endif
-#ifndef FLDS
-#define FLDS 80
-#endif
-#ifndef FQT
-#define FQT 2
-#endif
 template <bool BF, int DP, int DVP, int NW, int QT> struct MlaFwdShape {
     using S = typename Op<BF>::S;
     static constexpr int LDK = DP + Op<BF>::PAD, LDV = DVP + Op<BF>::PAD, QB = NW * QT * 16;
     // two tiles where a second workgroup still fits the CU's 160 KB beside them
-    static constexpr int NB = 2 * MLA_KT * (LDK + LDV) * (int)sizeof(S) <= (NW == 8 ? FLDS : 80) * 1024 ? 2 : 1;
-
+    static constexpr int NB = 2 * MLA_KT * (LDK + LDV) * (int)sizeof(S) <= 80 * 1024 ? 2 : 1;
 };
 
 // Block qb of the queries of head bh.
@@ -211,7 +198,7 @@ __device__ __forceinline__ void mla_fwd_block(const MlaFwdArgs a, int bh, int qb
 }
 
 template <bool BF, int DP, int DVP, int NW, int QT>
-__global__ __launch_bounds__(NW * 64, FOCC) void mla_fwd_kernel(MlaFwdArgs a) {
+__global__ __launch_bounds__(NW * 64, 2) void mla_fwd_kernel(MlaFwdArgs a) {
     using H = MlaFwdShape<BF, DP, DVP, NW, QT>;
     __shared__ __align__(16) typename H::S Ks[H::NB * MLA_KT * H::LDK];
     __shared__ __align__(16) typename H::S Vs[H::NB * MLA_KT * H::LDV];
@@ -227,12 +214,18 @@ __global__ __launch_bounds__(NW * 64, FOCC) void mla_fwd_kernel(MlaFwdArgs a) {
     }
 }
 
-template <bool BF, int DP, int DVP> hipError_t mla_fwd_run(const MlaFwdArgs &a, hipStream_t st) {
-    constexpr int NW = DP + DVP > 224 ? FNW : 4, QT = BF ? FQT : 1;
-    const long long nqb = (a.s.Tq + NW * QT * 16 - 1) / (NW * QT * 16), work = a.s.pair ? (nqb + 1) / 2 : nqb;
-    hipLaunchKernelGGL((mla_fwd_kernel<BF, DP, DVP, NW, QT>), dim3((unsigned)(work * a.s.B * a.s.H)), dim3(NW * 64), 0,
-                       st, a);
+template <bool BF, int DP, int DVP, int NW, int QT> hipError_t mla_fwd_start(MlaFwdArgs a, hipStream_t st) {
+    const long long work = mla_work(a.s, (long long)a.s.B * a.s.H, a.s.Tq, NW * QT * 16);
+    hipLaunchKernelGGL((mla_fwd_kernel<BF, DP, DVP, NW, QT>), dim3((unsigned)work), dim3(NW * 64), 0, st, a);
     return hipGetLastError();
+}
+template <bool BF, int DP, int DVP> hipError_t mla_fwd_run(const MlaFwdArgs &a, hipStream_t st) {
+    if constexpr (BF) {
+        constexpr int NW = mla_waves(DP, DVP);
+        if (mla_large((long long)a.s.B * a.s.H, a.s.Tq, NW * 32, 8 / NW))
+            return mla_fwd_start<BF, DP, DVP, NW, 2>(a, st);
+    }
+    return mla_fwd_start<BF, DP, DVP, 4, 1>(a, st);
 }
 
 template <bool BF> hipError_t mla_fwd_launch(const MlaFwdArgs &a, hipStream_t st) {
