@@ -61,9 +61,9 @@ struct MlaStepArgs {
     float *lse; // may be null
     int N, S, H, dl, dr, pages, page, cols;
     float scale;
-    int mt, nsplit; // blocks of 16 rows per workgroup; parts a sequence may be split into
-    float *part;    // workspace [N][S * H][nsplit][dl] when nsplit > 1
-    float *part_ml; // workspace [N][S * H][nsplit][2]
+    int mt, units;  // blocks of 16 rows per workgroup; shares the cached rows are cut into
+    float *part;    // workspace [2 * units][S * H][dl]
+    float *part_ml; // workspace [2 * units][S * H][2]
 };
 
 struct NormRopeArgs {
@@ -126,11 +126,9 @@ inline long long mla_work(MlaArgs &s, long long heads, long long n, int rows) {
 
 int mla_dq_pad(int d);  // padded query/key width the kernels are built for
 int mla_dv_pad(int d);  // padded value width
-void mla_step_plan(MlaStepArgs &a, bool bf16, int cus); // sets mt and nsplit from the sizes
+void mla_step_plan(MlaStepArgs &a, bool bf16, int cus); // sets mt and units from the sizes
 
 // workgroups of the backward of norm_rope: one row of dw partial sums each
-constexpr int MLA_SPLIT_MAX = 512; // parts of one sequence, at most
-
 int norm_rope_blocks(long long rows, int d);
 
 hipError_t launch_mla_fwd_bf16(const MlaFwdArgs &a, hipStream_t st);
@@ -276,8 +274,15 @@ template <bool BF, int N> struct Frags {
     }
 };
 
-// sixteen bytes of zeros: where a tile's padding columns are loaded from
-__device__ const uint4 mla_zeros = {0u, 0u, 0u, 0u};
+// Sixteen bytes in registers, and their load from global memory (said so
+// explicitly: a pointer picked from several would be read by flat loads, which
+// also hold up LDS waits).
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ u32x4 load16(const void *p) {
+    return *(const __attribute__((address_space(1))) u32x4 *)p;
+}
+// sixteen bytes of zeros: where padding columns and absent rows are loaded from
+__device__ const u32x4 mla_zeros = {0u, 0u, 0u, 0u};
 
 // Rows of a sequence, NR at a time, from global memory over registers into an
 // LDS tile [NR][ld]: columns 0 .. d0 - 1 from x0, d0 .. d0 + d1 - 1 from x1
@@ -291,7 +296,7 @@ template <bool BF, int DP, int NR, int NT> struct RowTile {
     static constexpr int V = Op<BF>::VEC;
     static constexpr int NG = DP / V;
     static constexpr int RP = NT / NG, NIT = (NR + RP - 1) / RP;
-    uint4 r[NIT];
+    u32x4 r[NIT];
     const S *p;
     unsigned rs;
     int j0, c;
@@ -306,18 +311,18 @@ template <bool BF, int DP, int NR, int NT> struct RowTile {
         const S *q = p + (rs ? shift : 0);
 #pragma unroll
         for (int m = 0; m < NIT; ++m)
-            r[m] = *reinterpret_cast<const uint4 *>(q + (size_t)(unsigned)min(row0 + j0 + m * RP, n - 1) * rs);
+            r[m] = load16(q + (size_t)(unsigned)min(row0 + j0 + m * RP, n - 1) * rs);
     }
     __device__ __forceinline__ void stash(S *dst, int ld, int row0, int n) {
         S *q = dst + j0 * ld + c;
         if (row0 + NR > n) { // (the last tile)
 #pragma unroll
             for (int m = 0; m < NIT; ++m)
-                if (row0 + j0 + m * RP >= n) r[m] = uint4{0u, 0u, 0u, 0u};
+                if (row0 + j0 + m * RP >= n) r[m] = u32x4{0u, 0u, 0u, 0u};
         }
 #pragma unroll
         for (int m = 0; m < NIT; ++m)
-            if (j0 + m * RP < NR) *reinterpret_cast<uint4 *>(q + m * RP * ld) = r[m];
+            if (j0 + m * RP < NR) *reinterpret_cast<u32x4 *>(q + m * RP * ld) = r[m];
     }
 };
 

@@ -135,7 +135,9 @@ gdn_status_t check_step(const gdn_mla_step_shape_t *s) {
     if ((double)s->pages * s->page_size >= LIMIT || (double)s->max_pages * s->page_size >= LIMIT ||
         (double)s->N * s->max_pages >= LIMIT)
         return fail(GDN_EINVAL, "cache or table too large");
-    if ((double)s->N * s->S * s->H * (s->dl + s->dr) >= LIMIT) return fail(GDN_EINVAL, "tokens too large");
+    if ((double)s->N * s->S * s->H * (s->dl + s->dr) >= LIMIT ||
+        (double)s->N * s->max_pages * s->page_size / 64 + s->N >= LIMIT / 2)
+        return fail(GDN_EINVAL, "tokens too large");
     if (!(s->scale > 0.f) || !isfinite(s->scale)) return fail(GDN_EINVAL, "scale must be positive and finite");
     return GDN_OK;
 }
@@ -151,14 +153,14 @@ gdn::MlaStepArgs step_args(const gdn_mla_step_shape_t *s) {
     a.cols = s->max_pages;
     a.scale = s->scale;
     if (s->N > 0 && s->S > 0) gdn::mla_step_plan(a, s->dtype == GDN_BF16, CUS);
-    else a.mt = a.nsplit = 1;
+    else a.mt = a.units = 0;
     return a;
 }
 size_t step_part_bytes(const gdn::MlaStepArgs &a) {
-    return a.nsplit > 1 ? align_up((size_t)a.N * a.S * a.H * a.nsplit * a.dl * 4) : 0;
+    return align_up((size_t)2 * a.units * a.S * a.H * a.dl * 4);
 }
 size_t step_ml_bytes(const gdn::MlaStepArgs &a) {
-    return a.nsplit > 1 ? align_up((size_t)a.N * a.S * a.H * a.nsplit * 8) : 0;
+    return align_up((size_t)2 * a.units * a.S * a.H * 8);
 }
 
 constexpr uint32_t ROPE_FLAGS = GDN_ROPE_NORM | GDN_ROPE_INTERLEAVED;
@@ -287,8 +289,7 @@ gdn_status_t gdn_mla_step(const gdn_mla_step_shape_t *s, const void *q, const vo
     if (need && (!ws || ws_bytes < need))
         return fail(GDN_EWORKSPACE, "gdn_mla_step needs %zu bytes of workspace, got %zu", need, ws ? ws_bytes : 0);
     if (need && (uintptr_t)ws % 256) return fail(GDN_EINVAL, "workspace must be 256-byte aligned");
-    const double blocks = ((double)s->S * s->H + 16) * ((double)s->N * a.nsplit + 8) / 16;
-    if (blocks >= LIMIT || (double)rows >= LIMIT) return fail(GDN_EINVAL, "too many tokens");
+    if ((double)rows >= LIMIT) return fail(GDN_EINVAL, "too many tokens");
     a.q = q;
     a.cache = cache;
     a.table = block_table;
@@ -300,7 +301,7 @@ gdn_status_t gdn_mla_step(const gdn_mla_step_shape_t *s, const void *q, const vo
     const bool bf = s->dtype == GDN_BF16;
     hipStream_t strm = (hipStream_t)stream;
     hipError_t he = gdn::bracketed(gdn::K_MLA_STEP, [&] { return gdn::launch_mla_step(a, bf, strm); }, strm);
-    if (he == hipSuccess && a.nsplit > 1)
+    if (he == hipSuccess)
         he = gdn::bracketed(gdn::K_MLA_JOIN, [&] { return gdn::launch_mla_join(a, bf, strm); }, strm);
     return hip_status(he, "gdn_mla_step launch");
 }

@@ -8,8 +8,8 @@
 // 16 * MT of them: a call is bound by the cache's bytes until S * H passes a
 // few hundred.
 //
-// A workgroup takes one sequence, MT * 16 of its queries and one part of its
-// length; the parts are joined by mla_join_kernel. Rows go through registers
+// A workgroup takes MT * 16 queries and an equal share of the cached rows; the
+// parts of a sequence are joined by mla_join_kernel. Rows go through registers
 // (requested one tile ahead, the table entries two) into an LDS tile of
 // 32 * WK rows; the four waves split it into WK groups of 32 keys times
 // 4 / WK groups of latent columns, each wave with a running softmax of its own
@@ -21,97 +21,165 @@
 
 namespace gdn {
 
+constexpr int STEP_TILE = 64; // a part is a whole number of these, two at least
 constexpr float STEP_RAISE = 8.f; // lazy maximum, as in the forward over expanded heads
 
-// Keys [k0, k1) of part `sp` of a sequence of n keys cut into at most nsplit
-// parts of whole tiles. The cut follows the sequence's own length, so a short
-// sequence in a long table is still spread over several workgroups.
-__device__ __forceinline__ int part_keys(int n, int nsplit, int tile) {
-    const int per = (n + nsplit - 1) / nsplit;
-    return max((per + tile - 1) / tile, 2) * tile;
+// How the cached rows are shared out. The sequences' tiles of STEP_TILE rows,
+// end to end, are cut into equal shares, one per workgroup, whatever the single
+// lengths are: a batch of 256 lengths from 0 to 4096 took 51 us with each
+// sequence cut into four equal parts (some CUs had twice the work of others).
+// A workgroup walks the pieces of one or more sequences; a sequence it holds
+// whole it finishes, of others it leaves a part. Only the first and the last
+// piece of a share can be parts, which gives each workgroup two places to
+// leave them.
+__device__ __forceinline__ int seq_rows(const MlaStepArgs &a, int n) {
+    return (int)min((long long)max(a.lens[n], 0), (long long)a.cols * a.page);
 }
+__device__ __forceinline__ int seq_tiles(const MlaStepArgs &a, int n) {
+    return n < a.N ? (int)(((long long)seq_rows(a, n) + STEP_TILE - 1) / STEP_TILE) : 0;
+}
+struct Share {
+    int share; // tiles per workgroup
+    int total; // tiles of all sequences
+    int per, before, mine; // sequences per lane; tiles before this lane's and in them
+};
+// Every wave forms it for itself: lane l sums the sequences l * per .. + per - 1.
+__device__ __forceinline__ Share share_out(const MlaStepArgs &a, int lane) {
+    Share s;
+    s.per = (a.N + 63) / 64;
+    s.mine = 0;
+    for (int i = 0; i < s.per; ++i) s.mine += seq_tiles(a, lane * s.per + i);
+    int x = s.mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int y = __shfl_up(x, o, 64);
+        if (lane >= o) x += y;
+    }
+    s.before = x - s.mine;
+    s.total = __builtin_amdgcn_readlane(x, 63);
+    s.share = max((s.total + a.units - 1) / a.units, 2);
+    return s;
+}
+// where workgroup w leaves its part of a sequence whose tiles begin at `begin`
+__device__ __forceinline__ int part_slot(int w, int begin, int share) { return 2 * w + (begin > w * share ? 1 : 0); }
 
-template <bool BF, int DLP, int WK> struct StepShape {
+// A tile holds KT rows; a wave takes KW of them (32 bf16 rows fill one MFMA's
+// K, 16 fp32 rows four) and DLP / WR columns. Two key groups times two column
+// groups: the scores are formed twice, which leaves a wave few enough
+// registers (112 at 128 + 32 bf16) for four waves per SIMD, and it is those
+// that hide a workgroup's start and end.
+template <bool BF, int DLP, int MT> struct StepShape {
     using S = typename Op<BF>::S;
-    static constexpr int DP = DLP + 64, LD = DP + Op<BF>::PAD, KT = 32 * WK, WR = 4 / WK, MV = DLP / 16 / WR,
-                         KS = DP / 32, NT = 256, V = Op<BF>::VEC, NIT = KT * (DP / V) / NT;
+    static constexpr int WK = 2, WR = 2, KW = BF && DLP <= 256 ? 32 : 16, KT = KW * WK, NJ = KW / 16, NT = 256, V = Op<BF>::VEC,
+                         DP = DLP + 64, LD = DP + Op<BF>::PAD, MV = DLP / 16 / WR, KS = DP / 32,
+                         RP = NT / (DP / V) > 0 ? NT / (DP / V) : 1, NIT = (KT + RP - 1) / RP,
+                         TILE_B = KT * LD * (int)sizeof(S), MERGE_B = 4 * MT * MV * WR * 64 * 4;
+    // queries in registers (bf16), or in LDS where they would take most of them
+    static constexpr bool QL = !BF;
 };
 
-template <bool BF, int DLP, int WK, int MT>
-__global__ __launch_bounds__(256, (DLP <= 256 && MT == 1 ? 2 : 1)) void mla_step_kernel(MlaStepArgs a) {
-    using P = StepShape<BF, DLP, WK>;
-    using S = typename P::S;
-    constexpr int TILE_B = P::KT * P::LD * (int)sizeof(S), MERGE_B = 4 * MT * P::MV * P::WR * 64 * 4;
-    __shared__ __align__(16) unsigned char smem[TILE_B > MERGE_B ? TILE_B : MERGE_B];
-    __shared__ __align__(16) float bias[P::KT];
-    __shared__ float Ms[WK][MT * 16], Ss[WK][MT * 16];
-    S *T = (S *)smem;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
-    const int kw = wave % WK, wr = wave / WK;
-    const int rows = a.S * a.H, rb = (rows + MT * 16 - 1) / (MT * 16);
-    // eight units (sequence, part) side by side on the eight XCDs, then the
-    // same units' next block of queries: it finds the rows in its XCD's L2
-    const int blk = blockIdx.x / (8 * rb), in = blockIdx.x % (8 * rb);
-    const int unit = blk * 8 + in % 8, row0 = (in / 8) * MT * 16;
-    if (unit >= a.N * a.nsplit) return;
-    const int sp = unit / a.N, nq = unit % a.N;
-    const int d = a.dl + a.dr, ng = d / P::V;
-    const long long cap = (long long)a.cols * a.page;
-    const int n = (int)min((long long)max(a.lens[nq], 0), cap);
-    const int per = part_keys(n, a.nsplit, P::KT);
-    const int k0 = min((long long)sp * per, (long long)n), k1 = min(k0 + per, n);
-    if (k0 >= k1 && a.nsplit > 1) return; // (alone, an empty sequence still writes its zeros)
+typedef short short8_t __attribute__((ext_vector_type(8)));
 
-    // table entries of a tile's rows: lane l holds rows l and (of 128) 64 + l
+// One more product over the NJ * 16 rows of an accumulator-ordered operand pair.
+template <int NJ> __device__ __forceinline__ f32x4 mma_rows(const Frag<true> &a, const Frag<true> &b, f32x4 c) {
+    if constexpr (NJ == 2) return mma8(a, b, c);
+    const short8_t x = __builtin_bit_cast(short8_t, a.v), y = __builtin_bit_cast(short8_t, b.v);
+    return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_shufflevector(x, x, 0, 1, 2, 3),
+                                                     __builtin_shufflevector(y, y, 0, 1, 2, 3), c, 0, 0, 0);
+}
+template <int NJ> __device__ __forceinline__ f32x4 mma_rows(const Frag<false> &a, const Frag<false> &b, f32x4 c) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.lo[j], b.lo[j], c, 0, 0, 0);
+    if (NJ == 2) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.hi[j], b.hi[j], c, 0, 0, 0);
+    }
+    return c;
+}
+template <int NJ> __device__ __forceinline__ Frag<true> col_rows(const u16 *X, int ld, int k0, int m0, int lane) {
+    if constexpr (NJ == 2) return col8(X, ld, k0, m0, lane);
+    const short4_t x = operand_tr4(X, ld, k0, m0, lane);
+    return {join8(x, x)};
+}
+template <int NJ> __device__ __forceinline__ Frag<false> col_rows(const float *X, int ld, int k0, int m0, int lane) {
+    const float *p = X + (k0 + 4 * (lane >> 4)) * ld + m0 + (lane & 15);
+    Frag<false> f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f.lo[e] = p[e * ld];
+    if (NJ == 2) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f.hi[e] = p[(16 + e) * ld];
+    }
+    return f;
+}
+
+// Rows [k0, k1e) of sequence nq for the queries from row0 on (k1e may pass its
+// end); slot: where to leave the part, -1: all of the sequence, finish it.
+template <bool BF, int DLP, int MT>
+__device__ __forceinline__ void step_piece(const MlaStepArgs a, int nq, int k0, int k1e, int row0, int slot,
+                                           unsigned char *smem, typename Op<BF>::S *Qs, float *bias, float *Ms,
+                                           float *Ss) {
+    using P = StepShape<BF, DLP, MT>;
+    using S = typename P::S;
+    S *T = (S *)smem;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15,
+              g = lane >> 4;
+    const int kw = wave % P::WK, wr = wave / P::WK, rows = a.S * a.H;
+    const int d = a.dl + a.dr, ng = d / P::V, rp = P::NT / ng;
+    const int n = seq_rows(a, nq), k1 = min(k1e, n);
+
+    // the table entry and the cache row of tile row `lane`, requested two tiles
+    // and known one tile ahead; -1: no row (past the part, or an entry outside
+    // the pool)
     const int *tb = a.table + (size_t)nq * a.cols;
-    constexpr int NSL = P::KT / 64 > 0 ? P::KT / 64 : 1;
-    int pg[NSL];
+    int entry = -1, row = -1;
     auto ask = [&](int t0) {
-#pragma unroll
-        for (int i = 0; i < NSL; ++i) pg[i] = tb[min(t0 + 64 * i + lane, k1 - 1) / a.page];
+        if (lane < P::KT) entry = tb[(unsigned)min(t0 + lane, k1 - 1) / (unsigned)a.page];
     };
-    int slot[NSL]; // row of the cache, -1: none (past the part, or an entry outside the pool)
     auto place = [&](int t0) {
-#pragma unroll
-        for (int i = 0; i < NSL; ++i) {
-            const int pos = t0 + 64 * i + lane;
-            slot[i] = pos < k1 && (unsigned)pg[i] < (unsigned)a.pages ? pg[i] : -1;
-        }
+        const int pos = t0 + lane;
+        row = lane < P::KT && pos < k1 && (unsigned)entry < (unsigned)a.pages
+                  ? entry * a.page + (int)((unsigned)pos % (unsigned)a.page)
+                  : -1;
     };
-    uint4 reg[P::NIT];
-    unsigned long long ok = 0; // bit m: item m lies in a row the part holds
-    auto fetch = [&](int t0) {
-        ok = 0;
+    // a thread loads one 16-byte column of every rp-th row of a tile
+    const int j0 = tid < rp * ng ? tid / ng : P::KT, c0 = (tid % ng) * P::V;
+    u32x4 reg[P::NIT];
+    auto fetch = [&] {
 #pragma unroll
         for (int m = 0; m < P::NIT; ++m) {
-            const int it = tid + m * P::NT, j = it / ng, c = (it % ng) * P::V;
-            int p = __shfl(slot[0], j & 63, 64);
-            if (NSL > 1) p = j < 64 ? p : __shfl(slot[NSL - 1], j & 63, 64);
-            const bool in_tile = j < P::KT && p >= 0;
-            const size_t row = in_tile ? (size_t)p * a.page + (unsigned)(t0 + j) % (unsigned)a.page : 0;
-            reg[m] = *reinterpret_cast<const uint4 *>((const S *)a.cache + row * d + c);
-            ok |= (in_tile ? 1ull : 0ull) << m;
+            const int j = j0 + m * rp, p = __shfl(row, j & 63, 64);
+            // (no row: zeros, chosen by address, so that nothing waits for the load here)
+            const S *src = (const S *)a.cache + (size_t)(unsigned)p * (unsigned)d + c0;
+            reg[m] = load16(j < P::KT && p >= 0 ? src : (const S *)&mla_zeros);
         }
     };
-    const bool any = k0 < k1;
-    if (any) {
-        ask(k0);
-        place(k0);
-        fetch(k0);
-        ask(k0 + P::KT);
-    }
+    ask(k0);
+    place(k0);
+    fetch();
     // queries as operand columns
-    Frag<BF> Q[MT][P::KS];
+    Frag<BF> Q[P::QL ? 1 : MT][P::KS];
     int see[MT]; // keys below this are seen
     const S *qp = (const S *)a.q + (size_t)nq * rows * d;
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
         const int i = row0 + 16 * t + r;
         see[t] = i < rows ? n - a.S + 1 + i / a.H : 0;
+        if constexpr (!P::QL) {
 #pragma unroll
-        for (int k = 0; k < P::KS; ++k) {
-            const int c = 32 * k + 8 * g;
-            Q[t][k] = (i < rows && c < d) ? row8(qp + (size_t)i * d + c) : zero8<BF>();
+            for (int k = 0; k < P::KS; ++k) {
+                const int c = 32 * k + 8 * g;
+                Q[t][k] = (i < rows && c < d) ? row8(qp + (size_t)i * d + c) : zero8<BF>();
+            }
+        }
+    }
+    if constexpr (P::QL) {
+        lds_barrier(); // (the previous piece's readers are done)
+        for (int e = tid; e < MT * 16 * (P::DP / P::V); e += P::NT) {
+            const int i = e / (P::DP / P::V), c = e % (P::DP / P::V) * P::V;
+            uint4 x = uint4{0u, 0u, 0u, 0u};
+            if (row0 + i < rows && c < d) x = *reinterpret_cast<const uint4 *>(qp + (size_t)(row0 + i) * d + c);
+            *reinterpret_cast<uint4 *>(Qs + i * P::LD + c) = x;
         }
     }
     f32x4 O[MT][P::MV];
@@ -123,68 +191,65 @@ __global__ __launch_bounds__(256, (DLP <= 256 && MT == 1 ? 2 : 1)) void mla_step
 #pragma unroll
         for (int v = 0; v < P::MV; ++v) O[t][v] = zero4();
     }
+    lds_barrier(); // (the previous piece's readers are done)
     // columns past d are never stored below: zero once
-    for (int e = tid; e < P::KT * (P::LD - d); e += P::NT) T[(e / (P::LD - d)) * P::LD + d + e % (P::LD - d)] = S(0);
+    for (int e = tid; e < P::TILE_B / 16; e += P::NT) ((u32x4 *)smem)[e] = u32x4{0u, 0u, 0u, 0u};
     const float c2 = a.scale * (float)LOG2E;
-    const int all_see = n - a.S + 1; // keys below this are seen by every query
-    wait_vmem(); // (q is there: else its first use in the loop waits for the tile in flight)
+    wait_vmem(); // (what is held is there: else its first use in the loop waits for the tile in flight)
+    ask(k0 + P::KT);
     for (int t0 = k0; t0 < k1; t0 += P::KT) {
-        lds_barrier();
+        lds_barrier(); // the previous tile's readers (or the zeros' writers) are done
 #pragma unroll
         for (int mm = 0; mm < P::NIT; ++mm) {
-            const int it = tid + mm * P::NT, j = it / ng, c = (it % ng) * P::V;
-            if (j < P::KT)
-                *reinterpret_cast<uint4 *>(T + j * P::LD + c) = (ok >> mm) & 1ull ? reg[mm] : uint4{0u, 0u, 0u, 0u};
+            const int j = j0 + mm * rp;
+            if (j < P::KT) *reinterpret_cast<u32x4 *>(T + j * P::LD + c0) = reg[mm];
         }
-        if (wave == 0) {
-#pragma unroll
-            for (int i = 0; i < NSL; ++i)
-                if (64 * i + lane < P::KT) bias[64 * i + lane] = slot[i] >= 0 ? 0.f : -INFINITY;
-        }
+        if (wave == 0 && lane < P::KT) bias[lane] = row >= 0 ? 0.f : -INFINITY;
         if (t0 + P::KT < k1) {
             place(t0 + P::KT);
-            fetch(t0 + P::KT);
             ask(t0 + 2 * P::KT);
+            fetch();
         }
         lds_barrier();
-        f32x4 X[MT][2];
+        f32x4 X[MT][P::NJ];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) X[t][0] = X[t][1] = zero4();
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int j = 0; j < P::NJ; ++j) X[t][j] = zero4();
+        const S *kr = T + (P::KW * kw + r) * P::LD + 8 * g;
 #pragma unroll
         for (int k = 0; k < P::KS; ++k) {
-            if (32 * k < d) {
+            Frag<BF> qf[MT];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const Frag<BF> kf = row8(T + (32 * kw + 16 * j + r) * P::LD + 32 * k + 8 * g);
+            for (int t = 0; t < MT; ++t) {
+                if constexpr (P::QL) qf[t] = row8(Qs + (16 * t + r) * P::LD + 32 * k + 8 * g);
+                else qf[t] = Q[t][k];
+            }
 #pragma unroll
-                    for (int t = 0; t < MT; ++t) X[t][j] = mma8(kf, Q[t][k], X[t][j]);
-                }
+            for (int j = 0; j < P::NJ; ++j) {
+                const Frag<BF> kf = row8(kr + 16 * j * P::LD + 32 * k);
+#pragma unroll
+                for (int t = 0; t < MT; ++t) X[t][j] = mma8(kf, qf[t], X[t][j]);
             }
         }
         bool raise = false;
         float mx[MT];
-        const f32x4 b0 = *reinterpret_cast<const f32x4 *>(bias + 32 * kw + 4 * g);
-        const f32x4 b1 = *reinterpret_cast<const f32x4 *>(bias + 32 * kw + 16 + 4 * g);
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
+            mx[t] = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                X[t][0][e] = b0[e] == 0.f ? X[t][0][e] * c2 : -INFINITY;
-                X[t][1][e] = b1[e] == 0.f ? X[t][1][e] * c2 : -INFINITY;
+            for (int j = 0; j < P::NJ; ++j) {
+                const f32x4 bj = *reinterpret_cast<const f32x4 *>(bias + P::KW * kw + 16 * j + 4 * g);
+                // Masked on every tile, without a branch: the compiler (ROCm 7.2) leaves out the wait states
+                // between an MFMA and a use of its result behind a conditional block that follows it at once.
+                const int lim = see[t] - t0 - P::KW * kw - 16 * j - 4 * g;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    X[t][j][e] = e < lim && bj[e] == 0.f ? X[t][j][e] * c2 : -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx[t] = fmaxf(mx[t], X[t][j][e]);
             }
-            if (t0 + P::KT > all_see) {
-                const int lim = see[t] - t0 - 32 * kw - 4 * g;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    X[t][0][e] = e < lim ? X[t][0][e] : -INFINITY;
-                    X[t][1][e] = 16 + e < lim ? X[t][1][e] : -INFINITY;
-                }
-            }
-            float x = X[t][0][0];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x = fmaxf(x, fmaxf(X[t][0][e], X[t][1][e]));
-            mx[t] = x;
-            raise |= x > m[t] + STEP_RAISE;
+            raise |= mx[t] > m[t] + STEP_RAISE;
         }
         if (__any(raise)) {
 #pragma unroll
@@ -202,45 +267,41 @@ __global__ __launch_bounds__(256, (DLP <= 256 && MT == 1 ? 2 : 1)) void mla_step
         for (int t = 0; t < MT; ++t) {
             const float mt = m[t] == -INFINITY ? 0.f : m[t];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                X[t][0][e] = exp2_fast(X[t][0][e] - mt);
-                X[t][1][e] = exp2_fast(X[t][1][e] - mt);
+            for (int j = 0; j < P::NJ; ++j) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) X[t][j][e] = exp2_fast(X[t][j][e] - mt);
+                l[t] += (X[t][j][0] + X[t][j][1]) + (X[t][j][2] + X[t][j][3]);
             }
-            const f32x4 sum = X[t][0] + X[t][1];
-            l[t] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            pf[t] = acc8<BF>(X[t][0], X[t][1]);
+            pf[t] = acc8<BF>(X[t][0], X[t][P::NJ - 1]);
         }
 #pragma unroll
         for (int v = 0; v < P::MV; ++v) {
-            const int c = 16 * (wr * P::MV + v);
-            if (c < a.dl) {
-                const Frag<BF> vf = col8(T, P::LD, 32 * kw, c, lane);
+            const Frag<BF> vf = col_rows<P::NJ>(T, P::LD, P::KW * kw, 16 * (wr * P::MV + v), lane);
 #pragma unroll
-                for (int t = 0; t < MT; ++t) O[t][v] = mma8(vf, pf[t], O[t][v]);
-            }
+            for (int t = 0; t < MT; ++t) O[t][v] = mma_rows<P::NJ>(vf, pf[t], O[t][v]);
         }
     }
-    // join the key groups: common maximum, then the rescaled sums one group after the other
+    // join the key groups: common maximum, then the rescaled sums of the second added to the first's
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
         l[t] = sum4g(l[t]);
         if (wr == 0 && g == 0) {
-            Ms[kw][16 * t + r] = m[t];
-            Ss[kw][16 * t + r] = l[t];
+            Ms[kw * MT * 16 + 16 * t + r] = m[t];
+            Ss[kw * MT * 16 + 16 * t + r] = l[t];
         }
     }
     lds_barrier();
     float ml[MT], sl[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-        float mm = Ms[0][16 * t + r];
+        float mm = Ms[16 * t + r];
 #pragma unroll
-        for (int w = 1; w < WK; ++w) mm = fmaxf(mm, Ms[w][16 * t + r]);
+        for (int w = 1; w < P::WK; ++w) mm = fmaxf(mm, Ms[w * MT * 16 + 16 * t + r]);
         float sm = 0.f;
 #pragma unroll
-        for (int w = 0; w < WK; ++w) {
-            const float mw = Ms[w][16 * t + r];
-            sm += mw == -INFINITY ? 0.f : Ss[w][16 * t + r] * exp2_fast(mw - mm);
+        for (int w = 0; w < P::WK; ++w) {
+            const float mw = Ms[w * MT * 16 + 16 * t + r];
+            sm += mw == -INFINITY ? 0.f : Ss[w * MT * 16 + 16 * t + r] * exp2_fast(mw - mm);
         }
         const float f = m[t] == -INFINITY ? 0.f : exp2_fast(m[t] - mm);
 #pragma unroll
@@ -249,130 +310,187 @@ __global__ __launch_bounds__(256, (DLP <= 256 && MT == 1 ? 2 : 1)) void mla_step
         sl[t] = sm;
     }
     f32x4 *X = (f32x4 *)smem + wr * MT * P::MV * 64;
+    if (kw == 1) {
 #pragma unroll
-    for (int w = 1; w < WK; ++w) {
-        if (kw == w) {
+        for (int t = 0; t < MT; ++t)
 #pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int v = 0; v < P::MV; ++v) X[(t * P::MV + v) * 64 + lane] = O[t][v];
-        }
-        lds_barrier();
-        if (kw == 0) {
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int v = 0; v < P::MV; ++v) O[t][v] += X[(t * P::MV + v) * 64 + lane];
-        }
-        if (w + 1 < WK) lds_barrier();
+            for (int v = 0; v < P::MV; ++v) X[(t * P::MV + v) * 64 + lane] = O[t][v];
     }
-    if (kw != 0) return;
+    lds_barrier();
+    if (kw == 1) return;
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
         const int i = row0 + 16 * t + r;
+#pragma unroll
+        for (int v = 0; v < P::MV; ++v) O[t][v] += X[(t * P::MV + v) * 64 + lane];
         if (i >= rows) continue;
-        const size_t row = (size_t)nq * rows + i;
+        const size_t out = (size_t)nq * rows + i;
         const float inv = sl[t] != 0.f ? 1.f / sl[t] : 0.f;
 #pragma unroll
         for (int v = 0; v < P::MV; ++v) {
             const int c = 16 * (wr * P::MV + v) + 4 * g;
             if (c >= a.dl) continue;
-            if (a.nsplit > 1) store4(a.part + (row * a.nsplit + sp) * a.dl + c, O[t][v]);
-            else store4((S *)a.o + row * a.dl + c, O[t][v] * inv);
+            if (slot >= 0) store4(a.part + ((size_t)slot * rows + i) * a.dl + c, O[t][v]);
+            else store4((S *)a.o + out * a.dl + c, O[t][v] * inv);
         }
         if (wr == 0 && g == 0) {
-            if (a.nsplit > 1) {
-                a.part_ml[(row * a.nsplit + sp) * 2] = ml[t];
-                a.part_ml[(row * a.nsplit + sp) * 2 + 1] = sl[t];
+            if (slot >= 0) {
+                *reinterpret_cast<f32x2 *>(a.part_ml + ((size_t)slot * rows + i) * 2) = f32x2{ml[t], sl[t]};
             } else if (a.lse) {
-                a.lse[row] = sl[t] == 0.f ? -INFINITY : (ml[t] + __builtin_amdgcn_logf(sl[t])) * 0.69314718055994531f;
+                a.lse[out] = sl[t] == 0.f ? -INFINITY : (ml[t] + __builtin_amdgcn_logf(sl[t])) * 0.69314718055994531f;
             }
         }
     }
 }
 
-// Joins the parts of a sequence: o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i,
-// in part order within each of 16 interleaved groups, then over the groups. A
-// workgroup takes one query and 64 columns.
-template <bool BF> __global__ __launch_bounds__(256) void mla_join_kernel(MlaStepArgs a, int tile) {
+template <bool BF, int DLP, int MT>
+__global__ __launch_bounds__(256, (DLP <= 128 && MT == 1 ? 3 : 2)) void mla_step_kernel(MlaStepArgs a) {
+    using P = StepShape<BF, DLP, MT>;
+    using S = typename P::S;
+    __shared__ __align__(16) unsigned char smem[P::TILE_B > P::MERGE_B ? P::TILE_B : P::MERGE_B];
+    __shared__ __align__(16) S Qs[P::QL ? MT * 16 * P::LD : 8];
+    __shared__ __align__(16) float bias[P::KT];
+    __shared__ float Ms[P::WK * MT * 16], Ss[P::WK * MT * 16];
+    const int lane = threadIdx.x & 63;
+    const int rows = a.S * a.H, rb = (rows + MT * 16 - 1) / (MT * 16);
+    // eight shares side by side on the eight XCDs, then the same shares' next
+    // block of queries: it finds the rows in its XCD's L2
+    const int blk = blockIdx.x / (8 * rb), in = blockIdx.x % (8 * rb);
+    const int unit = blk * 8 + in % 8, row0 = (in / 8) * MT * 16;
+    const Share sh = share_out(a, lane);
+    const int from = unit * sh.share, to = min(from + sh.share, sh.total);
+    if (unit >= a.units || from >= to) return;
+    // the sequence the share begins in, and where that begins
+    const int owner = __builtin_ctzll(__ballot(sh.before + sh.mine > from));
+    int nq = owner * sh.per, begin = __builtin_amdgcn_readlane(sh.before, owner);
+    for (int at = from; at < to;) {
+        int tiles = seq_tiles(a, nq);
+        while (begin + tiles <= at) {
+            begin += tiles;
+            tiles = seq_tiles(a, ++nq);
+        }
+        const int stop = min(begin + tiles, to);
+        step_piece<BF, DLP, MT>(a, nq, (at - begin) * STEP_TILE, (stop - begin) * STEP_TILE, row0,
+                                at == begin && stop == begin + tiles ? -1 : part_slot(unit, begin, sh.share), smem, Qs,
+                                bias, Ms, Ss);
+        at = stop;
+    }
+}
+// Joins the parts of a sequence: o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i.
+// A workgroup takes one sequence's queries, `mine` at a time; four columns a
+// thread, `groups` threads share the parts (part i with group i % groups, each
+// in order, then the groups in order). Sequences one workgroup finished are
+// done; empty ones get their zeros here.
+template <bool BF> __global__ __launch_bounds__(256) void mla_join_kernel(MlaStepArgs a, int groups) {
     using S = typename Op<BF>::S;
-    __shared__ float red[4], wgt[MLA_SPLIT_MAX];
-    __shared__ __align__(16) f32x4 acc[16][16];
-    const int tid = threadIdx.x, rows = a.S * a.H, lane = tid & 63, wave = tid >> 6;
-    const size_t row = blockIdx.x;
-    const int nq = blockIdx.x / rows;
-    const int n = (int)min((long long)max(a.lens[nq], 0), (long long)a.cols * a.page);
-    const int per = part_keys(n, a.nsplit, tile), cnt = (n + per - 1) / per;
-    const float *ml = a.part_ml + row * a.nsplit * 2;
-    float m = -INFINITY;
-    for (int i = tid; i < cnt; i += 256) m = fmaxf(m, ml[2 * i]);
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-    if (lane == 0) red[wave] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    __syncthreads();
-    float l = 0.f;
-    for (int i = tid; i < cnt; i += 256) {
-        const float w = ml[2 * i] == -INFINITY ? 0.f : exp2_fast(ml[2 * i] - m);
-        wgt[i] = w;
-        l += w * ml[2 * i + 1];
-    }
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) l += __shfl_xor(l, o, 64);
-    if (lane == 0) red[wave] = l;
-    __syncthreads();
-    l = (red[0] + red[1]) + (red[2] + red[3]);
-    const int c = blockIdx.y * 64 + (tid & 15) * 4, grp = tid >> 4;
+    __shared__ __align__(16) f32x4 acc[256];
+    __shared__ float ms[256], ls[256];
+    const int cols = a.dl / 4, tid = threadIdx.x, rows = a.S * a.H;
+    const int wide = min(cols, 256 / groups), per_row = wide * groups, mine = 256 / per_row;
+    const int bpr = (rows + mine - 1) / mine, nq = blockIdx.x / bpr;
+    const int q = tid / per_row, grp = tid % per_row / wide, c = (blockIdx.y * wide + tid % wide) * 4;
+    const int i0 = blockIdx.x % bpr * mine + q;
+    const Share sh = share_out(a, tid & 63);
+    const int lane_of = nq / sh.per, tiles = seq_tiles(a, nq);
+    int begin = __builtin_amdgcn_readlane(sh.before, lane_of);
+    for (int n = lane_of * sh.per; n < nq; ++n) begin += seq_tiles(a, n);
+    const int w0 = begin / sh.share, cnt = tiles ? (begin + tiles - 1) / sh.share - w0 + 1 : 0;
+    if (cnt == 1) return;
+    const bool on = q < mine && i0 < rows && c < a.dl;
+    float m = -INFINITY, l = 0.f;
     f32x4 x = zero4();
-    if (c < a.dl) {
-        const float *p = a.part + row * a.nsplit * a.dl + c;
-        for (int i = grp; i < cnt; i += 16)
-            if (wgt[i] != 0.f) x += *reinterpret_cast<const f32x4 *>(p + (size_t)i * a.dl) * wgt[i];
+    if (on) {
+        // JB parts at a time, all requested before the first is used (past the last: that one again, with weight 0)
+        constexpr int JB = 8;
+        for (int p0 = grp; p0 < cnt; p0 += JB * groups) {
+            f32x4 y[JB];
+            f32x2 s[JB];
+#pragma unroll
+            for (int k = 0; k < JB; ++k) {
+                const int p = min(p0 + k * groups, cnt - 1);
+                const size_t at = (size_t)(p ? 2 * (w0 + p) : part_slot(w0, begin, sh.share)) * rows + i0;
+                s[k] = *reinterpret_cast<const f32x2 *>(a.part_ml + at * 2);
+                y[k] = *reinterpret_cast<const f32x4 *>(a.part + at * a.dl + c);
+            }
+            float mn = m;
+#pragma unroll
+            for (int k = 0; k < JB; ++k) mn = fmaxf(mn, s[k][0]);
+            const float f = m == -INFINITY ? 0.f : exp2_fast(m - mn);
+            x *= f;
+            l *= f;
+            m = mn;
+#pragma unroll
+            for (int k = 0; k < JB; ++k) {
+                const float w = p0 + k * groups >= cnt || s[k][0] == -INFINITY ? 0.f : exp2_fast(s[k][0] - m);
+                l = fmaf(w, s[k][1], l);
+                x += (w != 0.f ? y[k] : zero4()) * w;
+            }
+        }
     }
-    acc[grp][tid & 15] = x;
-    __syncthreads();
-    if (grp == 0 && c < a.dl) {
-        for (int i = 1; i < 16; ++i) x += acc[i][tid & 15];
-        store4((S *)a.o + row * a.dl + c, x * (l != 0.f ? 1.f / l : 0.f));
+    if (groups > 1) {
+        acc[tid] = x;
+        ms[tid] = m;
+        ls[tid] = l;
+        __syncthreads();
+        if (grp != 0) return;
+        float mm = m;
+        for (int k = 1; k < groups; ++k) mm = fmaxf(mm, ms[tid + k * wide]);
+        f32x4 sum = zero4();
+        float sl = 0.f;
+        for (int k = 0; k < groups; ++k) {
+            const float mk = ms[tid + k * wide], w = mk == -INFINITY ? 0.f : exp2_fast(mk - mm);
+            sl += w * ls[tid + k * wide];
+            if (w != 0.f) sum += acc[tid + k * wide] * w;
+        }
+        x = sum;
+        l = sl;
+        m = mm;
     }
-    if (a.lse && blockIdx.y == 0 && tid == 0)
-        a.lse[row] = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
+    if (!on) return;
+    const size_t row = (size_t)nq * rows + i0;
+    store4((S *)a.o + row * a.dl + c, x * (l != 0.f ? 1.f / l : 0.f));
+    if (a.lse && c == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
 }
 
-static int step_class(int dl) { return dl <= 64 ? 64 : dl <= 128 ? 128 : dl <= 256 ? 256 : 512; }
-// key groups: 32 * WK rows per tile, so that a tile in flight fits the registers
-static int step_wk(int dl, bool bf16) { return bf16 ? (dl <= 128 ? 4 : 2) : dl <= 64 ? 4 : dl <= 256 ? 2 : 1; }
+static int step_class(int dl) { return dl <= 64 ? 64 : dl <= 128 ? 128 : dl <= 192 ? 192 : dl <= 256 ? 256 : dl <= 384 ? 384 : 512; }
+
+// workgroups a CU holds at once, by their registers and LDS
+static int step_per_cu(const MlaStepArgs &a, bool bf16) {
+    const int c = step_class(a.dl);
+    if (bf16) return c == 64 ? 5 - a.mt : c == 128 ? 4 - a.mt : 2;
+    return c == 64 ? 4 : c <= 128 ? 3 : c == 192 ? 4 - a.mt : c == 256 ? 3 - a.mt : 1;
+}
 
 void mla_step_plan(MlaStepArgs &a, bool bf16, int cus) {
     const long long rows = (long long)a.S * a.H;
-    // query blocks per workgroup: two where the registers hold them (fp32
-    // operands and the widest latent take twice the registers)
-    a.mt = rows > 16 && bf16 && a.dl <= 256 ? 2 : 1;
-    const long long rb = (rows + 16 * a.mt - 1) / (16 * a.mt), tile = 32 * step_wk(a.dl, bf16);
-    const long long cap = (long long)a.cols * a.page, want = (4LL * cus + a.N * rb - 1) / (a.N * rb);
-    long long n = (cap + 2 * tile - 1) / (2 * tile);
-    if (n > want) n = want;
-    if (n > MLA_SPLIT_MAX) n = MLA_SPLIT_MAX;
-    a.nsplit = n < 1 ? 1 : (int)n;
+    // query blocks per workgroup: two where the registers hold them
+    a.mt = rows > 16 && a.dl <= 256 ? 2 : 1;
+    const long long rb = (rows + 16 * a.mt - 1) / (16 * a.mt), cap = (long long)a.cols * a.page;
+    // as many shares as the chip holds, no share under two tiles
+    long long n = (long long)cus * step_per_cu(a, bf16) / rb;
+    const long long most = a.N * ((cap + 2 * STEP_TILE - 1) / (2 * STEP_TILE));
+    if (n > most) n = most;
+    a.units = n < 1 ? 1 : (int)n;
 }
 
-template <bool BF, int DLP, int WK, int MT> static hipError_t step_run(const MlaStepArgs &a, hipStream_t st) {
-    const long long rb = ((long long)a.S * a.H + MT * 16 - 1) / (MT * 16), units = ((long long)a.N * a.nsplit + 7) / 8 * 8;
-    hipLaunchKernelGGL((mla_step_kernel<BF, DLP, WK, MT>), dim3((unsigned)(units * rb)), dim3(256), 0, st, a);
+template <bool BF, int DLP, int MT> static hipError_t step_run(const MlaStepArgs &a, hipStream_t st) {
+    const long long rb = ((long long)a.S * a.H + MT * 16 - 1) / (MT * 16), units = ((long long)a.units + 7) / 8 * 8;
+    hipLaunchKernelGGL((mla_step_kernel<BF, DLP, MT>), dim3((unsigned)(units * rb)), dim3(256), 0, st, a);
     return hipGetLastError();
 }
-template <bool BF, int DLP, int WK> static hipError_t step_rows(const MlaStepArgs &a, hipStream_t st) {
-    if constexpr (BF && DLP <= 256)
-        if (a.mt == 2) return step_run<BF, DLP, WK, 2>(a, st);
-    return step_run<BF, DLP, WK, 1>(a, st);
+template <bool BF, int DLP> static hipError_t step_rows(const MlaStepArgs &a, hipStream_t st) {
+    if constexpr (DLP <= 256)
+        if (a.mt == 2) return step_run<BF, DLP, 2>(a, st);
+    return step_run<BF, DLP, 1>(a, st);
 }
 template <bool BF> static hipError_t step_launch(const MlaStepArgs &a, hipStream_t st) {
     switch (step_class(a.dl)) {
-    case 64: return step_rows<BF, 64, 4>(a, st);
-    case 128: return step_rows<BF, 128, BF ? 4 : 2>(a, st);
-    case 256: return step_rows<BF, 256, 2>(a, st);
-    default: return step_rows<BF, 512, BF ? 2 : 1>(a, st);
+    case 64: return step_rows<BF, 64>(a, st);
+    case 128: return step_rows<BF, 128>(a, st);
+    case 192: return step_rows<BF, 192>(a, st);
+    case 256: return step_rows<BF, 256>(a, st);
+    case 384: return step_rows<BF, 384>(a, st);
+    default: return step_rows<BF, 512>(a, st);
     }
 }
 hipError_t launch_mla_step(const MlaStepArgs &a, bool bf16, hipStream_t st) {
@@ -380,10 +498,14 @@ hipError_t launch_mla_step(const MlaStepArgs &a, bool bf16, hipStream_t st) {
 }
 
 hipError_t launch_mla_join(const MlaStepArgs &a, bool bf16, hipStream_t st) {
-    const dim3 grid((unsigned)((long long)a.N * a.S * a.H), (unsigned)((a.dl + 63) / 64));
-    const int tile = 32 * step_wk(a.dl, bf16);
-    if (bf16) hipLaunchKernelGGL(mla_join_kernel<true>, grid, dim3(256), 0, st, a, tile);
-    else hipLaunchKernelGGL(mla_join_kernel<false>, grid, dim3(256), 0, st, a, tile);
+    // parts of an average sequence decide how many threads share them
+    int groups = 1;
+    while (groups < 16 && groups * 8 * a.N < a.units) groups *= 2;
+    const int rows = a.S * a.H, cols = a.dl / 4, wide = cols < 256 / groups ? cols : 256 / groups,
+              mine = 256 / (wide * groups);
+    const dim3 grid((unsigned)((long long)a.N * ((rows + mine - 1) / mine)), (unsigned)((cols + wide - 1) / wide));
+    if (bf16) hipLaunchKernelGGL(mla_join_kernel<true>, grid, dim3(256), 0, st, a, groups);
+    else hipLaunchKernelGGL(mla_join_kernel<false>, grid, dim3(256), 0, st, a, groups);
     return hipGetLastError();
 }
 
