@@ -8,7 +8,7 @@
 // interleaved. All of it is bound by the bytes of x and y: a row (token, head)
 // is held by LPR lanes, eight columns each, in one read and one write; the
 // norm's sum goes over those lanes; a pair's other half is read again (it is
-// in L1). The sine and cosine of a token are formed once for all its heads, in
+// in L1, asked for together with the first). The sine and cosine of a token are formed once for all its heads, in
 // LDS. The angle is the product of position and frequency in fp64, reduced to
 // a fraction of a turn there, so that far positions lose nothing.
 #include "gdn_mla.hpp"
@@ -25,8 +25,21 @@ __device__ __forceinline__ float2 turn_of(int pos, double freq) {
     return cs;
 }
 
+// Sum over the lpr lanes of a row (a power of two), every lane gets it: moves
+// inside a 16-lane row, then between rows, none through LDS.
 __device__ __forceinline__ float lanes_sum(float x, int lpr) {
-    for (int o = lpr >> 1; o >= 1; o >>= 1) x += __shfl_xor(x, o, 64);
+    if (lpr >= 2) x += dpp_f<0xB1>(x);   // lane ^ 1
+    if (lpr >= 4) x += dpp_f<0x4E>(x);   // lane ^ 2
+    if (lpr >= 8) x += dpp_f<0x141>(x);  // mirrored within 8
+    if (lpr >= 16) x += dpp_f<0x140>(x); // mirrored within 16
+    if (lpr >= 32) {
+        const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+        x = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+    }
+    if (lpr >= 64) {
+        const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+        x = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+    }
     return x;
 }
 
@@ -36,32 +49,53 @@ __device__ __forceinline__ float lanes_sum(float x, int lpr) {
 template <bool VEC> __device__ __forceinline__ int col_of(int sub, int j, int lpr) {
     return VEC ? sub * 8 + j : sub + lpr * j;
 }
-template <bool BF, bool VEC>
-__device__ __forceinline__ void load_row(const typename Op<BF>::S *x, int sub, int lpr, int d, bool in, float *v) {
+
+// A lane's eight values of a row, as loaded; zeros where there is none.
+template <bool BF, bool VEC> struct Raw {
     using S = typename Op<BF>::S;
-    if constexpr (VEC) {
-        const bool on = in && sub * 8 < d;
-        S s[8];
-        if constexpr (BF) {
-            *reinterpret_cast<uint4 *>(s) = on ? *reinterpret_cast<const uint4 *>(x + sub * 8) : uint4{0u, 0u, 0u, 0u};
+    u32x4 q[VEC ? (BF ? 1 : 2) : 1];
+    S s[VEC ? 1 : 8];
+    __device__ __forceinline__ void load(const S *x, int sub, int lpr, int d, bool in) {
+        if constexpr (VEC) {
+            const void *p = in && sub * 8 < d ? (const void *)(x + sub * 8) : (const void *)&mla_zeros;
+            q[0] = load16(p);
+            if constexpr (!BF) q[1] = load16(in && sub * 8 < d ? (const void *)(x + sub * 8 + 4) : (const void *)&mla_zeros);
         } else {
-            *reinterpret_cast<f32x4 *>(s) = on ? *reinterpret_cast<const f32x4 *>(x + sub * 8) : zero4();
-            *reinterpret_cast<f32x4 *>(s + 4) = on ? *reinterpret_cast<const f32x4 *>(x + sub * 8 + 4) : zero4();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[j] = in && sub + lpr * j < d ? x[sub + lpr * j] : S(0);
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = to_f(s[j]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = in && sub + lpr * j < d ? to_f(x[sub + lpr * j]) : 0.f;
     }
-}
+    __device__ __forceinline__ void values(float *v) const {
+        if constexpr (VEC && BF) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[2 * j] = __uint_as_float(q[0][j] << 16);
+                v[2 * j + 1] = __uint_as_float(q[0][j] & 0xffff0000u);
+            }
+        } else if constexpr (VEC) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(q[j / 4][j % 4]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = to_f(s[j]);
+        }
+    }
+};
 template <bool BF, bool VEC>
 __device__ __forceinline__ void store_row(typename Op<BF>::S *y, int sub, int lpr, int d, const float *v) {
-    using S = typename Op<BF>::S;
     if constexpr (VEC) {
         if (sub * 8 >= d) return;
-        store4(y + sub * 8, f32x4{v[0], v[1], v[2], v[3]});
-        store4(y + sub * 8 + 4, f32x4{v[4], v[5], v[6], v[7]});
+        if constexpr (BF) {
+            uint4 w;
+            w.x = f2bf2(v[0], v[1]);
+            w.y = f2bf2(v[2], v[3]);
+            w.z = f2bf2(v[4], v[5]);
+            w.w = f2bf2(v[6], v[7]);
+            *reinterpret_cast<uint4 *>(y + sub * 8) = w;
+        } else {
+            store4(y + sub * 8, f32x4{v[0], v[1], v[2], v[3]});
+            store4(y + sub * 8 + 4, f32x4{v[4], v[5], v[6], v[7]});
+        }
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -69,103 +103,139 @@ __device__ __forceinline__ void store_row(typename Op<BF>::S *y, int sub, int lp
     }
 }
 
-// The column turned against column c (in the last r ones) and the pair's index.
-__device__ __forceinline__ int partner(int c, int d, int r, bool inter, int &pair, bool &second) {
-    const int p = c - (d - r);
-    if (inter) {
-        pair = p >> 1;
-        second = p & 1;
-        return second ? c - 1 : c + 1;
+// What a lane's columns have to do with the turn: fixed over all rows.
+//   VEC, interleaved: pairs (j, j + 1) of the lane itself, from pair `pair` on;
+//   VEC, halves: the eight columns `other` hold the pairs' other halves;
+//   else: each column by itself (part()).
+template <bool VEC> struct Turn {
+    bool any, second;
+    int other, pair;
+    __device__ __forceinline__ Turn(const NormRopeArgs &a, int sub) {
+        const int c = sub * 8 - (a.d - a.r); // first column, from the first turned one
+        any = VEC && a.r > 0 && c >= 0 && sub * 8 < a.d;
+        second = !a.inter && c >= a.r / 2;
+        pair = a.inter ? c / 2 : second ? c - a.r / 2 : c;
+        other = second ? sub * 8 - a.r / 2 : sub * 8 + a.r / 2;
     }
-    second = p >= r / 2;
-    pair = second ? p - r / 2 : p;
-    return second ? c - r / 2 : c + r / 2;
-}
+    // a single column's partner, pair and half
+    __device__ static __forceinline__ int part(const NormRopeArgs &a, int c, int &pair, bool &second) {
+        const int p = c - (a.d - a.r);
+        if (a.inter) {
+            pair = p >> 1;
+            second = p & 1;
+            return second ? c - 1 : c + 1;
+        }
+        second = p >= a.r / 2;
+        pair = second ? p - a.r / 2 : p;
+        return second ? c - a.r / 2 : c + a.r / 2;
+    }
+};
 
-// v (already scaled by w) turned by sign * angle. raw: the row before scaling
-// by `f` (and w); in: the row exists.
+// v turned by sign * angle (cs: cosine and sine of the token's pairs). o: the
+// other halves of a VEC lane's pairs; raw, f, w: for the rest, the row they are
+// read from and what scales them.
 template <bool BF, bool VEC>
-__device__ __forceinline__ void turn_row(float *v, const typename Op<BF>::S *raw, const float *w, float f, int sub,
-                                         int lpr, int d, int r, bool inter, float sign, const float2 *cs, bool in) {
-    if (r == 0) return;
-    if (VEC && inter) {
+__device__ __forceinline__ void turn_row(const NormRopeArgs &a, const Turn<VEC> &tn, float *v, const float *o,
+                                         const typename Op<BF>::S *raw, float f, const float *w, int sub, int lpr,
+                                         float sign, const float2 *cs, bool in) {
+    if constexpr (VEC) {
+        if (!tn.any) return;
+        if (a.inter) {
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            const int c = sub * 8 + j;
-            if (c < d - r || c >= d) continue;
-            const float2 t = cs[(c - (d - r)) >> 1];
-            const float a = v[j], b = v[j + 1], sn = sign * t.y;
-            v[j] = a * t.x - b * sn;
-            v[j + 1] = b * t.x + a * sn;
+            for (int j = 0; j < 8; j += 2) {
+                const float2 t = cs[tn.pair + j / 2];
+                const float x = v[j], y = v[j + 1], sn = sign * t.y;
+                v[j] = x * t.x - y * sn;
+                v[j + 1] = y * t.x + x * sn;
+            }
+        } else {
+            const float sg = tn.second ? sign : -sign;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 t = cs[tn.pair + j];
+                v[j] = v[j] * t.x + sg * o[j] * t.y;
+            }
         }
         return;
     }
-    if (VEC) {
-        const int c0 = sub * 8;
-        if (c0 < d - r || c0 >= d) return;
-        int pair;
-        bool second;
-        const int pc = partner(c0, d, r, false, pair, second);
-        float o[8];
-        load_row<BF, true>(raw + pc, 0, 1, 8, in, o);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float2 t = cs[pair + j];
-            const float b = o[j] * f * (w ? w[pc + j] : 1.f);
-            v[j] = v[j] * t.x + (second ? sign : -sign) * b * t.y;
-        }
-        return;
-    }
+    if (a.r == 0) return;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const int c = sub + lpr * j;
-        if (c < d - r || c >= d) continue;
+        if (c < a.d - a.r || c >= a.d) continue;
         int pair;
         bool second;
-        const int pc = partner(c, d, r, inter, pair, second);
+        const int pc = Turn<VEC>::part(a, c, pair, second);
         const float b = (in ? to_f(raw[pc]) : 0.f) * f * (w ? w[pc] : 1.f);
         v[j] = v[j] * cs[pair].x + (second ? sign : -sign) * b * cs[pair].y;
     }
 }
 
 // The turns of the tokens of rows row0 .. row0 + rpp - 1.
-__device__ __forceinline__ void fill_turns(const NormRopeArgs &a, float2 *cs, long long row0, int rpp, long long rows) {
+__device__ __forceinline__ void fill_turns(const NormRopeArgs &a, float2 *cs, unsigned row0, unsigned rpp, unsigned rows) {
     const int hp = a.r / 2;
     if (hp == 0) return;
-    const long long t0 = row0 / a.H, t1 = (min(row0 + rpp, rows) - 1) / a.H;
+    const unsigned t0 = row0 / (unsigned)a.H, t1 = (min(row0 + rpp, rows) - 1) / (unsigned)a.H;
     for (int e = threadIdx.x; e < (int)(t1 - t0 + 1) * hp; e += NR_THREADS)
         cs[e] = turn_of(a.pos[t0 + e / hp], a.freqs[e % hp]);
 }
 
-template <bool BF, bool VEC> __global__ __launch_bounds__(NR_THREADS) void norm_rope_kernel(NormRopeArgs a, int lpr) {
+// UN rows per thread and pass, all requested before the first is used: with
+// one row the kernel waits for memory most of the time (B8 T4096 H16 d88 bf16:
+// 130 us with one row in flight per thread).
+template <bool BF, bool VEC, int UN>
+__global__ __launch_bounds__(NR_THREADS) void norm_rope_kernel(NormRopeArgs a, int lpr) {
     using S = typename Op<BF>::S;
-    __shared__ float2 cs[NR_PAIRS];
-    const int rpp = NR_THREADS / lpr, sub = threadIdx.x % lpr, d = a.d;
-    const long long rows = a.M * a.H;
-    for (long long row0 = (long long)blockIdx.x * rpp; row0 < rows; row0 += (long long)gridDim.x * rpp) {
-        const long long row = row0 + threadIdx.x / lpr;
-        const bool in = row < rows;
-        const S *x = (const S *)a.x + (in ? row : 0) * d;
-        float v[8];
-        load_row<BF, VEC>(x, sub, lpr, d, in, v);
-        fill_turns(a, cs, row0, rpp, rows);
-        float inv = 1.f;
-        if (a.norm) {
-            float ss = 0.f;
+    __shared__ float2 cs[2][NR_PAIRS];
+    const int sub = threadIdx.x % lpr, d = a.d;
+    const unsigned slots = NR_THREADS / lpr, rpp = slots * UN;
+    const unsigned rows = (unsigned)(a.M * a.H); // (x has fewer than 2^31 elements)
+    const float per_d = 1.f / (float)d;
+    const Turn<VEC> tn(a, sub);
+    const bool halves = tn.any && !a.inter;
+    float w[8], wo[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
-            inv = 1.f / sqrtf(lanes_sum(ss, lpr) / (float)d + a.eps);
-        }
+    for (int j = 0; j < 8; ++j) {
+        const int c = col_of<VEC>(sub, j, lpr);
+        w[j] = a.w && c < d ? a.w[c] : 1.f;
+        wo[j] = a.w && halves ? a.w[tn.other + j] : 1.f;
+    }
+    int buf = 0;
+    for (unsigned row0 = blockIdx.x * rpp; row0 < rows; row0 += gridDim.x * rpp, buf ^= 1) {
+        const unsigned first = row0 + threadIdx.x / lpr, token0 = row0 / (unsigned)a.H;
+        Raw<BF, VEC> x[UN], o[UN];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = col_of<VEC>(sub, j, lpr);
-            v[j] *= inv * (a.w && c < d ? a.w[c] : 1.f);
+        for (int u = 0; u < UN; ++u) {
+            const unsigned row = first + u * slots;
+            const S *p = (const S *)a.x + (size_t)(row < rows ? row : 0) * d;
+            x[u].load(p, sub, lpr, d, row < rows);
+            if (VEC) o[u].load(p + (halves ? tn.other - sub * 8 : 0), sub, lpr, d, row < rows && halves);
         }
-        __syncthreads();
-        const float2 *t = cs + (a.r / 2) * (int)((in ? row : row0) / a.H - row0 / a.H);
-        turn_row<BF, VEC>(v, x, a.w, inv, sub, lpr, d, a.r, a.inter, 1.f, t, in);
-        if (in) store_row<BF, VEC>((S *)a.y + row * d, sub, lpr, d, v);
-        __syncthreads();
+        fill_turns(a, cs[buf], row0, rpp, rows);
+        __syncthreads(); // (the other table's last readers passed here too)
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            const unsigned row = first + u * slots;
+            const bool in = row < rows;
+            float v[8], ov[8];
+            x[u].values(v);
+            float inv = 1.f;
+            if (a.norm) {
+                float ss = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+                inv = rsqrtf(fmaf(lanes_sum(ss, lpr), per_d, a.eps));
+            }
+            if (VEC) o[u].values(ov);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[j] *= inv * w[j];
+                if (VEC) ov[j] *= inv * wo[j];
+            }
+            const float2 *t = cs[buf] + (a.r / 2) * ((in ? row : row0) / (unsigned)a.H - token0);
+            turn_row<BF, VEC>(a, tn, v, ov, (const S *)a.x + (size_t)(in ? row : 0) * d, inv, a.w, sub, lpr, 1.f, t, in);
+            if (in) store_row<BF, VEC>((S *)a.y + (size_t)row * d, sub, lpr, d, v);
+        }
     }
 }
 
@@ -174,44 +244,67 @@ template <bool BF, bool VEC> __global__ __launch_bounds__(NR_THREADS) void norm_
 // A thread keeps the same columns over all its rows and so sums its part of dw
 // in registers; the parts of a workgroup's row slots are added in slot order,
 // those of the workgroups by norm_sum_kernel: a fixed order throughout.
-template <bool BF, bool VEC> __global__ __launch_bounds__(NR_THREADS) void norm_rope_bwd_kernel(NormRopeArgs a, int lpr) {
+template <bool BF, bool VEC, int UN>
+__global__ __launch_bounds__(NR_THREADS) void norm_rope_bwd_kernel(NormRopeArgs a, int lpr) {
     using S = typename Op<BF>::S;
-    __shared__ float2 cs[NR_PAIRS];
+    __shared__ float2 cs[2][NR_PAIRS];
     __shared__ float red[NR_THREADS * 8];
-    const int rpp = NR_THREADS / lpr, sub = threadIdx.x % lpr, d = a.d;
-    const long long rows = a.M * a.H;
-    float dw[8] = {};
-    for (long long row0 = (long long)blockIdx.x * rpp; row0 < rows; row0 += (long long)gridDim.x * rpp) {
-        const long long row = row0 + threadIdx.x / lpr;
-        const bool in = row < rows;
-        const S *dy = (const S *)a.dy + (in ? row : 0) * d;
-        float v[8], x[8] = {};
-        load_row<BF, VEC>(dy, sub, lpr, d, in, v);
-        if (a.norm) load_row<BF, VEC>((const S *)a.x + (in ? row : 0) * d, sub, lpr, d, in, x);
-        fill_turns(a, cs, row0, rpp, rows);
-        __syncthreads();
-        const float2 *t = cs + (a.r / 2) * (int)((in ? row : row0) / a.H - row0 / a.H);
-        turn_row<BF, VEC>(v, dy, nullptr, 1.f, sub, lpr, d, a.r, a.inter, -1.f, t, in);
-        if (a.norm) {
-            float ss = 0.f;
+    const int sub = threadIdx.x % lpr, d = a.d;
+    const unsigned slots = NR_THREADS / lpr, rpp = slots * UN;
+    const unsigned rows = (unsigned)(a.M * a.H); // (x has fewer than 2^31 elements)
+    const float per_d = 1.f / (float)d;
+    const Turn<VEC> tn(a, sub);
+    const bool halves = tn.any && !a.inter;
+    float w[8], dw[8] = {};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-            const float inv = 1.f / sqrtf(lanes_sum(ss, lpr) / (float)d + a.eps);
-            float dot = 0.f;
+    for (int j = 0; j < 8; ++j) {
+        const int c = col_of<VEC>(sub, j, lpr);
+        w[j] = a.w && c < d ? a.w[c] : 1.f;
+    }
+    int buf = 0;
+    for (unsigned row0 = blockIdx.x * rpp; row0 < rows; row0 += gridDim.x * rpp, buf ^= 1) {
+        const unsigned first = row0 + threadIdx.x / lpr, token0 = row0 / (unsigned)a.H;
+        Raw<BF, VEC> g[UN], o[UN], x[UN];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int c = col_of<VEC>(sub, j, lpr);
-                x[j] *= inv;
-                dw[j] = fmaf(v[j], x[j], dw[j]);
-                v[j] *= a.w && c < d ? a.w[c] : 1.f;
-                dot = fmaf(v[j], x[j], dot);
-            }
-            dot = lanes_sum(dot, lpr) / (float)d;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = inv * (v[j] - x[j] * dot);
+        for (int u = 0; u < UN; ++u) {
+            const unsigned row = first + u * slots;
+            const size_t at = (size_t)(row < rows ? row : 0) * d;
+            const S *p = (const S *)a.dy + at;
+            g[u].load(p, sub, lpr, d, row < rows);
+            if (VEC) o[u].load(p + (halves ? tn.other - sub * 8 : 0), sub, lpr, d, row < rows && halves);
+            if (a.norm) x[u].load((const S *)a.x + at, sub, lpr, d, row < rows);
         }
-        if (in) store_row<BF, VEC>((S *)a.y + row * d, sub, lpr, d, v);
+        fill_turns(a, cs[buf], row0, rpp, rows);
         __syncthreads();
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            const unsigned row = first + u * slots;
+            const bool in = row < rows;
+            float v[8], ov[8];
+            g[u].values(v);
+            if (VEC) o[u].values(ov);
+            const float2 *t = cs[buf] + (a.r / 2) * ((in ? row : row0) / (unsigned)a.H - token0);
+            turn_row<BF, VEC>(a, tn, v, ov, (const S *)a.dy + (size_t)(in ? row : 0) * d, 1.f, nullptr, sub, lpr, -1.f, t, in);
+            if (a.norm) {
+                float xh[8], ss = 0.f;
+                x[u].values(xh);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) ss = fmaf(xh[j], xh[j], ss);
+                const float inv = rsqrtf(fmaf(lanes_sum(ss, lpr), per_d, a.eps));
+                float dot = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    xh[j] *= inv;
+                    dw[j] = fmaf(v[j], xh[j], dw[j]);
+                    v[j] *= w[j];
+                    dot = fmaf(v[j], xh[j], dot);
+                }
+                dot = lanes_sum(dot, lpr) * per_d;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = inv * (v[j] - xh[j] * dot);
+            }
+            if (in) store_row<BF, VEC>((S *)a.y + (size_t)row * d, sub, lpr, d, v);
+        }
     }
     if (!a.dw) return;
 #pragma unroll
@@ -220,25 +313,32 @@ template <bool BF, bool VEC> __global__ __launch_bounds__(NR_THREADS) void norm_
     for (int c = threadIdx.x; c < d; c += NR_THREADS) {
         const int sl = VEC ? c / 8 : c % lpr, j = VEC ? c % 8 : c / lpr;
         float x = 0.f;
-        for (int k = 0; k < rpp; ++k) x += red[(k * lpr + sl) * 8 + j];
+        for (unsigned k = 0; k < slots; ++k) x += red[(k * lpr + sl) * 8 + j];
         a.dw_part[(size_t)blockIdx.x * d + c] = x;
     }
 }
 
-// dw[c] = sum of the workgroups' parts; a workgroup takes 16 columns, 16
-// threads along the parts of each, in a fixed order.
+// dw[c] = sum of the workgroups' parts, in a fixed order: a workgroup takes
+// four columns, thread t the parts t, t + 256, ..., then the threads in halves.
 __global__ __launch_bounds__(256) void norm_sum_kernel(NormRopeArgs a) {
-    __shared__ float red[16][17];
-    const int c = blockIdx.x * 16 + (threadIdx.x & 15), k = threadIdx.x >> 4;
-    float x = 0.f;
-    if (c < a.d)
-        for (int b = k; b < a.nblk; b += 16) x += a.dw_part[(size_t)b * a.d + c];
-    red[k][threadIdx.x & 15] = x;
-    __syncthreads();
-    if (k == 0 && c < a.d) {
-        for (int i = 1; i < 16; ++i) x += red[i][threadIdx.x];
-        a.dw[c] = x;
+    __shared__ __align__(16) float red[256][4];
+    const int c0 = blockIdx.x * 4, t = threadIdx.x;
+    float x[4] = {};
+    for (int b = t; b < a.nblk; b += 256) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (c0 + k < a.d) x[k] += a.dw_part[(size_t)b * a.d + c0 + k];
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) red[t][k] = x[k];
+    for (int o = 128; o >= 1; o >>= 1) {
+        __syncthreads();
+        if (t < o) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) red[t][k] += red[t + o][k];
+        }
+    }
+    if (t < 4 && c0 + t < a.d) a.dw[c0 + t] = red[0][t];
 }
 
 static int lanes_per_row(int d) {
@@ -250,85 +350,117 @@ static int lanes_per_row(int d) {
 static bool row_vectors(int d, int r, int inter) {
     return d % 8 == 0 && (r == 0 || inter || (r % 16 == 0 && (d - r) % 8 == 0));
 }
-static long long passes(long long rows, int d) {
-    const int rpp = NR_THREADS / lanes_per_row(d);
+static long long passes(long long rows, int d, int un) {
+    const int rpp = NR_THREADS / lanes_per_row(d) * un;
     return (rows + rpp - 1) / rpp;
 }
+// Rows per thread: four once that still leaves a workgroup for every CU and
+// the turns of a pass's tokens fit the table.
+static int rows_per_thread(const NormRopeArgs &a, bool vec) {
+    const int rpp = NR_THREADS / lanes_per_row(a.d) * 4;
+    const long long tokens = (rpp - 1) / a.H + 2;
+    return vec && tokens * (a.r / 2) <= NR_PAIRS && passes(a.M * a.H, a.d, 4) >= 256 ? 4 : 1;
+}
 int norm_rope_blocks(long long rows, int d) {
-    const long long p = passes(rows, d);
+    const long long p = passes(rows, d, 1);
     return p < 1024 ? (int)p : 1024;
 }
 
-hipError_t launch_norm_rope(const NormRopeArgs &a, bool bf16, hipStream_t st) {
+template <bool BF> static hipError_t norm_launch(const NormRopeArgs &a, bool back, unsigned grid, hipStream_t st) {
     const int lpr = lanes_per_row(a.d);
-    const long long p = passes(a.M * a.H, a.d);
-    const dim3 grid((unsigned)(p < 16384 ? p : 16384));
     const bool vec = row_vectors(a.d, a.r, a.inter);
-    if (bf16 && vec) hipLaunchKernelGGL((norm_rope_kernel<true, true>), grid, dim3(NR_THREADS), 0, st, a, lpr);
-    else if (bf16) hipLaunchKernelGGL((norm_rope_kernel<true, false>), grid, dim3(NR_THREADS), 0, st, a, lpr);
-    else if (vec) hipLaunchKernelGGL((norm_rope_kernel<false, true>), grid, dim3(NR_THREADS), 0, st, a, lpr);
-    else hipLaunchKernelGGL((norm_rope_kernel<false, false>), grid, dim3(NR_THREADS), 0, st, a, lpr);
+    const dim3 g(grid), t(NR_THREADS);
+    if (vec && rows_per_thread(a, vec) == 4) {
+        if (back) hipLaunchKernelGGL((norm_rope_bwd_kernel<BF, true, 4>), g, t, 0, st, a, lpr);
+        else hipLaunchKernelGGL((norm_rope_kernel<BF, true, 4>), g, t, 0, st, a, lpr);
+    } else if (vec) {
+        if (back) hipLaunchKernelGGL((norm_rope_bwd_kernel<BF, true, 1>), g, t, 0, st, a, lpr);
+        else hipLaunchKernelGGL((norm_rope_kernel<BF, true, 1>), g, t, 0, st, a, lpr);
+    } else {
+        if (back) hipLaunchKernelGGL((norm_rope_bwd_kernel<BF, false, 1>), g, t, 0, st, a, lpr);
+        else hipLaunchKernelGGL((norm_rope_kernel<BF, false, 1>), g, t, 0, st, a, lpr);
+    }
     return hipGetLastError();
+}
+hipError_t launch_norm_rope(const NormRopeArgs &a, bool bf16, hipStream_t st) {
+    const long long p = passes(a.M * a.H, a.d, rows_per_thread(a, row_vectors(a.d, a.r, a.inter)));
+    const unsigned grid = (unsigned)(p < 16384 ? p : 16384);
+    return bf16 ? norm_launch<true>(a, false, grid, st) : norm_launch<false>(a, false, grid, st);
 }
 hipError_t launch_norm_rope_bwd(const NormRopeArgs &a, bool bf16, hipStream_t st) {
-    const int lpr = lanes_per_row(a.d);
-    const dim3 grid((unsigned)a.nblk);
-    const bool vec = row_vectors(a.d, a.r, a.inter);
-    if (bf16 && vec) hipLaunchKernelGGL((norm_rope_bwd_kernel<true, true>), grid, dim3(NR_THREADS), 0, st, a, lpr);
-    else if (bf16) hipLaunchKernelGGL((norm_rope_bwd_kernel<true, false>), grid, dim3(NR_THREADS), 0, st, a, lpr);
-    else if (vec) hipLaunchKernelGGL((norm_rope_bwd_kernel<false, true>), grid, dim3(NR_THREADS), 0, st, a, lpr);
-    else hipLaunchKernelGGL((norm_rope_bwd_kernel<false, false>), grid, dim3(NR_THREADS), 0, st, a, lpr);
-    return hipGetLastError();
+    return bf16 ? norm_launch<true>(a, true, (unsigned)a.nblk, st) : norm_launch<false>(a, true, (unsigned)a.nblk, st);
 }
 hipError_t launch_norm_sum(const NormRopeArgs &a, hipStream_t st) {
-    hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((a.d + 15) / 16)), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(norm_sum_kernel, dim3((unsigned)((a.d + 3) / 4)), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 
 // A new token's cache row: its latent normalised, its rotary key turned, at
-// the slot the plan gave it. One group of LPR lanes per token; each pair's
-// turn is needed once, so it is formed where it is used. Slots outside the
-// pool (-1: none) are skipped.
-template <bool BF> __global__ __launch_bounds__(NR_THREADS) void mla_write_kernel(MlaWriteArgs a, int lpr) {
+// the slot the plan gave it. A group of LPR lanes takes the latents of UN
+// tokens, requested together; the pairs of the workgroup's tokens are shared
+// by all its threads (each pair's turn is needed once, so it is formed where
+// it is used). Slots outside the pool (-1: none) are skipped. Bound by the
+// rows' bytes.
+template <bool BF, int UN> __global__ __launch_bounds__(NR_THREADS) void mla_write_kernel(MlaWriteArgs a, int lpr) {
     using S = typename Op<BF>::S;
-    const int sub = threadIdx.x % lpr;
-    const long long i = (long long)blockIdx.x * (NR_THREADS / lpr) + threadIdx.x / lpr;
-    const int slot = i < a.n ? a.slots[i] : -1;
-    const bool in = slot >= 0 && slot < a.n_slots; // (the whole group takes part in the sum below)
-    float v[8];
-    load_row<BF, true>((const S *)a.c + (in ? i : 0) * a.dl, sub, lpr, a.dl, in, v);
-    float inv = 1.f;
-    if (a.norm) {
-        float ss = 0.f;
+    const int slots = NR_THREADS / lpr, sub = threadIdx.x % lpr, d = a.dl + a.dr, hp = a.dr / 2;
+    const int i0 = blockIdx.x * slots * UN, first = i0 + threadIdx.x / lpr;
+    Raw<BF, true> c[UN];
+    int slot[UN];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
-        inv = 1.f / sqrtf(lanes_sum(ss, lpr) / (float)a.dl + a.eps);
+    for (int u = 0; u < UN; ++u) {
+        const int i = first + u * slots;
+        slot[u] = i < a.n ? a.slots[i] : -1;
+        if (slot[u] >= a.n_slots) slot[u] = -1;
+        c[u].load((const S *)a.c + (size_t)(i < a.n ? i : 0) * a.dl, sub, lpr, a.dl, i < a.n);
     }
-    if (!in) return;
-    S *row = (S *)a.cache + (size_t)slot * (a.dl + a.dr);
-    if (sub * 8 < a.dl) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= inv * (a.w ? a.w[sub * 8 + j] : 1.f);
-        store_row<BF, true>(row, sub, lpr, a.dl, v);
-    }
-    const S *kr = (const S *)a.kr + i * a.dr;
-    const int hp = a.dr / 2;
-    for (int p = sub; p < hp; p += lpr) {
+    for (int e = threadIdx.x; e < slots * UN * hp; e += NR_THREADS) {
+        const int i = i0 + e / hp;
+        if (i >= a.n) break;
+        const int at = a.slots[i], p = e % hp;
         const int ca = a.inter ? 2 * p : p, cb = a.inter ? 2 * p + 1 : p + hp;
+        const S *kr = (const S *)a.kr + (size_t)i * a.dr;
         const float x = to_f(kr[ca]), y = to_f(kr[cb]);
         const float2 t = a.freqs ? turn_of(a.pos[i], a.freqs[p]) : float2{1.f, 0.f};
-        row[a.dl + ca] = from_f<BF>(x * t.x - y * t.y);
-        row[a.dl + cb] = from_f<BF>(y * t.x + x * t.y);
+        if (at < 0 || at >= a.n_slots) continue;
+        S *row = (S *)a.cache + (size_t)at * d + a.dl;
+        row[ca] = from_f<BF>(x * t.x - y * t.y);
+        row[cb] = from_f<BF>(y * t.x + x * t.y);
+    }
+    float w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = a.w && sub * 8 < a.dl ? a.w[sub * 8 + j] : 1.f;
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+        float v[8];
+        c[u].values(v);
+        float inv = 1.f;
+        if (a.norm) {
+            float ss = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+            inv = rsqrtf(fmaf(lanes_sum(ss, lpr), 1.f / (float)a.dl, a.eps));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= inv * w[j];
+        if (slot[u] >= 0) store_row<BF, true>((S *)a.cache + (size_t)slot[u] * d, sub, lpr, a.dl, v);
     }
 }
 
+template <bool BF> static void write_launch(const MlaWriteArgs &a, hipStream_t st) {
+    const int lpr = lanes_per_row(a.dl);
+    const long long per = NR_THREADS / lpr;
+    // four tokens per lane group once that leaves a workgroup for every CU
+    if ((a.n + 4 * per - 1) / (4 * per) >= 256)
+        hipLaunchKernelGGL((mla_write_kernel<BF, 4>), dim3((unsigned)((a.n + 4 * per - 1) / (4 * per))),
+                           dim3(NR_THREADS), 0, st, a, lpr);
+    else
+        hipLaunchKernelGGL((mla_write_kernel<BF, 1>), dim3((unsigned)((a.n + per - 1) / per)), dim3(NR_THREADS), 0, st,
+                           a, lpr);
+}
 hipError_t launch_mla_write(const MlaWriteArgs &a, bool bf16, hipStream_t st) {
-    int lpr = lanes_per_row(a.dl);
-    if (lpr < 8) lpr = 8; // (narrow latents: the lanes share the pairs)
-    const int per = NR_THREADS / lpr;
-    const dim3 grid((unsigned)((a.n + per - 1) / per));
-    if (bf16) hipLaunchKernelGGL(mla_write_kernel<true>, grid, dim3(NR_THREADS), 0, st, a, lpr);
-    else hipLaunchKernelGGL(mla_write_kernel<false>, grid, dim3(NR_THREADS), 0, st, a, lpr);
+    if (bf16) write_launch<true>(a, st);
+    else write_launch<false>(a, st);
     return hipGetLastError();
 }
 

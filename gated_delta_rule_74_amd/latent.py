@@ -10,10 +10,28 @@ import ctypes
 
 import torch
 
-from . import MlaShape, MlaStepShape, _bytes, _check, _dtype_code, _need, _p, _stream, lib
+from . import MlaShape, MlaStepShape, _bytes, _check, _dtype_code, _need as _explain, lib
 
 ROPE_NORM, ROPE_INTERLEAVED = 1, 2
 _HERE = contextlib.nullcontext()
+
+
+def _need(t, name, dtype=None, shape=None, device=None):
+    """The package's tensor check; the usual case (all is well) in a few
+    comparisons, since a decode step makes dozens of them."""
+    if (t is None or (type(t) is torch.Tensor and t.is_cuda and (dtype is None or t.dtype is dtype)
+                      and (shape is None or t.shape == shape) and (device is None or t.device == device)
+                      and t.is_contiguous())):
+        return
+    _explain(t, name, dtype, shape, device)
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _on(dev):
