@@ -124,8 +124,11 @@ inline long long mla_work(MlaArgs &s, long long heads, long long n, int rows) {
     return heads * (s.pair ? (blocks + 1) / 2 : blocks);
 }
 
-int mla_dq_pad(int d);  // padded query/key width the kernels are built for
-int mla_dv_pad(int d);  // padded value width
+// Padded widths the attention kernels are built for: queries and keys, values.
+struct MlaPad {
+    int d, dv;
+};
+MlaPad mla_pad(const MlaArgs &s);
 void mla_step_plan(MlaStepArgs &a, bool bf16, int cus); // sets mt and units from the sizes
 
 // workgroups of the backward of norm_rope: one row of dw partial sums each

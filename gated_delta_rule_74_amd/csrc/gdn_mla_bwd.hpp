@@ -324,7 +324,7 @@ __device__ __forceinline__ void mla_bwd_k_block(const MlaBwdArgs a, int bh, int 
             in_flight();
             times<KS>(P, 1, qb, K);
             in_flight();
-            constexpr int CV = 4, CK = MD % 4 == 0 ? 4 : 3; // operands requested at a time
+            constexpr int CV = MV < 4 ? MV : 4, CK = MD < 3 ? MD : MD % 4 == 0 ? 4 : 3; // operands requested at a time
             Frags<BF, CV> vc;
             vc.cols(Gs, LDG, 32 * u, 0, lane);
             in_flight();
@@ -461,8 +461,10 @@ template <bool BF, bool Q, int DP, int DVP> hipError_t mla_bwd_run(const MlaBwdA
     else return mla_bwd_k_run<BF, DP, DVP>(a, st);
 }
 template <bool BF, bool Q> hipError_t mla_bwd_launch(const MlaBwdArgs &a, hipStream_t st) {
-    const int D = mla_dq_pad(a.s.dn + a.s.dr);
-    if (mla_dv_pad(a.s.dv) == 64) {
+    const MlaPad pad = mla_pad(a.s);
+    const int D = pad.d;
+    if (D == 32) return mla_bwd_run<BF, Q, 32, 32>(a, st);
+    if (pad.dv == 64) {
         if (D == 64) return mla_bwd_run<BF, Q, 64, 64>(a, st);
         if (D == 96) return mla_bwd_run<BF, Q, 96, 64>(a, st);
         if (D == 128) return mla_bwd_run<BF, Q, 128, 64>(a, st);

@@ -229,8 +229,10 @@ template <bool BF, int DP, int DVP> hipError_t mla_fwd_run(const MlaFwdArgs &a, 
 }
 
 template <bool BF> hipError_t mla_fwd_launch(const MlaFwdArgs &a, hipStream_t st) {
-    const int D = mla_dq_pad(a.s.dn + a.s.dr);
-    if (mla_dv_pad(a.s.dv) == 64) {
+    const MlaPad pad = mla_pad(a.s);
+    const int D = pad.d;
+    if (D == 32) return mla_fwd_run<BF, 32, 32>(a, st);
+    if (pad.dv == 64) {
         if (D == 64) return mla_fwd_run<BF, 64, 64>(a, st);
         if (D == 96) return mla_fwd_run<BF, 96, 64>(a, st);
         if (D == 128) return mla_fwd_run<BF, 128, 64>(a, st);

@@ -64,13 +64,16 @@ __device__ __forceinline__ Share share_out(const MlaStepArgs &a, int lane) {
 __device__ __forceinline__ int part_slot(int w, int begin, int share) { return 2 * w + (begin > w * share ? 1 : 0); }
 
 // A tile holds KT rows; a wave takes KW of them (32 bf16 rows fill one MFMA's
-// K, 16 fp32 rows four) and DLP / WR columns. Two key groups times two column
-// groups: the scores are formed twice, which leaves a wave few enough
-// registers (112 at 128 + 32 bf16) for four waves per SIMD, and it is those
-// that hide a workgroup's start and end.
+// K, 16 fp32 rows four) and DLP / WR columns. In bf16 two key groups times two
+// column groups: the scores are formed twice, which is nothing beside the
+// memory, and leaves a wave few enough registers for three waves per SIMD;
+// those hide a piece's start and end. In fp32 the products are what takes the
+// time (a sixteenth of the bf16 rate), so up to 192 columns four key groups form
+// each score once (256 sequences of 128 + 32: 124 us with two groups, 103 with
+// four); beyond, the accumulators of all columns do not fit a wave.
 template <bool BF, int DLP, int MT> struct StepShape {
     using S = typename Op<BF>::S;
-    static constexpr int WK = 2, WR = 2, KW = BF && DLP <= 256 ? 32 : 16, KT = KW * WK, NJ = KW / 16, NT = 256, V = Op<BF>::VEC,
+        static constexpr int WK = !BF && DLP <= 192 ? 4 : 2, WR = 4 / WK, KW = BF && DLP <= 256 ? 32 : 16, KT = KW * WK, NJ = KW / 16, NT = 256, V = Op<BF>::VEC,
                          DP = DLP + 64, LD = DP + Op<BF>::PAD, MV = DLP / 16 / WR, KS = DP / 32,
                          RP = NT / (DP / V) > 0 ? NT / (DP / V) : 1, NIT = (KT + RP - 1) / RP,
                          TILE_B = KT * LD * (int)sizeof(S), MERGE_B = 4 * MT * MV * WR * 64 * 4;
@@ -281,7 +284,7 @@ __device__ __forceinline__ void step_piece(const MlaStepArgs a, int nq, int k0, 
             for (int t = 0; t < MT; ++t) O[t][v] = mma_rows<P::NJ>(vf, pf[t], O[t][v]);
         }
     }
-    // join the key groups: common maximum, then the rescaled sums of the second added to the first's
+    // join the key groups: common maximum, then the rescaled sums added to the first's, one after the other
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
         l[t] = sum4g(l[t]);
@@ -310,19 +313,27 @@ __device__ __forceinline__ void step_piece(const MlaStepArgs a, int nq, int k0, 
         sl[t] = sm;
     }
     f32x4 *X = (f32x4 *)smem + wr * MT * P::MV * 64;
-    if (kw == 1) {
+#pragma unroll 1
+    for (int w = 1; w < P::WK; ++w) {
+        if (kw == w) {
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
+            for (int t = 0; t < MT; ++t)
 #pragma unroll
-            for (int v = 0; v < P::MV; ++v) X[(t * P::MV + v) * 64 + lane] = O[t][v];
+                for (int v = 0; v < P::MV; ++v) X[(t * P::MV + v) * 64 + lane] = O[t][v];
+        }
+        lds_barrier();
+        if (kw == 0) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int v = 0; v < P::MV; ++v) O[t][v] += X[(t * P::MV + v) * 64 + lane];
+        }
+        if (w + 1 < P::WK) lds_barrier();
     }
-    lds_barrier();
-    if (kw == 1) return;
+    if (kw != 0) return;
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
         const int i = row0 + 16 * t + r;
-#pragma unroll
-        for (int v = 0; v < P::MV; ++v) O[t][v] += X[(t * P::MV + v) * 64 + lane];
         if (i >= rows) continue;
         const size_t out = (size_t)nq * rows + i;
         const float inv = sl[t] != 0.f ? 1.f / sl[t] : 0.f;
@@ -458,7 +469,7 @@ static int step_class(int dl) { return dl <= 64 ? 64 : dl <= 128 ? 128 : dl <= 1
 static int step_per_cu(const MlaStepArgs &a, bool bf16) {
     const int c = step_class(a.dl);
     if (bf16) return c == 64 ? 5 - a.mt : c == 128 ? 4 - a.mt : 2;
-    return c == 64 ? 4 : c <= 128 ? 3 : c == 192 ? 4 - a.mt : c == 256 ? 3 - a.mt : 1;
+    return c == 64 ? 3 : c == 128 ? 2 : c == 256 ? 3 - a.mt : 1;
 }
 
 void mla_step_plan(MlaStepArgs &a, bool bf16, int cus) {
