@@ -346,9 +346,10 @@ static int lanes_per_row(int d) {
     while (l * 8 < d) l *= 2;
     return l;
 }
-// Every pair lies in one 8-column vector, or the halves are whole vectors apart.
+// The turned columns begin with a vector, and every pair lies in one vector
+// (interleaved: vectors are of even length) or its halves are whole vectors apart.
 static bool row_vectors(int d, int r, int inter) {
-    return d % 8 == 0 && (r == 0 || inter || (r % 16 == 0 && (d - r) % 8 == 0));
+    return d % 8 == 0 && (r == 0 || ((d - r) % 8 == 0 && (inter || r % 16 == 0)));
 }
 static long long passes(long long rows, int d, int un) {
     const int rpp = NR_THREADS / lanes_per_row(d) * un;

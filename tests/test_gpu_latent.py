@@ -265,6 +265,8 @@ NORM = [
     (70, 1, 512, 512, False, True, True), (70, 1, 64, 64, True, False, False), (17, 8, 200, 0, False, True, True),
     (300, 5, 24, 16, False, True, True), (2, 1, 509, 508, False, True, True), (11, 3, 40, 40, False, False, False),
     (1000, 1, 1, 0, False, True, True),
+    # interleaved turns that begin inside eight columns
+    (21, 3, 64, 12, True, True, True), (6, 2, 8, 2, True, True, False), (300, 16, 24, 22, True, False, False),
 ]
 
 
