@@ -303,8 +303,9 @@ __device__ __forceinline__ void step_piece(const MlaStepArgs a, int nq, int k0, 
         float sm = 0.f;
 #pragma unroll
         for (int w = 0; w < P::WK; ++w) {
-            const float mw = Ms[w * MT * 16 + 16 * t + r];
-            sm += mw == -INFINITY ? 0.f : Ss[w * MT * 16 + 16 * t + r] * exp2_fast(mw - mm);
+            // (an empty group counts for nothing; one of NaN scores has a NaN sum and no maximum)
+            const float mw = Ms[w * MT * 16 + 16 * t + r], lw = Ss[w * MT * 16 + 16 * t + r];
+            sm += lw == 0.f ? 0.f : lw * exp2_fast(mw - mm);
         }
         const float f = m[t] == -INFINITY ? 0.f : exp2_fast(m[t] - mm);
 #pragma unroll
@@ -432,7 +433,7 @@ template <bool BF> __global__ __launch_bounds__(256) void mla_join_kernel(MlaSte
             m = mn;
 #pragma unroll
             for (int k = 0; k < JB; ++k) {
-                const float w = p0 + k * groups >= cnt || s[k][0] == -INFINITY ? 0.f : exp2_fast(s[k][0] - m);
+                const float w = p0 + k * groups >= cnt || s[k][1] == 0.f ? 0.f : exp2_fast(s[k][0] - m);
                 l = fmaf(w, s[k][1], l);
                 x += (w != 0.f ? y[k] : zero4()) * w;
             }
@@ -449,8 +450,8 @@ template <bool BF> __global__ __launch_bounds__(256) void mla_join_kernel(MlaSte
         f32x4 sum = zero4();
         float sl = 0.f;
         for (int k = 0; k < groups; ++k) {
-            const float mk = ms[tid + k * wide], w = mk == -INFINITY ? 0.f : exp2_fast(mk - mm);
-            sl += w * ls[tid + k * wide];
+            const float lk = ls[tid + k * wide], w = lk == 0.f ? 0.f : exp2_fast(ms[tid + k * wide] - mm);
+            sl = fmaf(w, lk, sl);
             if (w != 0.f) sum += acc[tid + k * wide] * w;
         }
         x = sum;

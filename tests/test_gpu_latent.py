@@ -234,6 +234,24 @@ def test_step_with_every_page_outside_the_pool():
     assert not o.any() and (lse == -float("inf")).all()
 
 
+@pytest.mark.parametrize("n", [5, 90, 40000])
+def test_step_with_a_nan_query(n):
+    """NaN in one head's query: that head gets NaN, cut into parts or not, the others what they had."""
+    say(f"step, a NaN query, {n} rows")
+    page, dl, dr, H = 64, 64, 16, 3
+    pages = -(-n // page)
+    g = rng(17)
+    cache, _ = dev(g.standard_normal((pages, page, dl + dr)), "bf16")
+    q, _ = dev(g.standard_normal((1, H, dl + dr)), "bf16")
+    table = ints(np.arange(pages)[None])
+    o, lse = gdn.mla_step(q, cache, table, ints([n]), dl, scale=0.1)
+    q[0, 1, 0] = float("nan")
+    o1, lse1 = gdn.mla_step(q, cache, table, ints([n]), dl, scale=0.1)
+    assert o1[0, 1].isnan().all() and lse1[0, 1].isnan()
+    for h in (0, 2):
+        assert torch.equal(o[0, h], o1[0, h]) and torch.equal(lse[0, h], lse1[0, h])
+
+
 def test_step_beyond_32_bit_offsets():
     """Rows past 2^32 bytes (and 2^31 elements) of the cache, written and read there."""
     say("cache of 5.4 GB: write and step at its end")
