@@ -9,6 +9,7 @@ import contextlib
 import ctypes
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import MlaShape, MlaStepShape, _bytes, _check, _dtype_code, _need as _explain, lib
 
@@ -24,6 +25,19 @@ def _need(t, name, dtype=None, shape=None, device=None):
                       and t.is_contiguous())):
         return
     _explain(t, name, dtype, shape, device)
+
+
+def _tensors(**ts):
+    for name, t in ts.items():
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a tensor")
+
+
+def _int32(**sizes):
+    """Sizes the library takes as int32 (ctypes would cut the rest off)."""
+    for name, n in sizes.items():
+        if not -2 ** 31 <= n < 2 ** 31:
+            raise ValueError(f"{name} = {n} is too large")
 
 
 def _p(t):
@@ -45,11 +59,12 @@ def _mla_shape(q, k, v, k_rope, lens, scale):
     B, Tq, H, D = q.shape
     _, Tk, Hk, dn = k.shape
     dr, dv, dev = D - dn, v.shape[-1], q.device
-    if dr < 0 or (dr > 0) != (k_rope is not None):
+    _int32(q=q.numel(), k=k.numel(), v=v.numel())
+    if D < 1 or dr < 0 or (dr > 0) != (k_rope is not None):
         raise ValueError("the last dimension of q must be that of k, plus that of k_rope when it is given")
     Hr = 0
     if k_rope is not None:
-        if k_rope.dim() != 4:
+        if not isinstance(k_rope, torch.Tensor) or k_rope.dim() != 4:
             raise ValueError("k_rope must be [B, T, heads, dr]")
         Hr = k_rope.shape[2]
     _need(q, "q", q.dtype, (B, Tq, H, D))
@@ -123,6 +138,7 @@ class LatentAttention(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do):
         q, k, v, k_rope, lens, o, lse = ctx.saved_tensors
         r = mla_bwd(q, k, v, o, lse, do.contiguous(), k_rope, lens, scale=ctx.scale)
@@ -136,8 +152,10 @@ def mla_step(q, cache, block_table, lens, dl, *, scale, o=None, lse=None, worksp
     are in the cache already). Returns (o [..., dl], lse)."""
     if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
         raise ValueError("q must be [N, S, H, d] or [N, H, d]")
+    _tensors(cache=cache, block_table=block_table, lens=lens)
     if cache.dim() != 3 or block_table.dim() != 2:
         raise ValueError("cache must be [pages, page_size, d], block_table [N, max_pages]")
+    _int32(q=q.numel(), dl=dl, pages=cache.shape[0], page_size=cache.shape[1], max_pages=block_table.shape[1])
     lead, d, dev = tuple(q.shape[:-1]), q.shape[-1], q.device
     N, H, S = lead[0], lead[-1], lead[1] if len(lead) == 3 else 1
     _need(q, "q", q.dtype)
@@ -167,6 +185,7 @@ def _rope_args(x, weight, positions, freqs, norm, interleaved):
     if not isinstance(x, torch.Tensor) or x.dim() < 2:
         raise ValueError("x must be [..., H, d]")
     dev, lead, d = x.device, tuple(x.shape[:-2]), x.shape[-1]
+    _int32(x=x.numel())
     _need(x, "x", x.dtype)
     if weight is not None and not norm:
         raise ValueError("weight needs norm=True")
@@ -234,6 +253,7 @@ class NormRope(torch.autograd.Function):
         return norm_rope(x, weight, positions, freqs, norm=norm, eps=eps, interleaved=interleaved)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, positions, freqs = ctx.saved_tensors
         r = norm_rope_bwd(dy.contiguous(), x, weight, positions, freqs, want_dw=weight is not None
@@ -247,9 +267,11 @@ def mla_write(c, k_rope, slots, cache, weight=None, positions=None, freqs=None, 
     place: row slots[i] = [norm(c[i]) * weight | k_rope[i] turned by
     positions[i] * freqs]. c [n,dl], k_rope [n,dr] or None, slots [n] int32
     (outside the cache: skipped; no slot twice). Returns cache."""
+    _tensors(c=c, slots=slots, cache=cache)
     if c.dim() != 2 or cache.dim() != 3:
         raise ValueError("c must be [n, dl], cache [pages, page_size, dl + dr]")
     n, dl = c.shape
+    _int32(c=c.numel(), d=cache.shape[2])
     dr, dev = cache.shape[2] - dl, c.device
     if dr < 0 or (dr > 0) != (k_rope is not None):
         raise ValueError("the last dimension of cache must be that of c, plus that of k_rope when it is given")
@@ -282,9 +304,11 @@ def page_plan(lens, new_lens, block_table, free_pages, n_free, page_size, max_to
     [N + 1], granted [N], lens [N], n_free [1], slots and positions
     [max_tokens], block_table and free_pages. lens_out=lens and
     n_free_out=n_free update those in place too."""
+    _tensors(lens=lens, new_lens=new_lens, block_table=block_table, free_pages=free_pages, n_free=n_free)
     if block_table.dim() != 2 or free_pages.dim() != 1:
         raise ValueError("block_table must be [N, max_pages], free_pages [n_pages]")
     N, cols = block_table.shape
+    _int32(block_table=block_table.numel(), free_pages=free_pages.numel(), page_size=page_size, max_tokens=max_tokens)
     i32, dev = torch.int32, block_table.device
     for t, name, shape in ((block_table, "block_table", (N, cols)), (lens, "lens", (N,)),
                            (new_lens, "new_lens", (N,)), (free_pages, "free_pages", None), (n_free, "n_free", (1,)),

@@ -169,3 +169,33 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         gdn.mla_write(torch.zeros(3, 16), None, torch.zeros(3), torch.zeros(4, 2, 24))
     with pytest.raises(ValueError):
         gdn.page_plan(*[torch.zeros(3)] * 2, torch.zeros(3), torch.zeros(3), torch.zeros(1), 4, 8)
+
+
+def test_binding_refuses_what_int32_does_not_hold_and_missing_tensors():
+    i32 = dict(dtype=torch.int32)
+    plan = [torch.zeros(3, **i32), torch.zeros(3, **i32), torch.zeros(3, 2, **i32), torch.zeros(6, **i32),
+            torch.zeros(1, **i32)]
+    for page, cap in ((2 ** 32 + 4, 8), (4, 2 ** 32 + 8), (4, -1), (0, 2 ** 31)):
+        with pytest.raises(ValueError):
+            gdn.page_plan(*plan, page, cap)
+    for k in range(5):
+        with pytest.raises(ValueError):
+            gdn.page_plan(*[None if i == k else t for i, t in enumerate(plan)], 4, 8)
+    wide = torch.zeros(1, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="too large"):
+        gdn.norm_rope(wide.expand(1, 2 ** 32 + 8))
+    long = wide.expand(1, 2 ** 32 + 64, 1, 8)
+    with pytest.raises(ValueError, match="too large"):
+        gdn.mla_fwd(wide.expand(1, 64, 1, 8), long, long)
+    with pytest.raises(ValueError, match="too large"):
+        gdn.mla_step(wide.expand(1, 1, 24), wide.expand(2 ** 32 + 1, 2, 24), torch.zeros(1, 2, **i32),
+                     torch.zeros(1, **i32), 16, scale=1.0)
+    with pytest.raises(ValueError, match="too large"):
+        gdn.mla_write(wide.expand(1, 2 ** 32 + 8), None, torch.zeros(1, **i32), wide.expand(1, 1, 2 ** 32 + 8))
+    empty = torch.zeros(1, 3, 2, 0)
+    with pytest.raises(ValueError):
+        gdn.mla_fwd(empty, empty, empty)
+    with pytest.raises(ValueError):
+        gdn.mla_step(torch.zeros(1, 1, 24), torch.zeros(1, 2, 24), torch.zeros(1, 2, **i32), None, 16, scale=1.0)
+    with pytest.raises(ValueError):
+        gdn.mla_write(torch.zeros(1, 16), None, None, torch.zeros(1, 2, 16))
