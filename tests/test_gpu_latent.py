@@ -62,6 +62,56 @@ def test_attention(case, dtype):
     check_attn(case, dtype, 7900)
 
 
+# B, Tq, past, H, Hk, Hr, dn, dr, dv: enough heads that large and paired blocks are taken
+MANY = [
+    (16, 300, 37, 64, 64, 16, 56, 32, 56), (16, 300, 0, 64, 64, 16, 128, 64, 128), (64, 140, 0, 16, 8, 8, 32, 16, 40),
+    (16, 257, 3, 64, 32, 32, 96, 24, 64), (16, 270, 0, 64, 64, 64, 32, 0, 32), (8, 270, 0, 64, 64, 16, 64, 0, 104),
+]
+
+
+def slices_within(f, got, case, dtype, lens, scale, where):
+    """The heads that share rotary head g of sequence b, for every (b, g) of `where`."""
+    H, Hk, Hr = case[3:6]
+    parts = {"q": H, "k": Hk, "kr": Hr, "v": Hk, "do": H, "o": H, "lse": H, "dq": H, "dk": Hk, "dkr": Hr, "dv": Hk}
+
+    def cut(n, x, b, g):
+        per = parts[n] // Hr
+        return None if x is None else x[b:b + 1, :, g * per:(g + 1) * per]
+
+    for b, g in where:
+        q, k, kr, v, do = (cut(n, x, b, g) for n, x in zip(("q", "k", "kr", "v", "do"), f))
+        for n, (x, tol) in attention(q, k, kr, v, None if lens is None else lens[b:b + 1], scale, do, dtype).items():
+            within(f"{n} of sequence {b}, group {g}", cut(n, got[n], b, g), x, tol)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("case", MANY, ids=lambda c: "-".join(map(str, c)))
+def test_attention_with_many_heads(case, dtype):
+    say(f"attention, many heads {case} {dtype}")
+    B, Tq, past, Hr = case[0], case[1], case[2], case[5]
+    lens = [Tq + past - 9 * b for b in range(B)]
+    lens[-1] = 0
+    t, f, ln, scale = attn_inputs(case + (lens,), dtype, 7910)
+    got = run_attn(t, ln, scale)
+    slices_within(f, got, case, dtype, lens, scale, [(0, 0), (0, Hr - 1), (B // 2, Hr // 2), (B - 2, Hr - 1)])
+    assert not got["o"][-1, past:].any() and not got["dk"][-1].any() and not got["dv"][-1].any()
+
+
+def test_attention_beyond_32_bit_offsets():
+    """Keys of more than 2^32 bytes, the last head checked."""
+    case = (1, 16, 14984, 600, 600, 600, 128, 0, 8)
+    say(f"attention {case} fp32")
+    B, Tq, past, H, dn, dv = 1, 16, 14984, 600, 128, 8
+    make = lambda *s: torch.randn(s, device="cuda", generator=torch.Generator("cuda").manual_seed(s[1]))  # noqa: E731
+    t = [make(B, Tq, H, dn), make(B, Tq + past, H, dn), None, make(B, Tq + past, H, dv), make(B, Tq, H, dv)]
+    assert t[1].numel() * 4 > 2 ** 32
+    got = run_attn(t, None, 0.1)
+    f = [None if x is None else host(x[:, :, -1:]) for x in t]
+    want = attention(f[0], f[1], None, f[3], None, 0.1, f[4], "fp32")
+    for n, (x, tol) in want.items():
+        within(n, got[n][:, :, -1:], x, tol)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_attention_with_sharp_scores(dtype):
     """Scores far apart: the maximum moves late, most weights vanish."""
@@ -175,6 +225,9 @@ STEP = [
     (1, 7, 3, 496, 40, 7, 60, [419]),
     (4, 1, 8, 64, 64, 128, 3, [384, 1000, -3, 129]),
     (1, 1, 33, 80, 16, 32, 40, [1280]),
+    (130, 1, 4, 32, 8, 16, 40, [i * i % 641 for i in range(130)]),
+    (67, 2, 2, 384, 16, 32, 8, [(37 * i) % 250 for i in range(67)]),
+    (3, 1, 2, 192, 64, 64, 190, [12160, 5, 9001]),
 ]
 
 
@@ -283,6 +336,8 @@ NORM = [
     (70, 1, 512, 512, False, True, True), (70, 1, 64, 64, True, False, False), (17, 8, 200, 0, False, True, True),
     (300, 5, 24, 16, False, True, True), (2, 1, 509, 508, False, True, True), (11, 3, 40, 40, False, False, False),
     (1000, 1, 1, 0, False, True, True),
+    # rows enough for several per thread
+    (3001, 16, 88, 32, False, True, True), (4100, 9, 128, 64, True, True, True), (50001, 1, 64, 16, False, True, False),
     # interleaved turns that begin inside eight columns
     (21, 3, 64, 12, True, True, True), (6, 2, 8, 2, True, True, False), (300, 16, 24, 22, True, False, False),
 ]
@@ -330,7 +385,8 @@ def test_norm_rope(case, dtype):
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("n,dl,dr,page,inter,norm", [(1, 8, 0, 1, False, True), (37, 128, 32, 16, False, True),
                                                      (300, 512, 64, 64, True, True), (65, 24, 8, 7, False, False),
-                                                     (5, 72, 64, 3, True, False)])
+                                                     (5, 72, 64, 3, True, False), (4500, 512, 64, 64, False, True),
+                                                     (8300, 200, 16, 16, True, True)])
 def test_write(n, dl, dr, page, inter, norm, dtype):
     say(f"cache write {n} {dl} {dr} {page} {dtype}")
     g, h = rng(7930), H16 if dtype == "bf16" else 0.0
