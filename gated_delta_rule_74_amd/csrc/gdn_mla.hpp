@@ -117,6 +117,23 @@ inline bool mla_large(long long heads, long long n, int rows, int per_cu) {
 // would not fit beside the operands of four (192 | 128: forward 1.59 ms with
 // four, 1.46 with eight; query gradients 2.74 and 2.28 ms, T 16384).
 constexpr int mla_waves(int dp, int dvp) { return dp + dvp > 224 ? 8 : 4; }
+// Where blocks of four times 16 rows leave the chip half empty, the waves of a
+// workgroup share rows instead and split every tile of the walk, joining their
+// sums at the end: two waves to 16 rows up to two such workgroups per CU (B1
+// T512, 16 heads 56 + 32 | 56, forward and backward: 52 us without, 44 with;
+// 1024 blocks: 55 and 69 us forward), four, and tiles of 128, where each then
+// has a CU to itself, or half of one and much to do: fp32 products, or a long
+// walk (B1 T1024, 16 heads on 4, key gradients: 97 us without, 66 with two, 50
+// with four; T2048: 186, 126, 104; T512, 16 heads: 19, 16, 20).
+constexpr int mla_tile(int split) { return split == 4 ? 128 : 64; }
+template <bool BF> constexpr bool mla_fits4(int dp, int dvp) { // (the tiles in LDS)
+    return mla_tile(4) * (dp + dvp + 2 * Op<BF>::PAD) * (int)sizeof(typename Op<BF>::S) <= 96 * 1024;
+}
+template <bool BF> int mla_split(long long heads, long long n, long long walk, int dp, int dvp) {
+    const long long w = heads * mla_blocks(n, 16);
+    if (mla_fits4<BF>(dp, dvp) && (w <= MLA_CUS || (w <= 2 * MLA_CUS && (!BF || walk >= 2048)))) return 4;
+    return heads * mla_blocks(n, 64) <= 2 * MLA_CUS ? 2 : 1;
+}
 // Workgroups of a launch over blocks of `rows`; sets pair.
 inline long long mla_work(MlaArgs &s, long long heads, long long n, int rows) {
     const long long blocks = mla_blocks(n, rows);
@@ -255,6 +272,32 @@ __device__ __forceinline__ void store4(float *p, f32x4 x) { *reinterpret_cast<f3
 // loads already in flight into registers stay in flight.
 __device__ __forceinline__ void lds_barrier() {
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Adds the accumulators of the WS waves that share rows, through LDS (64 * T * N
+// f32x4 for every group of waves: the tile's own size); true for the one that
+// has the sums.
+template <int N, int T, int WS>
+__device__ __forceinline__ bool join_parts(f32x4 (&x)[T][N], f32x4 *X, int wg, int wu, int lane) {
+    f32x4 *p = X + wg * T * N * 64 + lane;
+#pragma unroll 1
+    for (int w = 1; w < WS; ++w) {
+        lds_barrier(); // the last tile's, or part's, readers are done
+        if (wu == w) {
+#pragma unroll
+            for (int t = 0; t < T; ++t)
+#pragma unroll
+                for (int v = 0; v < N; ++v) p[(t * N + v) * 64] = x[t][v];
+        }
+        lds_barrier();
+        if (wu == 0) {
+#pragma unroll
+            for (int t = 0; t < T; ++t)
+#pragma unroll
+                for (int v = 0; v < N; ++v) x[t][v] += p[(t * N + v) * 64];
+        }
+    }
+    return wu == 0;
 }
 
 // Keeps the compiler from moving instructions across: what is requested before

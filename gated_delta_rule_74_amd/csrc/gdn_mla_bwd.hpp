@@ -23,32 +23,32 @@
 
 namespace gdn {
 
-constexpr int MLA_BT = 64;          // walked rows per tile
-constexpr int MLA_EXACT_TILES = 4; // blocks that see at most so many tiles form delta from the products
+constexpr int MLA_EXACT = 256; // blocks that see at most so many keys form delta from the products
 
 // dq of block qb of the queries of head bh, and their delta.
-template <bool BF, int DP, int DVP, int NW, int QT, class S>
-__device__ __forceinline__ void mla_bwd_q_block(const MlaBwdArgs a, int bh, int qb, S *Ks, S *Vs) {
+template <bool BF, int DP, int DVP, int NW, int QT, int WS, class S>
+__device__ __forceinline__ void mla_bwd_q_block(const MlaBwdArgs a, int bh, int qb, S *Ks, S *Vs, float *Dx) {
     constexpr int LDK = DP + Op<BF>::PAD, LDV = DVP + Op<BF>::PAD, NT = NW * 64, KS = DP / 32, VS = DVP / 32,
                   MD = DP / 16;
     const MlaArgs s = a.s;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
-    constexpr int QB = NW * QT * 16;
+    constexpr int QB = NW / WS * QT * 16, BT = mla_tile(WS);
+    const int wg = wave / WS, wu = wave % WS; // the wave's queries, its part of each tile
     const int b = bh / s.H, h = bh % s.H, hk = h / (s.H / s.Hk);
     const int hr = s.Hr > 0 ? h / (s.H / s.Hr) : 0;
     const int D = s.dn + s.dr, off = s.Tk - s.Tq;
     const int n = s.lens ? min(max(s.lens[b], 0), s.Tk) : s.Tk;
-    const int q0 = qb * QB + wave * QT * 16;
+    const int q0 = qb * QB + wg * QT * 16;
     const size_t rq = (size_t)s.H * D, rk = (size_t)s.Hk * s.dn, rr = (size_t)s.Hr * s.dr, rv = (size_t)s.Hk * s.dv,
                  ro = (size_t)s.H * s.dv;
     const S *kp = (const S *)s.k + (size_t)b * s.Tk * rk + (size_t)hk * s.dn;
     const S *krp = s.dr > 0 ? (const S *)s.kr + (size_t)b * s.Tk * rr + (size_t)hr * s.dr : kp;
     const S *vp = (const S *)s.v + (size_t)b * s.Tk * rv + (size_t)hk * s.dv;
     const int last = min(min(qb * QB + QB, s.Tq) - 1 + off, n - 1);
-    const int nt = qb * QB + off < n ? last / MLA_BT + 1 : 0;
+    const int nt = qb * QB + off < n ? last / BT + 1 : 0;
 
-    RowTile<BF, DP, MLA_BT, NT> kt;
-    RowTile<BF, DVP, MLA_BT, NT> vt;
+    RowTile<BF, DP, BT, NT> kt;
+    RowTile<BF, DVP, BT, NT> vt;
     kt.init(kp, rk, s.dn, krp, rr, s.dr, tid);
     vt.init(vp, rv, s.dv, vp, 0, 0, tid);
     if (nt > 0) {
@@ -90,10 +90,10 @@ __device__ __forceinline__ void mla_bwd_q_block(const MlaBwdArgs a, int bh, int 
     // Where a row sees few keys, dP - delta cancels, and do . o with o rounded
     // to bf16 is not near enough: a first walk forms delta = sum_j P_ij dP_ij
     // from the products themselves.
-    if (BF && nt <= MLA_EXACT_TILES) {
+    if (BF && nt * BT <= MLA_EXACT) {
         float sum[QT] = {};
         for (int kb = 0; kb < nt; ++kb) {
-            const int key0 = kb * MLA_BT, next = kb + 1 < nt ? key0 + MLA_BT : 0; // (0: for the walk below)
+            const int key0 = kb * BT, next = kb + 1 < nt ? key0 + BT : 0; // (0: for the walk below)
             lds_barrier();
             kt.stash(Ks, LDK, key0, n);
             vt.stash(Vs, LDV, key0, n);
@@ -101,7 +101,7 @@ __device__ __forceinline__ void mla_bwd_q_block(const MlaBwdArgs a, int bh, int 
             vt.fetch(next, n);
             lds_barrier();
 #pragma unroll 1
-            for (int j = 0; j < MLA_BT / 16; ++j)
+            for (int j = wu; j < BT / 16; j += WS)
 #pragma unroll
                 for (int t = 0; t < QT; ++t) {
                     f32x4 z = zero4(), dp = zero4();
@@ -117,6 +117,18 @@ __device__ __forceinline__ void mla_bwd_q_block(const MlaBwdArgs a, int bh, int 
         }
 #pragma unroll
         for (int t = 0; t < QT; ++t) delta[t] = sum4g(sum[t]);
+        if constexpr (WS > 1) { // (the same order on both waves)
+#pragma unroll
+            for (int t = 0; t < QT; ++t)
+                if (g == 0) Dx[(wave * QT + t) * 16 + r] = delta[t];
+            lds_barrier();
+#pragma unroll
+            for (int t = 0; t < QT; ++t) {
+                delta[t] = 0.f;
+#pragma unroll
+                for (int w = 0; w < WS; ++w) delta[t] += Dx[((wg * WS + w) * QT + t) * 16 + r];
+            }
+        }
     }
     f32x4 dQ[QT][MD];
 #pragma unroll
@@ -125,19 +137,19 @@ __device__ __forceinline__ void mla_bwd_q_block(const MlaBwdArgs a, int bh, int 
         for (int v = 0; v < MD; ++v) dQ[t][v] = zero4();
     wait_vmem(); // (what is held is there: else its first use in the loop waits for the tile in flight)
     for (int kb = 0; kb < nt; ++kb) {
-        const int key0 = kb * MLA_BT;
+        const int key0 = kb * BT;
         lds_barrier(); // the previous tile's readers are done
         kt.stash(Ks, LDK, key0, n);
         vt.stash(Vs, LDV, key0, n);
         if (kb + 1 < nt) {
-            kt.fetch(key0 + MLA_BT, n);
-            vt.fetch(key0 + MLA_BT, n);
+            kt.fetch(key0 + BT, n);
+            vt.fetch(key0 + BT, n);
         }
         lds_barrier();
-        const int nu = key0 > wlast || wfirst >= n ? 0 : MLA_BT / 32; // (0: no query of the wave sees the tile)
-        const bool mask = key0 + MLA_BT - 1 > wfirst || key0 + MLA_BT > n;
+        const int nu = key0 > wlast || wfirst >= n ? 0 : BT / 32; // (0: no query of the wave sees the tile)
+        const bool mask = key0 + BT - 1 > wfirst || key0 + BT > n;
 #pragma unroll 1
-        for (int u = 0; u < nu; ++u) {
+        for (int u = wu; u < nu; u += WS) {
             f32x4 P[QT][2], dP[QT][2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -181,6 +193,9 @@ __device__ __forceinline__ void mla_bwd_q_block(const MlaBwdArgs a, int bh, int 
             }
         }
     }
+    if constexpr (WS > 1) { // the parts of the walk, one after the other
+        if (!join_parts<MD, QT, WS>(dQ, (f32x4 *)Ks, wg, wu, lane)) return;
+    }
     S *dqp = (S *)a.dq + (size_t)b * s.Tq * rq + (size_t)h * D;
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
@@ -195,19 +210,20 @@ __device__ __forceinline__ void mla_bwd_q_block(const MlaBwdArgs a, int bh, int 
     }
 }
 
-template <bool BF, int DP, int DVP, int NW, int QT>
-__global__ __launch_bounds__(NW * 64, 2) void mla_bwd_q_kernel(MlaBwdArgs a) {
+template <bool BF, int DP, int DVP, int NW, int QT, int WS>
+__global__ __launch_bounds__(NW * 64, WS == 4 ? 1 : 2) void mla_bwd_q_kernel(MlaBwdArgs a) {
     using S = typename Op<BF>::S;
-    __shared__ __align__(16) S Ks[MLA_BT * (DP + Op<BF>::PAD)];
-    __shared__ __align__(16) S Vs[MLA_BT * (DVP + Op<BF>::PAD)];
-    constexpr int QB = NW * QT * 16;
+    constexpr int QB = NW / WS * QT * 16, BT = mla_tile(WS);
+    __shared__ __align__(16) S Ks[BT * (DP + Op<BF>::PAD)];
+    __shared__ __align__(16) S Vs[BT * (DVP + Op<BF>::PAD)];
+    __shared__ float Dx[WS > 1 ? NW * QT * 16 : 1];
     const int nqb = (a.s.Tq + QB - 1) / QB, work = a.s.pair ? (nqb + 1) / 2 : nqb;
     int bh, i;
     head_block(blockIdx.x, a.s.B * a.s.H, work, bh, i);
     // the last queries walk longest (a block begins with a barrier, so the tiles may be reused)
     const int parts = a.s.pair && i < nqb - 1 - i ? 2 : 1;
 #pragma unroll 1
-    for (int p = 0; p < parts; ++p) mla_bwd_q_block<BF, DP, DVP, NW, QT>(a, bh, p ? i : nqb - 1 - i, Ks, Vs);
+    for (int p = 0; p < parts; ++p) mla_bwd_q_block<BF, DP, DVP, NW, QT, WS>(a, bh, p ? i : nqb - 1 - i, Ks, Vs, Dx);
 }
 
 // x[t][j] += the products of N walked operands with the held ones of tile t.
@@ -220,39 +236,40 @@ __device__ __forceinline__ void times(f32x4 (&x)[T][2], int j, const Frags<BF, N
 }
 
 // dk, dkr and dv of block kb of the keys of key head bh.
-template <bool BF, int DP, int DVP, int NW, int KT, class S>
+template <bool BF, int DP, int DVP, int NW, int KT, int WS, class S>
 __device__ __forceinline__ void mla_bwd_k_block(const MlaBwdArgs a, int bh, int kb, S *Qs, S *Gs, float *Ls,
                                                 float *Ds) {
     constexpr int LDQ = DP + Op<BF>::PAD, LDG = DVP + Op<BF>::PAD, NT = NW * 64, KS = DP / 32, VS = DVP / 32,
                   MD = DP / 16, MV = DVP / 16;
     const MlaArgs s = a.s;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
-    constexpr int KB = NW * KT * 16;
+    constexpr int KB = NW / WS * KT * 16, BT = mla_tile(WS);
+    const int wg = wave / WS, wu = wave % WS; // the wave's keys, its part of each tile
     const int b = bh / s.Hk, hk = bh % s.Hk, per = s.H / s.Hk;
     const int hr = s.Hr > 0 ? hk / (s.Hk / s.Hr) : 0;
     const int D = s.dn + s.dr, off = s.Tk - s.Tq;
     const int n = s.lens ? min(max(s.lens[b], 0), s.Tk) : s.Tk;
-    const int key0 = kb * KB, w0 = key0 + wave * KT * 16; // first key of the workgroup, of the wave
+    const int key0 = kb * KB, w0 = key0 + wg * KT * 16; // first key of the workgroup, of the wave
     const size_t rq = (size_t)s.H * D, rk = (size_t)s.Hk * s.dn, rr = (size_t)s.Hr * s.dr, rv = (size_t)s.Hk * s.dv,
                  ro = (size_t)s.H * s.dv;
     // queries that see a key of this workgroup: q_lo .. nq - 1, a tile-aligned walk of each head
     const int nq = min(s.Tq, n - off);
-    const int t_lo = max(key0 - off, 0) / MLA_BT;
-    const int tiles = key0 < n && nq > t_lo * MLA_BT ? (nq + MLA_BT - 1) / MLA_BT - t_lo : 0;
+    const int t_lo = max(key0 - off, 0) / BT;
+    const int tiles = key0 < n && nq > t_lo * BT ? (nq + BT - 1) / BT - t_lo : 0;
     const int total = tiles * per;
 
-    RowTile<BF, DP, MLA_BT, NT> qt;
-    RowTile<BF, DVP, MLA_BT, NT> gt;
+    RowTile<BF, DP, BT, NT> qt;
+    RowTile<BF, DVP, BT, NT> gt;
     const S *qp = (const S *)s.q + (size_t)b * s.Tq * rq + (size_t)hk * per * D; // first of the heads
     const S *gp = (const S *)a.dout + (size_t)b * s.Tq * ro + (size_t)hk * per * s.dv;
     qt.init(qp, rq, D, qp, 0, 0, tid);
     gt.init(gp, ro, s.dv, gp, 0, 0, tid);
     float lreg = 0.f, dreg = 0.f;
     auto fetch = [&](int x) {
-        const int h = hk * per + x / tiles, row0 = (t_lo + x % tiles) * MLA_BT;
+        const int h = hk * per + x / tiles, row0 = (t_lo + x % tiles) * BT;
         qt.fetch(row0, nq, (size_t)(x / tiles) * D);
         gt.fetch(row0, nq, (size_t)(x / tiles) * s.dv);
-        if (tid < MLA_BT) {
+        if (tid < BT) {
             const int i = min(row0 + tid, nq - 1);
             lreg = a.lse[((size_t)b * s.Tq + i) * s.H + h];
             dreg = a.delta[((size_t)b * s.H + h) * s.Tq + i];
@@ -289,21 +306,21 @@ __device__ __forceinline__ void mla_bwd_k_block(const MlaBwdArgs a, int bh, int 
     const float c2 = s.scale * (float)LOG2E;
     wait_vmem(); // (as above)
     for (int x = 0; x < total; ++x) {
-        const int row0 = (t_lo + x % tiles) * MLA_BT;
+        const int row0 = (t_lo + x % tiles) * BT;
         lds_barrier();
         qt.stash(Qs, LDQ, row0, nq);
         gt.stash(Gs, LDG, row0, nq);
-        if (tid < MLA_BT) {
+        if (tid < BT) {
             Ls[tid] = lreg == -INFINITY ? INFINITY : lreg * (float)LOG2E;
             Ds[tid] = dreg;
         }
         if (x + 1 < total) fetch(x + 1);
         lds_barrier();
         // (0: no query of the tile sees a key of this wave)
-        const int nu = row0 + MLA_BT - 1 + off < w0 || w0 >= n ? 0 : MLA_BT / 32;
-        const bool mask = row0 + off < w0 + KT * 16 - 1 || row0 + MLA_BT > nq || w0 + KT * 16 > n;
+        const int nu = row0 + BT - 1 + off < w0 || w0 >= n ? 0 : BT / 32;
+        const bool mask = row0 + off < w0 + KT * 16 - 1 || row0 + BT > nq || w0 + KT * 16 > n;
 #pragma unroll 1
-        for (int u = 0; u < nu; ++u) {
+        for (int u = wu; u < nu; u += WS) {
             f32x4 P[KT][2], dP[KT][2];
             // operands are requested one group ahead of the products that use them
             Frags<BF, KS> qa, qb;
@@ -382,6 +399,10 @@ __device__ __forceinline__ void mla_bwd_k_block(const MlaBwdArgs a, int bh, int 
             }
         }
     }
+    if constexpr (WS > 1) {
+        join_parts<MD, KT, WS>(dK, (f32x4 *)Qs, wg, wu, lane);
+        if (!join_parts<MV, KT, WS>(dV, (f32x4 *)Gs, wg, wu, lane)) return;
+    }
     S *dkp = (S *)a.dk + (size_t)b * s.Tk * rk + (size_t)hk * s.dn;
     S *dvp = (S *)a.dv + (size_t)b * s.Tk * rv + (size_t)hk * s.dv;
 #pragma unroll
@@ -415,45 +436,54 @@ __device__ __forceinline__ void mla_bwd_k_block(const MlaBwdArgs a, int bh, int 
 // per wave: 3.2 ms at T 16384, one tile and two waves 3.8).
 constexpr int mla_bwd_k_waves(int kt, int dp, int dvp) { return kt == 1 || dp + dvp <= 160 ? 2 : 1; }
 
-template <bool BF, int DP, int DVP, int NW, int KT>
-__global__ __launch_bounds__(NW * 64, mla_bwd_k_waves(KT, DP, DVP)) void mla_bwd_k_kernel(MlaBwdArgs a) {
+template <bool BF, int DP, int DVP, int NW, int KT, int WS>
+__global__ __launch_bounds__(NW * 64, WS == 4 ? 1 : mla_bwd_k_waves(KT, DP, DVP)) void mla_bwd_k_kernel(MlaBwdArgs a) {
     using S = typename Op<BF>::S;
-    __shared__ __align__(16) S Qs[MLA_BT * (DP + Op<BF>::PAD)];
-    __shared__ __align__(16) S Gs[MLA_BT * (DVP + Op<BF>::PAD)];
-    __shared__ __align__(16) float Ls[MLA_BT], Ds[MLA_BT];
-    constexpr int KB = NW * KT * 16;
+    constexpr int KB = NW / WS * KT * 16, BT = mla_tile(WS);
+    __shared__ __align__(16) S Qs[BT * (DP + Op<BF>::PAD)];
+    __shared__ __align__(16) S Gs[BT * (DVP + Op<BF>::PAD)];
+    __shared__ __align__(16) float Ls[BT], Ds[BT];
     const int nkb = (a.s.Tk + KB - 1) / KB, work = a.s.pair ? (nkb + 1) / 2 : nkb;
     int bh, i;
     head_block(blockIdx.x, a.s.B * a.s.Hk, work, bh, i);
     // the first keys are seen by the most queries
     const int parts = a.s.pair && i < nkb - 1 - i ? 2 : 1;
 #pragma unroll 1
-    for (int p = 0; p < parts; ++p) mla_bwd_k_block<BF, DP, DVP, NW, KT>(a, bh, p ? nkb - 1 - i : i, Qs, Gs, Ls, Ds);
+    for (int p = 0; p < parts; ++p) mla_bwd_k_block<BF, DP, DVP, NW, KT, WS>(a, bh, p ? nkb - 1 - i : i, Qs, Gs, Ls, Ds);
 }
 
-template <bool BF, int DP, int DVP, int NW, int QT> hipError_t mla_bwd_q_start(MlaBwdArgs a, hipStream_t st) {
-    const long long work = mla_work(a.s, (long long)a.s.B * a.s.H, a.s.Tq, NW * QT * 16);
-    hipLaunchKernelGGL((mla_bwd_q_kernel<BF, DP, DVP, NW, QT>), dim3((unsigned)work), dim3(NW * 64), 0, st, a);
+template <bool BF, int DP, int DVP, int NW, int QT, int WS> hipError_t mla_bwd_q_start(MlaBwdArgs a, hipStream_t st) {
+    const long long work = mla_work(a.s, (long long)a.s.B * a.s.H, a.s.Tq, NW / WS * QT * 16);
+    hipLaunchKernelGGL((mla_bwd_q_kernel<BF, DP, DVP, NW, QT, WS>), dim3((unsigned)work), dim3(NW * 64), 0, st, a);
     return hipGetLastError();
 }
 template <bool BF, int DP, int DVP> hipError_t mla_bwd_q_run(const MlaBwdArgs &a, hipStream_t st) {
+    const long long heads = (long long)a.s.B * a.s.H;
     if constexpr (BF) {
         constexpr int NW = mla_waves(DP, DVP);
-        if (mla_large((long long)a.s.B * a.s.H, a.s.Tq, NW * 32, 8 / NW))
-            return mla_bwd_q_start<BF, DP, DVP, NW, 2>(a, st);
+        if (mla_large(heads, a.s.Tq, NW * 32, 8 / NW)) return mla_bwd_q_start<BF, DP, DVP, NW, 2, 1>(a, st);
     }
-    return mla_bwd_q_start<BF, DP, DVP, 4, 1>(a, st);
+    const int split = mla_split<BF>(heads, a.s.Tq, a.s.Tk, DP, DVP);
+    if constexpr (mla_fits4<BF>(DP, DVP))
+        if (split == 4) return mla_bwd_q_start<BF, DP, DVP, 4, 1, 4>(a, st);
+    if (split == 2) return mla_bwd_q_start<BF, DP, DVP, 4, 1, 2>(a, st);
+    return mla_bwd_q_start<BF, DP, DVP, 4, 1, 1>(a, st);
 }
-template <bool BF, int DP, int DVP, int NW, int KT> hipError_t mla_bwd_k_start(MlaBwdArgs a, hipStream_t st) {
-    const long long work = mla_work(a.s, (long long)a.s.B * a.s.Hk, a.s.Tk, NW * KT * 16);
-    hipLaunchKernelGGL((mla_bwd_k_kernel<BF, DP, DVP, NW, KT>), dim3((unsigned)work), dim3(NW * 64), 0, st, a);
+template <bool BF, int DP, int DVP, int NW, int KT, int WS> hipError_t mla_bwd_k_start(MlaBwdArgs a, hipStream_t st) {
+    const long long work = mla_work(a.s, (long long)a.s.B * a.s.Hk, a.s.Tk, NW / WS * KT * 16);
+    hipLaunchKernelGGL((mla_bwd_k_kernel<BF, DP, DVP, NW, KT, WS>), dim3((unsigned)work), dim3(NW * 64), 0, st, a);
     return hipGetLastError();
 }
 template <bool BF, int DP, int DVP> hipError_t mla_bwd_k_run(const MlaBwdArgs &a, hipStream_t st) {
+    const long long heads = (long long)a.s.B * a.s.Hk;
     if constexpr (BF)
-        if (mla_large((long long)a.s.B * a.s.Hk, a.s.Tk, 128, mla_bwd_k_waves(2, DP, DVP)))
-            return mla_bwd_k_start<BF, DP, DVP, 4, 2>(a, st);
-    return mla_bwd_k_start<BF, DP, DVP, 4, 1>(a, st);
+        if (mla_large(heads, a.s.Tk, 128, mla_bwd_k_waves(2, DP, DVP)))
+            return mla_bwd_k_start<BF, DP, DVP, 4, 2, 1>(a, st);
+    const int split = mla_split<BF>(heads, a.s.Tk, (long long)a.s.Tq * (a.s.H / a.s.Hk), DP, DVP);
+    if constexpr (mla_fits4<BF>(DP, DVP))
+        if (split == 4) return mla_bwd_k_start<BF, DP, DVP, 4, 1, 4>(a, st);
+    if (split == 2) return mla_bwd_k_start<BF, DP, DVP, 4, 1, 2>(a, st);
+    return mla_bwd_k_start<BF, DP, DVP, 4, 1, 1>(a, st);
 }
 
 template <bool BF, bool Q, int DP, int DVP> hipError_t mla_bwd_run(const MlaBwdArgs &a, hipStream_t st) {

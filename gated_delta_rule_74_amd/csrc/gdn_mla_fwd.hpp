@@ -17,35 +17,40 @@
 // 2^RAISE too large, in P, in the sum and in O alike, which fp32 holds without
 // loss; this keeps the cross-lane maximum and the rescaling of O out of almost
 // every tile.
+// Wide heads (192 | 128) run at 0.8 of the rate a large matrix product reaches
+// (8 heads on 1, T 16384: 1.41 ms); at 96 | 64 the exponentials and the mask
+// take as long as the products (B8 H16 T4096: 0.46 ms, 0.54 of that rate). More
+// waves per SIMD (three, four) or value operands requested ahead do not change
+// either.
 #pragma once
 
 #include "gdn_mla.hpp"
 
 namespace gdn {
 
-constexpr int MLA_KT = 64;      // keys per tile
 constexpr float MLA_RAISE = 8.f; // see above
 
-template <bool BF, int DP, int DVP, int NW, int QT> struct MlaFwdShape {
+template <bool BF, int DP, int DVP, int NW, int QT, int WS> struct MlaFwdShape {
     using S = typename Op<BF>::S;
-    static constexpr int LDK = DP + Op<BF>::PAD, LDV = DVP + Op<BF>::PAD, QB = NW * QT * 16;
+    static constexpr int LDK = DP + Op<BF>::PAD, LDV = DVP + Op<BF>::PAD, QB = NW / WS * QT * 16, BT = mla_tile(WS);
     // two tiles where a second workgroup still fits the CU's 160 KB beside them
-    static constexpr int NB = 2 * MLA_KT * (LDK + LDV) * (int)sizeof(S) <= 80 * 1024 ? 2 : 1;
+    static constexpr int NB = 2 * BT * (LDK + LDV) * (int)sizeof(S) <= 80 * 1024 ? 2 : 1;
 };
 
 // Block qb of the queries of head bh.
-template <bool BF, int DP, int DVP, int NW, int QT, class S>
-__device__ __forceinline__ void mla_fwd_block(const MlaFwdArgs a, int bh, int qb, S *Kst, S *Vst) {
-    using H = MlaFwdShape<BF, DP, DVP, NW, QT>;
+template <bool BF, int DP, int DVP, int NW, int QT, int WS, class S>
+__device__ __forceinline__ void mla_fwd_block(const MlaFwdArgs a, int bh, int qb, S *Kst, S *Vst, float2 *ML) {
+    using H = MlaFwdShape<BF, DP, DVP, NW, QT, WS>;
     constexpr int LDK = H::LDK, LDV = H::LDV, NB = H::NB, NT = NW * 64, KS = DP / 32, MV = DVP / 16;
     const MlaArgs s = a.s;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
-    constexpr int QB = H::QB;
+    constexpr int QB = H::QB, BT = H::BT;
+    const int wg = wave / WS, wu = wave % WS; // the wave's queries, its part of each tile
     const int b = bh / s.H, h = bh % s.H, hk = h / (s.H / s.Hk);
     const int hr = s.Hr > 0 ? h / (s.H / s.Hr) : 0;
     const int D = s.dn + s.dr, off = s.Tk - s.Tq;
     const int n = s.lens ? min(max(s.lens[b], 0), s.Tk) : s.Tk;
-    const int q0 = qb * QB + wave * QT * 16; // first query of this wave
+    const int q0 = qb * QB + wg * QT * 16; // first query of this wave
     const size_t rq = (size_t)s.H * D, rk = (size_t)s.Hk * s.dn, rr = (size_t)s.Hr * s.dr, rv = (size_t)s.Hk * s.dv;
     const S *kp = (const S *)s.k + (size_t)b * s.Tk * rk + (size_t)hk * s.dn;
     const S *krp = s.dr > 0 ? (const S *)s.kr + (size_t)b * s.Tk * rr + (size_t)hr * s.dr : kp;
@@ -54,10 +59,10 @@ __device__ __forceinline__ void mla_fwd_block(const MlaFwdArgs a, int bh, int qb
     // keys the workgroup has to see: those of its last query that is not padding
     const int last = min(min(qb * QB + QB, s.Tq) - 1 + off, n - 1);
     const int first = qb * QB + off; // position of its first query
-    const int nt = first < n ? last / MLA_KT + 1 : 0;
+    const int nt = first < n ? last / BT + 1 : 0;
 
-    RowTile<BF, DP, MLA_KT, NT> kt;
-    RowTile<BF, DVP, MLA_KT, NT> vt;
+    RowTile<BF, DP, BT, NT> kt;
+    RowTile<BF, DVP, BT, NT> vt;
     kt.init(kp, rk, s.dn, krp, rr, s.dr, tid);
     vt.init(vp, rv, s.dv, vp, 0, 0, tid);
     if (nt > 0) {
@@ -94,16 +99,16 @@ __device__ __forceinline__ void mla_fwd_block(const MlaFwdArgs a, int bh, int qb
     wait_vmem(); // (Q is there: else its first use in the loop waits for the tile in flight)
     const int wlast = min(q0 + QT * 16 - 1 + off, n - 1), wfirst = q0 + off;
     for (int kb = 0; kb < nt; ++kb) {
-        const int key0 = kb * MLA_KT;
+        const int key0 = kb * BT;
         if (kb + 1 < nt) {
-            kt.fetch(key0 + MLA_KT, n);
-            vt.fetch(key0 + MLA_KT, n);
+            kt.fetch(key0 + BT, n);
+            vt.fetch(key0 + BT, n);
         }
         if (key0 <= wlast && wfirst < n) {
-            const S *K = Kst + kb % NB * (MLA_KT * LDK), *V = Vst + kb % NB * (MLA_KT * LDV);
-            const bool mask = key0 + MLA_KT - 1 > wfirst || key0 + MLA_KT > n;
+            const S *K = Kst + kb % NB * (BT * LDK), *V = Vst + kb % NB * (BT * LDV);
+            const bool mask = key0 + BT - 1 > wfirst || key0 + BT > n;
 #pragma unroll 1
-            for (int u = 0; u < MLA_KT / 32; ++u) {
+            for (int u = wu; u < BT / 32; u += WS) {
                 f32x4 P[QT][2];
 #pragma unroll
                 for (int t = 0; t < QT; ++t) P[t][0] = P[t][1] = zero4();
@@ -172,16 +177,42 @@ __device__ __forceinline__ void mla_fwd_block(const MlaFwdArgs a, int bh, int qb
         if (kb + 1 < nt) {
             // with two buffers the other one's last readers passed the previous barrier
             if (NB == 1) lds_barrier();
-            kt.stash(Kst + (kb + 1) % NB * (MLA_KT * LDK), LDK, key0 + MLA_KT, n);
-            vt.stash(Vst + (kb + 1) % NB * (MLA_KT * LDV), LDV, key0 + MLA_KT, n);
+            kt.stash(Kst + (kb + 1) % NB * (BT * LDK), LDK, key0 + BT, n);
+            vt.stash(Vst + (kb + 1) % NB * (BT * LDV), LDV, key0 + BT, n);
             lds_barrier();
         }
+    }
+    if constexpr (WS > 1) {
+        // the parts of the walk: common maximum, sums rescaled to it and added
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+            l[t] = sum4g(l[t]);
+            if (g == 0) ML[(wave * QT + t) * 16 + r] = float2{m[t], l[t]};
+        }
+        lds_barrier();
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+            float mm = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < WS; ++w) mm = fmaxf(mm, ML[((wg * WS + w) * QT + t) * 16 + r].x);
+#pragma unroll
+            for (int w = 0; w < WS; ++w) { // (a part without keys counts for nothing)
+                const float2 x = ML[((wg * WS + w) * QT + t) * 16 + r];
+                sum += x.y == 0.f ? 0.f : x.y * exp2_fast(x.x - mm);
+            }
+            const float f = l[t] == 0.f ? 0.f : exp2_fast(m[t] - mm);
+#pragma unroll
+            for (int v = 0; v < MV; ++v) O[t][v] *= f;
+            m[t] = mm;
+            l[t] = sum;
+        }
+        if (!join_parts<MV, QT, WS>(O, (f32x4 *)Vst, wg, wu, lane)) return;
     }
     S *op = (S *)a.o + (size_t)b * s.Tq * s.H * s.dv + (size_t)h * s.dv;
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
         const int i = q0 + 16 * t + r;
-        const float lt = sum4g(l[t]);
+        const float lt = WS > 1 ? l[t] : sum4g(l[t]);
         const bool some = i + off < n; // (a query at or past the length has no key)
         const float inv = some && lt != 0.f ? 1.f / lt : 0.f; // (every score -inf: o = 0)
         if (i >= s.Tq) continue;
@@ -197,11 +228,12 @@ __device__ __forceinline__ void mla_fwd_block(const MlaFwdArgs a, int bh, int qb
     }
 }
 
-template <bool BF, int DP, int DVP, int NW, int QT>
-__global__ __launch_bounds__(NW * 64, 2) void mla_fwd_kernel(MlaFwdArgs a) {
-    using H = MlaFwdShape<BF, DP, DVP, NW, QT>;
-    __shared__ __align__(16) typename H::S Ks[H::NB * MLA_KT * H::LDK];
-    __shared__ __align__(16) typename H::S Vs[H::NB * MLA_KT * H::LDV];
+template <bool BF, int DP, int DVP, int NW, int QT, int WS>
+__global__ __launch_bounds__(NW * 64, WS == 4 ? 1 : 2) void mla_fwd_kernel(MlaFwdArgs a) {
+    using H = MlaFwdShape<BF, DP, DVP, NW, QT, WS>;
+    __shared__ float2 ML[WS > 1 ? NW * QT * 16 : 1];
+    __shared__ __align__(16) typename H::S Ks[H::NB * H::BT * H::LDK];
+    __shared__ __align__(16) typename H::S Vs[H::NB * H::BT * H::LDV];
     const int nqb = (a.s.Tq + H::QB - 1) / H::QB, work = a.s.pair ? (nqb + 1) / 2 : nqb;
     int bh, i;
     head_block(blockIdx.x, a.s.B * a.s.H, work, bh, i);
@@ -210,22 +242,26 @@ __global__ __launch_bounds__(NW * 64, 2) void mla_fwd_kernel(MlaFwdArgs a) {
 #pragma unroll 1
     for (int p = 0; p < parts; ++p) {
         if (p) lds_barrier(); // (the first block's readers are done)
-        mla_fwd_block<BF, DP, DVP, NW, QT>(a, bh, p ? i : nqb - 1 - i, Ks, Vs);
+        mla_fwd_block<BF, DP, DVP, NW, QT, WS>(a, bh, p ? i : nqb - 1 - i, Ks, Vs, ML);
     }
 }
 
-template <bool BF, int DP, int DVP, int NW, int QT> hipError_t mla_fwd_start(MlaFwdArgs a, hipStream_t st) {
-    const long long work = mla_work(a.s, (long long)a.s.B * a.s.H, a.s.Tq, NW * QT * 16);
-    hipLaunchKernelGGL((mla_fwd_kernel<BF, DP, DVP, NW, QT>), dim3((unsigned)work), dim3(NW * 64), 0, st, a);
+template <bool BF, int DP, int DVP, int NW, int QT, int WS> hipError_t mla_fwd_start(MlaFwdArgs a, hipStream_t st) {
+    const long long work = mla_work(a.s, (long long)a.s.B * a.s.H, a.s.Tq, NW / WS * QT * 16);
+    hipLaunchKernelGGL((mla_fwd_kernel<BF, DP, DVP, NW, QT, WS>), dim3((unsigned)work), dim3(NW * 64), 0, st, a);
     return hipGetLastError();
 }
 template <bool BF, int DP, int DVP> hipError_t mla_fwd_run(const MlaFwdArgs &a, hipStream_t st) {
+    const long long heads = (long long)a.s.B * a.s.H;
     if constexpr (BF) {
         constexpr int NW = mla_waves(DP, DVP);
-        if (mla_large((long long)a.s.B * a.s.H, a.s.Tq, NW * 32, 8 / NW))
-            return mla_fwd_start<BF, DP, DVP, NW, 2>(a, st);
+        if (mla_large(heads, a.s.Tq, NW * 32, 8 / NW)) return mla_fwd_start<BF, DP, DVP, NW, 2, 1>(a, st);
     }
-    return mla_fwd_start<BF, DP, DVP, 4, 1>(a, st);
+    const int split = mla_split<BF>(heads, a.s.Tq, a.s.Tk, DP, DVP);
+    if constexpr (mla_fits4<BF>(DP, DVP))
+        if (split == 4) return mla_fwd_start<BF, DP, DVP, 4, 1, 4>(a, st);
+    if (split == 2) return mla_fwd_start<BF, DP, DVP, 4, 1, 2>(a, st);
+    return mla_fwd_start<BF, DP, DVP, 4, 1, 1>(a, st);
 }
 
 template <bool BF> hipError_t mla_fwd_launch(const MlaFwdArgs &a, hipStream_t st) {
