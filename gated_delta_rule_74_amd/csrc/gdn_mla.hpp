@@ -62,6 +62,7 @@ struct MlaStepArgs {
     int N, S, H, dl, dr, pages, page, cols;
     float scale;
     int mt, units;  // blocks of 16 rows per workgroup; shares the cached rows are cut into
+    int tile;       // log2 of a tile's rows; a share is a whole number of tiles
     float *part;    // workspace [2 * units][S * H][dl]
     float *part_ml; // workspace [2 * units][S * H][2]
 };
@@ -197,11 +198,25 @@ __device__ __forceinline__ Frag<true> row8(const u16 *p) { return {*reinterpret_
 __device__ __forceinline__ Frag<false> row8(const float *p) {
     return {*reinterpret_cast<const f32x4 *>(p), *reinterpret_cast<const f32x4 *>(p + 4)};
 }
-template <bool BF> __device__ __forceinline__ Frag<BF> zero8();
-template <> __device__ __forceinline__ Frag<true> zero8<true>() {
-    return {__builtin_bit_cast(bf16x8, uint4{0u, 0u, 0u, 0u})};
+// Sixteen bytes in registers, and their load from global memory (said so
+// explicitly: a pointer picked from several would be read by flat loads, which
+// also hold up LDS waits).
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ u32x4 load16(const void *p) {
+    return *(const __attribute__((address_space(1))) u32x4 *)p;
 }
-template <> __device__ __forceinline__ Frag<false> zero8<false>() { return {zero4(), zero4()}; }
+// sixteen bytes of zeros: where padding columns and absent rows are loaded from
+__device__ const u32x4 mla_zeros = {0u, 0u, 0u, 0u};
+
+// row8 from global memory, zeros unless `in`: chosen by address, since a load
+// behind a branch is waited for before the next is requested.
+__device__ __forceinline__ Frag<true> row8_if(bool in, const u16 *p) {
+    return {__builtin_bit_cast(bf16x8, load16(in ? (const void *)p : (const void *)&mla_zeros))};
+}
+__device__ __forceinline__ Frag<false> row8_if(bool in, const float *p) {
+    return {__builtin_bit_cast(f32x4, load16(in ? (const void *)p : (const void *)&mla_zeros)),
+            __builtin_bit_cast(f32x4, load16(in ? (const void *)(p + 4) : (const void *)&mla_zeros))};
+}
 
 // sum of the eight products, in fp32
 __device__ __forceinline__ float dot8(const Frag<true> &a, const Frag<true> &b) {
@@ -319,16 +334,6 @@ template <bool BF, int N> struct Frags {
         for (int v = 0; v < N; ++v) f[v] = col8(X, ld, k0, m0 + 16 * v, lane);
     }
 };
-
-// Sixteen bytes in registers, and their load from global memory (said so
-// explicitly: a pointer picked from several would be read by flat loads, which
-// also hold up LDS waits).
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ u32x4 load16(const void *p) {
-    return *(const __attribute__((address_space(1))) u32x4 *)p;
-}
-// sixteen bytes of zeros: where padding columns and absent rows are loaded from
-__device__ const u32x4 mla_zeros = {0u, 0u, 0u, 0u};
 
 // Rows of a sequence, NR at a time, from global memory over registers into an
 // LDS tile [NR][ld]: columns 0 .. d0 - 1 from x0, d0 .. d0 + d1 - 1 from x1

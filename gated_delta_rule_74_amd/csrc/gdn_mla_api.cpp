@@ -136,7 +136,7 @@ gdn_status_t check_step(const gdn_mla_step_shape_t *s) {
         (double)s->N * s->max_pages >= LIMIT)
         return fail(GDN_EINVAL, "cache or table too large");
     if ((double)s->N * s->S * s->H * (s->dl + s->dr) >= LIMIT ||
-        (double)s->N * s->max_pages * s->page_size / 64 + s->N >= LIMIT / 2)
+        (double)s->N * s->max_pages * s->page_size / 32 + s->N >= LIMIT / 2)
         return fail(GDN_EINVAL, "tokens too large");
     if (!(s->scale > 0.f) || !isfinite(s->scale)) return fail(GDN_EINVAL, "scale must be positive and finite");
     return GDN_OK;

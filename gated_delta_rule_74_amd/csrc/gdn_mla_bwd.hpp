@@ -67,21 +67,17 @@ __device__ __forceinline__ void mla_bwd_q_block(const MlaBwdArgs a, int bh, int 
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
             const int c = 32 * k + 8 * g;
-            Q[t][k] = (live && c < D) ? row8(qp + (size_t)i * rq + c) : zero8<BF>();
+            Q[t][k] = row8_if(live && c < D, qp + (size_t)i * rq + c);
         }
         float d = 0.f;
 #pragma unroll
         for (int k = 0; k < VS; ++k) {
             const int c = 32 * k + 8 * g;
-            G[t][k] = zero8<BF>();
-            if (live && c < s.dv) {
-                G[t][k] = row8(gp + (size_t)i * ro + c);
-                const Frag<BF> o = row8(op + (size_t)i * ro + c);
-                d += dot8(G[t][k], o);
-            }
+            G[t][k] = row8_if(live && c < s.dv, gp + (size_t)i * ro + c);
+            d += dot8(G[t][k], row8_if(live && c < s.dv, op + (size_t)i * ro + c));
         }
+        const float saved = a.lse[((size_t)b * s.Tq + min(i, s.Tq - 1)) * s.H + h], ls = live ? saved : -INFINITY;
         delta[t] = sum4g(d);
-        const float ls = live ? a.lse[((size_t)b * s.Tq + i) * s.H + h] : -INFINITY;
         // a row without keys: every probability is exp2(z - inf) = 0
         lse2[t] = ls == -INFINITY ? INFINITY : ls * (float)LOG2E;
     }
@@ -286,13 +282,12 @@ __device__ __forceinline__ void mla_bwd_k_block(const MlaBwdArgs a, int bh, int 
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
             const int c = 32 * k + 8 * g;
-            K[t][k] = zero8<BF>();
-            if (j < n && c < D) K[t][k] = row8(c < s.dn ? kp + (size_t)j * rk + c : krp + (size_t)j * rr + (c - s.dn));
+            K[t][k] = row8_if(j < n && c < D, c < s.dn ? kp + (size_t)j * rk + c : krp + (size_t)j * rr + (c - s.dn));
         }
 #pragma unroll
         for (int k = 0; k < VS; ++k) {
             const int c = 32 * k + 8 * g;
-            V[t][k] = (j < n && c < s.dv) ? row8(vp + (size_t)j * rv + c) : zero8<BF>();
+            V[t][k] = row8_if(j < n && c < s.dv, vp + (size_t)j * rv + c);
         }
     }
     f32x4 dK[KT][MD], dV[KT][MV];

@@ -18,7 +18,7 @@
 // loss; this keeps the cross-lane maximum and the rescaling of O out of almost
 // every tile.
 // Wide heads (192 | 128) run at 0.8 of the rate a large matrix product reaches
-// (8 heads on 1, T 16384: 1.41 ms); at 96 | 64 the exponentials and the mask
+// (T 16384, 16 heads on 4: 1.41 ms); at 96 | 64 the exponentials and the mask
 // take as long as the products (B8 H16 T4096: 0.46 ms, 0.54 of that rate). More
 // waves per SIMD (three, four) or value operands requested ahead do not change
 // either.
@@ -78,7 +78,7 @@ __device__ __forceinline__ void mla_fwd_block(const MlaFwdArgs a, int bh, int qb
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
             const int c = 32 * k + 8 * g;
-            Q[t][k] = (i < s.Tq && c < D) ? row8(qp + (size_t)i * rq + c) : zero8<BF>();
+            Q[t][k] = row8_if(i < s.Tq && c < D, qp + (size_t)i * rq + c);
         }
     }
     f32x4 O[QT][MV];

@@ -21,10 +21,9 @@
 
 namespace gdn {
 
-constexpr int STEP_TILE = 64; // a part is a whole number of these, two at least
 constexpr float STEP_RAISE = 8.f; // lazy maximum, as in the forward over expanded heads
 
-// How the cached rows are shared out. The sequences' tiles of STEP_TILE rows,
+// How the cached rows are shared out. The sequences' tiles (2^MlaStepArgs::tile rows),
 // end to end, are cut into equal shares, one per workgroup, whatever the single
 // lengths are: a batch of 256 lengths from 0 to 4096 took 51 us with each
 // sequence cut into four equal parts (some CUs had twice the work of others).
@@ -36,7 +35,7 @@ __device__ __forceinline__ int seq_rows(const MlaStepArgs &a, int n) {
     return (int)min((long long)max(a.lens[n], 0), (long long)a.cols * a.page);
 }
 __device__ __forceinline__ int seq_tiles(const MlaStepArgs &a, int n) {
-    return n < a.N ? (int)(((long long)seq_rows(a, n) + STEP_TILE - 1) / STEP_TILE) : 0;
+    return n < a.N ? (int)(((long long)seq_rows(a, n) + (1 << a.tile) - 1) >> a.tile) : 0;
 }
 struct Share {
     int share; // tiles per workgroup
@@ -57,7 +56,7 @@ __device__ __forceinline__ Share share_out(const MlaStepArgs &a, int lane) {
     }
     s.before = x - s.mine;
     s.total = __builtin_amdgcn_readlane(x, 63);
-    s.share = max((s.total + a.units - 1) / a.units, 2);
+    s.share = max((s.total + a.units - 1) / a.units, 1);
     return s;
 }
 // where workgroup w leaves its part of a sequence whose tiles begin at `begin`
@@ -66,19 +65,23 @@ __device__ __forceinline__ int part_slot(int w, int begin, int share) { return 2
 // A tile holds KT rows; a wave takes KW of them (32 bf16 rows fill one MFMA's
 // K, 16 fp32 rows four) and DLP / WR columns. In bf16 two key groups times two
 // column groups: the scores are formed twice, which is nothing beside the
-// memory, and leaves a wave few enough registers for three waves per SIMD;
-// those hide a piece's start and end. In fp32 the products are what takes the
-// time (a sixteenth of the bf16 rate), so up to 192 columns four key groups form
-// each score once (256 sequences of 128 + 32: 124 us with two groups, 103 with
-// four); beyond, the accumulators of all columns do not fit a wave.
+// memory, and leaves a wave few enough registers for two or three waves per
+// SIMD; those hide a piece's start and end. In fp32 the products are what takes
+// the time (a sixteenth of the bf16 rate), so up to 256 columns four key groups
+// form each score once (8 sequences of 30000 rows of 256 + 64, 32 queries: 104
+// us with two groups, 85 with four); beyond, the accumulators of all columns do
+// not fit a wave.
 template <bool BF, int DLP, int MT> struct StepShape {
     using S = typename Op<BF>::S;
-        static constexpr int WK = !BF && DLP <= 192 ? 4 : 2, WR = 4 / WK, KW = BF && DLP <= 256 ? 32 : 16, KT = KW * WK, NJ = KW / 16, NT = 256, V = Op<BF>::VEC,
-                         DP = DLP + 64, LD = DP + Op<BF>::PAD, MV = DLP / 16 / WR, KS = DP / 32,
-                         RP = NT / (DP / V) > 0 ? NT / (DP / V) : 1, NIT = (KT + RP - 1) / RP,
-                         TILE_B = KT * LD * (int)sizeof(S), MERGE_B = 4 * MT * MV * WR * 64 * 4;
-    // queries in registers (bf16), or in LDS where they would take most of them
-    static constexpr bool QL = !BF;
+    static constexpr int WK = !BF && DLP <= 256 ? 4 : 2, WR = 4 / WK, KW = BF && DLP <= 256 ? 32 : 16, KT = KW * WK,
+                         NJ = KW / 16, NT = 256, V = Op<BF>::VEC, DP = DLP + 64, LD = DP + Op<BF>::PAD,
+                         MV = DLP / 16 / WR, MP = MV / WK, KS = DP / 32, RP = NT / (DP / V) > 0 ? NT / (DP / V) : 1,
+                         NIT = (KT + RP - 1) / RP, TILE_B = KT * LD * (int)sizeof(S), MERGE_B = 4 * MT * MP * 64 * 16;
+    // The queries' operands stay in registers where those hold them without
+    // crowding the rows in flight, else in LDS (bf16 256 + 64, 32 queries, as
+    // above: 56 us in registers, 36 in LDS; 512 + 64, 16 queries, 200 sequences
+    // up to 1000 rows: 53 and 49).
+    static constexpr bool QL = !BF || DLP * MT >= 256;
 };
 
 typedef short short8_t __attribute__((ext_vector_type(8)));
@@ -172,19 +175,30 @@ __device__ __forceinline__ void step_piece(const MlaStepArgs a, int nq, int k0, 
 #pragma unroll
             for (int k = 0; k < P::KS; ++k) {
                 const int c = 32 * k + 8 * g;
-                Q[t][k] = (i < rows && c < d) ? row8(qp + (size_t)i * d + c) : zero8<BF>();
+                Q[t][k] = row8_if(i < rows && c < d, qp + (size_t)i * d + c);
             }
         }
     }
     if constexpr (P::QL) {
         lds_barrier(); // (the previous piece's readers are done)
-        for (int e = tid; e < MT * 16 * (P::DP / P::V); e += P::NT) {
-            const int i = e / (P::DP / P::V), c = e % (P::DP / P::V) * P::V;
-            uint4 x = uint4{0u, 0u, 0u, 0u};
-            if (row0 + i < rows && c < d) x = *reinterpret_cast<const uint4 *>(qp + (size_t)(row0 + i) * d + c);
-            *reinterpret_cast<uint4 *>(Qs + i * P::LD + c) = x;
+        constexpr int NV = P::DP / P::V, NQ = (MT * 16 * NV + P::NT - 1) / P::NT;
+        u32x4 x[NQ]; // all requested before the first is waited for
+#pragma unroll
+        for (int k = 0; k < NQ; ++k) {
+            const int e = tid + k * P::NT, i = row0 + e / NV, c = e % NV * P::V;
+            x[k] = load16(e < MT * 16 * NV && i < rows && c < d ? (const void *)(qp + (size_t)i * d + c)
+                                                                : (const void *)&mla_zeros);
+        }
+#pragma unroll
+        for (int k = 0; k < NQ; ++k) {
+            const int e = tid + k * P::NT;
+            if (e < MT * 16 * NV) *reinterpret_cast<u32x4 *>(Qs + e / NV * P::LD + e % NV * P::V) = x[k];
         }
     }
+    lds_barrier(); // (the previous piece's readers are done)
+    // columns past d are never stored below: zero once
+    for (int w = (P::DP - d) / P::V, e = tid; e < P::KT * w; e += P::NT)
+        *reinterpret_cast<u32x4 *>(T + e / w * P::LD + d + e % w * P::V) = u32x4{0u, 0u, 0u, 0u};
     f32x4 O[MT][P::MV];
     float m[MT], l[MT];
 #pragma unroll
@@ -194,9 +208,6 @@ __device__ __forceinline__ void step_piece(const MlaStepArgs a, int nq, int k0, 
 #pragma unroll
         for (int v = 0; v < P::MV; ++v) O[t][v] = zero4();
     }
-    lds_barrier(); // (the previous piece's readers are done)
-    // columns past d are never stored below: zero once
-    for (int e = tid; e < P::TILE_B / 16; e += P::NT) ((u32x4 *)smem)[e] = u32x4{0u, 0u, 0u, 0u};
     const float c2 = a.scale * (float)LOG2E;
     wait_vmem(); // (what is held is there: else its first use in the loop waits for the tile in flight)
     ask(k0 + P::KT);
@@ -313,25 +324,30 @@ __device__ __forceinline__ void step_piece(const MlaStepArgs a, int nq, int k0, 
         ml[t] = mm;
         sl[t] = sm;
     }
-    f32x4 *X = (f32x4 *)smem + wr * MT * P::MV * 64;
+    // Every group ends with the sums of its own part of the columns: in round w it
+    // hands the one w groups on its part and adds what it is handed.
+    f32x4 *X = (f32x4 *)smem + lane;
 #pragma unroll 1
     for (int w = 1; w < P::WK; ++w) {
-        if (kw == w) {
+        if (w > 1) lds_barrier(); // the previous round's readers are done
+#pragma unroll
+        for (int p = 0; p < P::WK; ++p) {
+            if ((kw + w) % P::WK != p) continue;
 #pragma unroll
             for (int t = 0; t < MT; ++t)
 #pragma unroll
-                for (int v = 0; v < P::MV; ++v) X[(t * P::MV + v) * 64 + lane] = O[t][v];
+                for (int v = 0; v < P::MP; ++v) X[(((wr * P::WK + p) * MT + t) * P::MP + v) * 64] = O[t][p * P::MP + v];
         }
         lds_barrier();
-        if (kw == 0) {
+#pragma unroll
+        for (int p = 0; p < P::WK; ++p) {
+            if (kw != p) continue;
 #pragma unroll
             for (int t = 0; t < MT; ++t)
 #pragma unroll
-                for (int v = 0; v < P::MV; ++v) O[t][v] += X[(t * P::MV + v) * 64 + lane];
+                for (int v = 0; v < P::MP; ++v) O[t][p * P::MP + v] += X[(((wr * P::WK + p) * MT + t) * P::MP + v) * 64];
         }
-        if (w + 1 < P::WK) lds_barrier();
     }
-    if (kw != 0) return;
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
         const int i = row0 + 16 * t + r;
@@ -341,11 +357,11 @@ __device__ __forceinline__ void step_piece(const MlaStepArgs a, int nq, int k0, 
 #pragma unroll
         for (int v = 0; v < P::MV; ++v) {
             const int c = 16 * (wr * P::MV + v) + 4 * g;
-            if (c >= a.dl) continue;
+            if (v / P::MP != kw || c >= a.dl) continue;
             if (slot >= 0) store4(a.part + ((size_t)slot * rows + i) * a.dl + c, O[t][v]);
             else store4((S *)a.o + out * a.dl + c, O[t][v] * inv);
         }
-        if (wr == 0 && g == 0) {
+        if (wave == 0 && g == 0) {
             if (slot >= 0) {
                 *reinterpret_cast<f32x2 *>(a.part_ml + ((size_t)slot * rows + i) * 2) = f32x2{ml[t], sl[t]};
             } else if (a.lse) {
@@ -356,7 +372,7 @@ __device__ __forceinline__ void step_piece(const MlaStepArgs a, int nq, int k0, 
 }
 
 template <bool BF, int DLP, int MT>
-__global__ __launch_bounds__(256, (DLP <= 128 && MT == 1 ? 3 : 2)) void mla_step_kernel(MlaStepArgs a) {
+__global__ __launch_bounds__(256, (DLP <= 128 && MT == 1 ? 3 : !BF && DLP == 256 ? 1 : 2)) void mla_step_kernel(MlaStepArgs a) {
     using P = StepShape<BF, DLP, MT>;
     using S = typename P::S;
     __shared__ __align__(16) unsigned char smem[P::TILE_B > P::MERGE_B ? P::TILE_B : P::MERGE_B];
@@ -382,7 +398,7 @@ __global__ __launch_bounds__(256, (DLP <= 128 && MT == 1 ? 3 : 2)) void mla_step
             tiles = seq_tiles(a, ++nq);
         }
         const int stop = min(begin + tiles, to);
-        step_piece<BF, DLP, MT>(a, nq, (at - begin) * STEP_TILE, (stop - begin) * STEP_TILE, row0,
+        step_piece<BF, DLP, MT>(a, nq, (at - begin) << a.tile, (stop - begin) << a.tile, row0,
                                 at == begin && stop == begin + tiles ? -1 : part_slot(unit, begin, sh.share), smem, Qs,
                                 bias, Ms, Ss);
         at = stop;
@@ -466,11 +482,14 @@ template <bool BF> __global__ __launch_bounds__(256) void mla_join_kernel(MlaSte
 
 static int step_class(int dl) { return dl <= 64 ? 64 : dl <= 128 ? 128 : dl <= 192 ? 192 : dl <= 256 ? 256 : dl <= 384 ? 384 : 512; }
 
+// log2 of a tile's rows (StepShape::KT)
+static int step_tile(int dl) { return step_class(dl) <= 256 ? 6 : 5; }
+
 // workgroups a CU holds at once, by their registers and LDS
 static int step_per_cu(const MlaStepArgs &a, bool bf16) {
     const int c = step_class(a.dl);
     if (bf16) return c == 64 ? 5 - a.mt : c == 128 ? 4 - a.mt : 2;
-    return c == 64 ? 3 : c == 128 ? 2 : c == 256 ? 3 - a.mt : 1;
+    return c == 64 ? 3 : c == 128 ? 2 : 1;
 }
 
 void mla_step_plan(MlaStepArgs &a, bool bf16, int cus) {
@@ -478,9 +497,10 @@ void mla_step_plan(MlaStepArgs &a, bool bf16, int cus) {
     // query blocks per workgroup: two where the registers hold them
     a.mt = rows > 16 && a.dl <= 256 ? 2 : 1;
     const long long rb = (rows + 16 * a.mt - 1) / (16 * a.mt), cap = (long long)a.cols * a.page;
-    // as many shares as the chip holds, no share under two tiles
+    a.tile = step_tile(a.dl);
+    // as many shares as the chip holds, each a tile or more
     long long n = (long long)cus * step_per_cu(a, bf16) / rb;
-    const long long most = a.N * ((cap + 2 * STEP_TILE - 1) / (2 * STEP_TILE));
+    const long long most = a.N * ((cap + (1 << a.tile) - 1) >> a.tile);
     if (n > most) n = most;
     a.units = n < 1 ? 1 : (int)n;
 }
