@@ -17,13 +17,20 @@
 // the walked tiles are read row by row for the first two products and by
 // transposing reads for the last. The sums P and dS enter in bf16 (rounded to
 // nearest even) when the tensors are bf16; everything else is fp32.
+// S and dP are formed in both kernels: seven products instead of five, for
+// which no sum needs atomics or a second pass. Bound by the matrix products
+// and, at narrow heads, as much by the exponentials and the reads of LDS:
+// B8 H16 T4096 56 + 32 | 56 0.68 + 0.83 ms (0.6 of the rate a large product
+// reaches), T16384 16 heads on 4, 128 + 64 | 128 2.10 + 3.06 ms (0.77 of it).
 #pragma once
 
 #include "gdn_mla.hpp"
 
 namespace gdn {
 
-constexpr int MLA_EXACT = 256; // blocks that see at most so many keys form delta from the products
+// Blocks that see at most so many keys form delta from the products, at the
+// price of a second walk over them.
+constexpr int MLA_EXACT = 256;
 
 // dq of block qb of the queries of head bh, and their delta.
 template <bool BF, int DP, int DVP, int NW, int QT, int WS, class S>
@@ -31,7 +38,8 @@ __device__ __forceinline__ void mla_bwd_q_block(const MlaBwdArgs a, int bh, int 
     constexpr int LDK = DP + Op<BF>::PAD, LDV = DVP + Op<BF>::PAD, NT = NW * 64, KS = DP / 32, VS = DVP / 32,
                   MD = DP / 16;
     const MlaArgs s = a.s;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15,
+              g = lane >> 4;
     constexpr int QB = NW / WS * QT * 16, BT = mla_tile(WS);
     const int wg = wave / WS, wu = wave % WS; // the wave's queries, its part of each tile
     const int b = bh / s.H, h = bh % s.H, hk = h / (s.H / s.Hk);
@@ -146,11 +154,13 @@ __device__ __forceinline__ void mla_bwd_q_block(const MlaBwdArgs a, int bh, int 
         const bool mask = key0 + BT - 1 > wfirst || key0 + BT > n;
 #pragma unroll 1
         for (int u = wu; u < nu; u += WS) {
-            f32x4 P[QT][2], dP[QT][2];
+            // sixteen keys at a time: dP of only so many is held (192 | 128: 2.29 ms with all 32, 2.10 so; T 16384)
+            f32x4 P[QT][2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
+                f32x4 dP[QT];
 #pragma unroll
-                for (int t = 0; t < QT; ++t) P[t][j] = dP[t][j] = zero4();
+                for (int t = 0; t < QT; ++t) P[t][j] = dP[t] = zero4();
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
                     const Frag<BF> kf = row8(Ks + (32 * u + 16 * j + r) * LDK + 32 * k + 8 * g);
@@ -161,26 +171,21 @@ __device__ __forceinline__ void mla_bwd_q_block(const MlaBwdArgs a, int bh, int 
                 for (int k = 0; k < VS; ++k) {
                     const Frag<BF> vf = row8(Vs + (32 * u + 16 * j + r) * LDV + 32 * k + 8 * g);
 #pragma unroll
-                    for (int t = 0; t < QT; ++t) dP[t][j] = mma8(vf, G[t][k], dP[t][j]);
+                    for (int t = 0; t < QT; ++t) dP[t] = mma8(vf, G[t][k], dP[t]);
                 }
+#pragma unroll
+                for (int t = 0; t < QT; ++t) {
+                    const int lim = mask ? min(q0 + 16 * t + r + off, n - 1) - key0 - 32 * u - 16 * j - 4 * g : 3;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        P[t][j][e] =
+                            exp2_fast(fmaf(e <= lim ? P[t][j][e] : -INFINITY, c2, -lse2[t])) * (dP[t][e] - delta[t]);
+                }
+                in_flight();
             }
             Frag<BF> ds[QT];
 #pragma unroll
-            for (int t = 0; t < QT; ++t) {
-                if (mask) {
-                    const int lim = min(q0 + 16 * t + r + off, n - 1) - key0 - 32 * u - 4 * g;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) P[t][j][e] = 16 * j + e <= lim ? P[t][j][e] : -INFINITY;
-                }
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        P[t][j][e] = exp2_fast(fmaf(P[t][j][e], c2, -lse2[t])) * (dP[t][j][e] - delta[t]);
-                ds[t] = acc8<BF>(P[t][0], P[t][1]);
-            }
+            for (int t = 0; t < QT; ++t) ds[t] = acc8<BF>(P[t][0], P[t][1]);
 #pragma unroll
             for (int v = 0; v < MD; ++v) {
                 const Frag<BF> kf = col8(Ks, LDK, 32 * u, 16 * v, lane);
@@ -238,7 +243,8 @@ __device__ __forceinline__ void mla_bwd_k_block(const MlaBwdArgs a, int bh, int 
     constexpr int LDQ = DP + Op<BF>::PAD, LDG = DVP + Op<BF>::PAD, NT = NW * 64, KS = DP / 32, VS = DVP / 32,
                   MD = DP / 16, MV = DVP / 16;
     const MlaArgs s = a.s;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15,
+              g = lane >> 4;
     constexpr int KB = NW / WS * KT * 16, BT = mla_tile(WS);
     const int wg = wave / WS, wu = wave % WS; // the wave's keys, its part of each tile
     const int b = bh / s.Hk, hk = bh % s.Hk, per = s.H / s.Hk;

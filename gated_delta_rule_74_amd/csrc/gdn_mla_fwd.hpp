@@ -43,7 +43,8 @@ __device__ __forceinline__ void mla_fwd_block(const MlaFwdArgs a, int bh, int qb
     using H = MlaFwdShape<BF, DP, DVP, NW, QT, WS>;
     constexpr int LDK = H::LDK, LDV = H::LDV, NB = H::NB, NT = NW * 64, KS = DP / 32, MV = DVP / 16;
     const MlaArgs s = a.s;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15,
+              g = lane >> 4;
     constexpr int QB = H::QB, BT = H::BT;
     const int wg = wave / WS, wu = wave % WS; // the wave's queries, its part of each tile
     const int b = bh / s.H, h = bh % s.H, hk = h / (s.H / s.Hk);

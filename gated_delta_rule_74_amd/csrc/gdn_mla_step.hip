@@ -17,6 +17,11 @@
 // forward pass over expanded heads the products are formed transposed: a lane
 // owns one query, and the probabilities are at once the operand of the second
 // product, whose other operand is read from the same tile by transposing reads.
+// Bound by the cache's bytes with what a workgroup has in flight (two or three
+// waves per SIMD, a tile each): 256 sequences of 0 to 4096 rows of 128 + 32
+// bf16 in 41 us and 4 us for the join, 4.1 TB/s where a large copy reaches 5.6;
+// one of 131072 rows of 512 + 64 in 33 us and 9 us, 4.6 TB/s. In fp32 by the
+// matrix products (48 drafts of three tokens, 8 heads of 256 + 64: 42 us).
 #include "gdn_mla.hpp"
 
 namespace gdn {
@@ -480,7 +485,9 @@ template <bool BF> __global__ __launch_bounds__(256) void mla_join_kernel(MlaSte
     if (a.lse && c == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
 }
 
-static int step_class(int dl) { return dl <= 64 ? 64 : dl <= 128 ? 128 : dl <= 192 ? 192 : dl <= 256 ? 256 : dl <= 384 ? 384 : 512; }
+static int step_class(int dl) {
+    return dl <= 64 ? 64 : dl <= 128 ? 128 : dl <= 192 ? 192 : dl <= 256 ? 256 : dl <= 384 ? 384 : 512;
+}
 
 // log2 of a tile's rows (StepShape::KT)
 static int step_tile(int dl) { return step_class(dl) <= 256 ? 6 : 5; }
