@@ -99,6 +99,13 @@ struct PagePlanArgs {
     int N, cols, F, page, cap;
 };
 
+// Elements between the rows of an LDS tile beside its columns. bf16: row strides
+// of an odd number of 32-byte groups, so that the 32-byte pieces of eight rows
+// that a transposing read touches lie in all 64 banks (B2 H16 T2048, forward and
+// backward: 227 us with 8 elements, 210 with 16; T16384, 128 + 64 | 128: 6.56
+// and 6.46 ms).
+template <bool BF> constexpr int MLA_PAD = BF ? 16 : 4;
+
 // How the attention launches share out their blocks (MI355X: 256 CUs).
 // A causal walk is as long as its block is late, so two blocks of opposite
 // length make one workgroup (MlaArgs::pair) once that still leaves one for
@@ -128,7 +135,7 @@ constexpr int mla_waves(int dp, int dvp) { return dp + dvp > 224 ? 8 : 4; }
 // with four; T2048: 186, 126, 104; T512, 16 heads: 19, 16, 20).
 constexpr int mla_tile(int split) { return split == 4 ? 128 : 64; }
 template <bool BF> constexpr bool mla_fits4(int dp, int dvp) { // (the tiles in LDS)
-    return mla_tile(4) * (dp + dvp + 2 * Op<BF>::PAD) * (int)sizeof(typename Op<BF>::S) <= 96 * 1024;
+    return mla_tile(4) * (dp + dvp + 2 * MLA_PAD<BF>) * (int)sizeof(typename Op<BF>::S) <= 96 * 1024;
 }
 template <bool BF> int mla_split(long long heads, long long n, long long walk, int dp, int dvp) {
     const long long w = heads * mla_blocks(n, 16);

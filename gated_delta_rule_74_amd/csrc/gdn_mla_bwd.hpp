@@ -35,7 +35,7 @@ constexpr int MLA_EXACT = 256;
 // dq of block qb of the queries of head bh, and their delta.
 template <bool BF, int DP, int DVP, int NW, int QT, int WS, class S>
 __device__ __forceinline__ void mla_bwd_q_block(const MlaBwdArgs a, int bh, int qb, S *Ks, S *Vs, float *Dx) {
-    constexpr int LDK = DP + Op<BF>::PAD, LDV = DVP + Op<BF>::PAD, NT = NW * 64, KS = DP / 32, VS = DVP / 32,
+    constexpr int LDK = DP + MLA_PAD<BF>, LDV = DVP + MLA_PAD<BF>, NT = NW * 64, KS = DP / 32, VS = DVP / 32,
                   MD = DP / 16;
     const MlaArgs s = a.s;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15,
@@ -215,8 +215,8 @@ template <bool BF, int DP, int DVP, int NW, int QT, int WS>
 __global__ __launch_bounds__(NW * 64, WS == 4 ? 1 : 2) void mla_bwd_q_kernel(MlaBwdArgs a) {
     using S = typename Op<BF>::S;
     constexpr int QB = NW / WS * QT * 16, BT = mla_tile(WS);
-    __shared__ __align__(16) S Ks[BT * (DP + Op<BF>::PAD)];
-    __shared__ __align__(16) S Vs[BT * (DVP + Op<BF>::PAD)];
+    __shared__ __align__(16) S Ks[BT * (DP + MLA_PAD<BF>)];
+    __shared__ __align__(16) S Vs[BT * (DVP + MLA_PAD<BF>)];
     __shared__ float Dx[WS > 1 ? NW * QT * 16 : 1];
     const int nqb = (a.s.Tq + QB - 1) / QB, work = a.s.pair ? (nqb + 1) / 2 : nqb;
     int bh, i;
@@ -240,7 +240,7 @@ __device__ __forceinline__ void times(f32x4 (&x)[T][2], int j, const Frags<BF, N
 template <bool BF, int DP, int DVP, int NW, int KT, int WS, class S>
 __device__ __forceinline__ void mla_bwd_k_block(const MlaBwdArgs a, int bh, int kb, S *Qs, S *Gs, float *Ls,
                                                 float *Ds) {
-    constexpr int LDQ = DP + Op<BF>::PAD, LDG = DVP + Op<BF>::PAD, NT = NW * 64, KS = DP / 32, VS = DVP / 32,
+    constexpr int LDQ = DP + MLA_PAD<BF>, LDG = DVP + MLA_PAD<BF>, NT = NW * 64, KS = DP / 32, VS = DVP / 32,
                   MD = DP / 16, MV = DVP / 16;
     const MlaArgs s = a.s;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15,
@@ -441,8 +441,8 @@ template <bool BF, int DP, int DVP, int NW, int KT, int WS>
 __global__ __launch_bounds__(NW * 64, WS == 4 ? 1 : mla_bwd_k_waves(KT, DP, DVP)) void mla_bwd_k_kernel(MlaBwdArgs a) {
     using S = typename Op<BF>::S;
     constexpr int KB = NW / WS * KT * 16, BT = mla_tile(WS);
-    __shared__ __align__(16) S Qs[BT * (DP + Op<BF>::PAD)];
-    __shared__ __align__(16) S Gs[BT * (DVP + Op<BF>::PAD)];
+    __shared__ __align__(16) S Qs[BT * (DP + MLA_PAD<BF>)];
+    __shared__ __align__(16) S Gs[BT * (DVP + MLA_PAD<BF>)];
     __shared__ __align__(16) float Ls[BT], Ds[BT];
     const int nkb = (a.s.Tk + KB - 1) / KB, work = a.s.pair ? (nkb + 1) / 2 : nkb;
     int bh, i;

@@ -32,7 +32,7 @@ constexpr float MLA_RAISE = 8.f; // see above
 
 template <bool BF, int DP, int DVP, int NW, int QT, int WS> struct MlaFwdShape {
     using S = typename Op<BF>::S;
-    static constexpr int LDK = DP + Op<BF>::PAD, LDV = DVP + Op<BF>::PAD, QB = NW / WS * QT * 16, BT = mla_tile(WS);
+    static constexpr int LDK = DP + MLA_PAD<BF>, LDV = DVP + MLA_PAD<BF>, QB = NW / WS * QT * 16, BT = mla_tile(WS);
     // two tiles where a second workgroup still fits the CU's 160 KB beside them
     static constexpr int NB = 2 * BT * (LDK + LDV) * (int)sizeof(S) <= 80 * 1024 ? 2 : 1;
 };

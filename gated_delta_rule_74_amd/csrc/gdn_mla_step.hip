@@ -79,7 +79,7 @@ __device__ __forceinline__ int part_slot(int w, int begin, int share) { return 2
 template <bool BF, int DLP, int MT> struct StepShape {
     using S = typename Op<BF>::S;
     static constexpr int WK = !BF && DLP <= 256 ? 4 : 2, WR = 4 / WK, KW = BF && DLP <= 256 ? 32 : 16, KT = KW * WK,
-                         NJ = KW / 16, NT = 256, V = Op<BF>::VEC, DP = DLP + 64, LD = DP + Op<BF>::PAD,
+                         NJ = KW / 16, NT = 256, V = Op<BF>::VEC, DP = DLP + 64, LD = DP + MLA_PAD<BF>,
                          MV = DLP / 16 / WR, MP = MV / WK, KS = DP / 32, RP = NT / (DP / V) > 0 ? NT / (DP / V) : 1,
                          NIT = (KT + RP - 1) / RP, TILE_B = KT * LD * (int)sizeof(S), MERGE_B = 4 * MT * MP * 64 * 16;
     // The queries' operands stay in registers where those hold them without
