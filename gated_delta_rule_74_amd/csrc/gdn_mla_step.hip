@@ -19,9 +19,10 @@
 // product, whose other operand is read from the same tile by transposing reads.
 // Bound by the cache's bytes with what a workgroup has in flight (two or three
 // waves per SIMD, a tile each): 256 sequences of 0 to 4096 rows of 128 + 32
-// bf16 in 41 us and 4 us for the join, 4.1 TB/s where a large copy reaches 5.6;
-// one of 131072 rows of 512 + 64 in 33 us and 9 us, 4.6 TB/s. In fp32 by the
-// matrix products (48 drafts of three tokens, 8 heads of 256 + 64: 42 us).
+// bf16 in 36 us and 6 us for the join, 4.7 TB/s where a large copy reaches 5.6;
+// one of 131072 rows of 512 + 64 in 34 us and 12 us, 4.5 TB/s. In fp32 by the
+// matrix products (48 drafts of three tokens up to 1500 rows, 8 heads of
+// 256 + 64: 38 us).
 #include "gdn_mla.hpp"
 
 namespace gdn {
@@ -500,14 +501,18 @@ static int step_per_cu(const MlaStepArgs &a, bool bf16) {
 }
 
 void mla_step_plan(MlaStepArgs &a, bool bf16, int cus) {
-    const long long rows = (long long)a.S * a.H;
-    // query blocks per workgroup: two where the registers hold them
-    a.mt = rows > 16 && a.dl <= 256 ? 2 : 1;
-    const long long rb = (rows + 16 * a.mt - 1) / (16 * a.mt), cap = (long long)a.cols * a.page;
+    const long long rows = (long long)a.S * a.H, cap = (long long)a.cols * a.page;
     a.tile = step_tile(a.dl);
+    const long long most = a.N * ((cap + (1 << a.tile) - 1) >> a.tile); // tiles there may be
+    // Query blocks per workgroup: two where the registers hold them and there may
+    // be twelve tiles for each CU, which pays for a longer start and end (fp32,
+    // 24 queries of 256 + 64, 48 sequences up to 1500 rows: 48 us with two, 42
+    // with one; up to 6000: 96 and 103); at 64 columns a block's rows cost too
+    // little to be shared (32 queries, 200 sequences up to 2000: 31 and 29 us).
+    a.mt = rows > 16 && a.dl > 64 && a.dl <= 256 && most >= 12LL * cus ? 2 : 1;
+    const long long rb = (rows + 16 * a.mt - 1) / (16 * a.mt);
     // as many shares as the chip holds, each a tile or more
     long long n = (long long)cus * step_per_cu(a, bf16) / rb;
-    const long long most = a.N * ((cap + (1 << a.tile) - 1) >> a.tile);
     if (n > most) n = most;
     a.units = n < 1 ? 1 : (int)n;
 }
@@ -518,7 +523,7 @@ template <bool BF, int DLP, int MT> static hipError_t step_run(const MlaStepArgs
     return hipGetLastError();
 }
 template <bool BF, int DLP> static hipError_t step_rows(const MlaStepArgs &a, hipStream_t st) {
-    if constexpr (DLP <= 256)
+    if constexpr (DLP > 64 && DLP <= 256)
         if (a.mt == 2) return step_run<BF, DLP, 2>(a, st);
     return step_run<BF, DLP, 1>(a, st);
 }

@@ -8,8 +8,10 @@
 // interleaved. All of it is bound by the bytes of x and y: a row (token, head)
 // is held by LPR lanes, eight columns each, in one read and one write; the
 // norm's sum goes over those lanes; a pair's other half is read again (it is
-// in L1, asked for together with the first). The sine and cosine of a token are formed once for all its heads, in
-// LDS. The angle is the product of position and frequency in fp64, reduced to
+// in L1, asked for together with the first). The sine and cosine of a token are
+// formed once for all its heads, in LDS. B8 T4096 H16 d88 bf16: forward 49 us
+// (3.8 TB/s), backward 60 us (4.6 TB/s) and 6 us for dw's sum, where a large
+// copy reaches 5.6. The angle is the product of position and frequency in fp64, reduced to
 // a fraction of a turn there, so that far positions lose nothing.
 #include "gdn_mla.hpp"
 
@@ -401,7 +403,8 @@ hipError_t launch_norm_sum(const NormRopeArgs &a, hipStream_t st) {
 // tokens, requested together; the pairs of the workgroup's tokens are shared
 // by all its threads (each pair's turn is needed once, so it is formed where
 // it is used). Slots outside the pool (-1: none) are skipped. Bound by the
-// rows' bytes.
+// rows' bytes (32768 rows of 512 + 64 bf16: 20 us, 3.9 TB/s; 256 rows: 4 us,
+// the launch).
 template <bool BF, int UN> __global__ __launch_bounds__(NR_THREADS) void mla_write_kernel(MlaWriteArgs a, int lpr) {
     using S = typename Op<BF>::S;
     const int slots = NR_THREADS / lpr, sub = threadIdx.x % lpr, d = a.dl + a.dr, hp = a.dr / 2;

@@ -228,6 +228,10 @@ STEP = [
     (130, 1, 4, 32, 8, 16, 40, [i * i % 641 for i in range(130)]),
     (67, 2, 2, 384, 16, 32, 8, [(37 * i) % 250 for i in range(67)]),
     (3, 1, 2, 192, 64, 64, 190, [12160, 5, 9001]),
+    # tables wide enough for two query blocks per workgroup
+    (6, 2, 12, 128, 40, 16, 2500, [700, 0, 33, 64, 2, 1]),
+    (5, 1, 40, 256, 64, 64, 700, [150, 1, 128, 0, 63]),
+    (4, 1, 20, 176, 8, 32, 1600, [129, 300, 31, 7]),
 ]
 
 
