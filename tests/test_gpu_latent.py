@@ -62,10 +62,13 @@ def test_attention(case, dtype):
     check_attn(case, dtype, 7900)
 
 
-# B, Tq, past, H, Hk, Hr, dn, dr, dv: enough heads that large and paired blocks are taken
+# B, Tq, past, H, Hk, Hr, dn, dr, dv: heads enough that every size of block is taken, paired and not
 MANY = [
     (16, 300, 37, 64, 64, 16, 56, 32, 56), (16, 300, 0, 64, 64, 16, 128, 64, 128), (64, 140, 0, 16, 8, 8, 32, 16, 40),
     (16, 257, 3, 64, 32, 32, 96, 24, 64), (16, 270, 0, 64, 64, 64, 32, 0, 32), (8, 270, 0, 64, 64, 16, 64, 0, 104),
+    # blocks of 64 rows: more than two for each CU, fewer
+    (4, 200, 0, 64, 64, 16, 56, 32, 56), (4, 200, 10, 64, 32, 16, 128, 64, 128), (4, 210, 0, 64, 64, 16, 32, 0, 24),
+    (2, 200, 0, 64, 64, 16, 56, 32, 56), (2, 190, 30, 64, 32, 16, 128, 64, 128), (2, 200, 0, 64, 64, 64, 104, 0, 64),
 ]
 
 
@@ -595,6 +598,45 @@ def test_calls_run_on_the_current_stream():
     s.synchronize()
     for n in want:
         assert torch.equal(got[n], want[n]), n
+
+
+def test_two_calls_at_once():
+    """Attention and paged steps on two streams at the same time, each with its own workspace."""
+    say("attention and step on two streams at once")
+    t, _, lens, scale = attn_inputs((2, 700, 0, 8, 4, 2, 56, 32, 56, [700, 333]), "bf16", 7951)
+    q, qf, c, cf, table, sc = paged((9, 1, 16, 128, 32, 64, 40, [2000, 5, 0, 800, 64, 65, 1, 2559, 7]), "bf16", 7952)
+    ln = ints([2000, 5, 0, 800, 64, 65, 1, 2559, 7])
+    table = ints(table)
+
+    def both():
+        return run_attn(t, lens, scale), gdn.mla_step(q, c, table, ln, 128, scale=sc)
+
+    want = both()
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [[], []]
+    for _ in range(5):
+        for s, out in zip(streams, got):
+            with torch.cuda.stream(s):
+                out.append(both())
+    torch.cuda.synchronize()
+    for r, (o, lse) in got[0] + got[1]:
+        for n in want[0]:
+            assert torch.equal(r[n], want[0][n]), n
+        assert torch.equal(o, want[1][0]) and torch.equal(lse, want[1][1])
+
+
+def test_autograd_with_broadcast_gradients_and_once():
+    """The gradient of a plain sum arrives broadcast; a second derivative is refused."""
+    say("autograd: sum, second derivative")
+    t, _, _, scale = attn_inputs((1, 33, 0, 2, 1, 1, 16, 8, 16, None), "fp32", 7953)
+    q, k, kr, v = (x.requires_grad_() for x in t[:4])
+    gdn.LatentAttention.apply(q, k, v, kr, None, scale).sum().backward()
+    want = run_attn([q.detach(), k.detach(), kr.detach(), v.detach(), torch.ones_like(t[4])], None, scale)
+    for x, n in ((q, "dq"), (k, "dk"), (kr, "dkr"), (v, "dv")):
+        assert torch.equal(x.grad, want[n]), n
+    g, = torch.autograd.grad(gdn.LatentAttention.apply(q, k, v, kr, None, scale).square().sum(), q, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
 
 
 def test_launches_are_bracketed():
