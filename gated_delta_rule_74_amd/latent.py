@@ -317,10 +317,11 @@ def page_plan(lens, new_lens, block_table, free_pages, n_free, page_size, max_to
     if max_tokens < 0:
         raise ValueError("max_tokens must be >= 0")
     cap = int(max_tokens)
-    granted, starts, slots, positions = torch.empty(2 * (N + cap) + 1, dtype=i32, device=dev).split(
-        [N, N + 1, cap, cap])
-    lens_out = torch.empty_like(lens) if lens_out is None else lens_out
-    n_free_out = torch.empty_like(n_free) if n_free_out is None else n_free_out
+    # one allocation for what the call makes
+    granted, starts, slots, positions, lens_new, n_free_new = torch.empty(
+        3 * N + 2 * cap + 2, dtype=i32, device=dev).split([N, N + 1, cap, cap, N, 1])
+    lens_out = lens_new if lens_out is None else lens_out
+    n_free_out = n_free_new if n_free_out is None else n_free_out
     with _on(dev):
         st = lib().gdn_page_plan(N, cols, free_pages.numel(), page_size, cap, _p(lens), _p(new_lens),
                                  _p(block_table), _p(free_pages), _p(n_free), _p(lens_out), _p(n_free_out),
