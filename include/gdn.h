@@ -237,7 +237,7 @@ gdn_status_t gdn_step_tokens(int32_t N, int32_t S, int32_t H, int32_t dk, int32_
  * allocation, bitwise reproducible results). Tensors are contiguous; q, k, v,
  * o, c, x, cache and their gradients are fp32 or bf16 as the call's dtype
  * says, sums and softmax statistics fp32. NaN/Inf in rows that take part
- * propagate (and within a tile of 64 keys may reach queries before them);
+ * propagate (and within a tile of up to 128 keys may reach queries before them);
  * rows at or past a length, and cache rows no table entry in use names, are
  * not read.
  */
