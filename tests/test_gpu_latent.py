@@ -418,6 +418,26 @@ def test_write(n, dl, dr, page, inter, norm, dtype):
     within("cache", cache.view(-1, dl + dr), want, np.where(touched[:, None], bound, 0))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("inter", [False, True])
+def test_write_without_frequencies_copies_the_rotary_key(inter, dtype):
+    """Infinities, NaN and negative zeros arrive as they are, beside any partner."""
+    say(f"cache write without frequencies, non-finite columns, {dtype}")
+    n, dl, dr = 9, 16, 8
+    c, _ = dev(rng(7931).standard_normal((n, dl)), dtype)
+    kr, _ = dev(rng(7932).standard_normal((n, dr)), dtype)
+    inf = float("inf")
+    for i, (col, x) in enumerate([(0, inf), (4, -inf), (7, float("nan")), (3, inf), (1, -0.0), (5, -0.0)]):
+        kr[i, col] = x
+    kr[6], kr[7, ::2] = inf, -inf
+    cache = torch.zeros((3, 4, dl + dr), dtype=TYPES[dtype], device="cuda")
+    slots = rng(7933).permutation(12)[:n]
+    gdn.mla_write(c, kr, ints(slots), cache, interleaved=inter)
+    bits = torch.int16 if dtype == "bf16" else torch.int32
+    got = cache.view(12, dl + dr)[torch.from_numpy(slots).cuda(), dl:].contiguous()
+    assert torch.equal(got.view(bits), kr.view(bits))
+
+
 def plan_inputs(seed, N, page, cols, most, free=None):
     g = rng(seed)
     F = N * cols + 1
