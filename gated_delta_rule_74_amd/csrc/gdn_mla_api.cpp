@@ -29,6 +29,9 @@ gdn_status_t hip_status(hipError_t e, const char *what) {
 size_t align_up(size_t x) { return (x + 255) & ~(size_t)255; }
 size_t esize(int dtype) { return dtype == GDN_BF16 ? 2 : 4; }
 constexpr double LIMIT = 2147483648.0; // elements of a tensor, workgroups of a launch
+// What the kernels add to a position or a count (a few tiles ahead, a thread's
+// run) must not pass int32: sizes that bound those stay so much below it.
+constexpr double AHEAD = 2048.0;
 constexpr int CUS = 256;               // compute units of the chip the kernels are built for
 
 // One buffer of a call.
@@ -132,7 +135,7 @@ gdn_status_t check_step(const gdn_mla_step_shape_t *s) {
         return fail(GDN_EUNSUPPORTED, "dl must be a multiple of 16 up to 512, dr one of 8 up to 64");
     if (s->pages < 1 || s->page_size < 1 || s->max_pages < 1)
         return fail(GDN_EINVAL, "pages, page_size and max_pages must be >= 1");
-    if ((double)s->pages * s->page_size >= LIMIT || (double)s->max_pages * s->page_size >= LIMIT ||
+    if ((double)s->pages * s->page_size >= LIMIT || (double)s->max_pages * s->page_size > LIMIT - AHEAD ||
         (double)s->N * s->max_pages >= LIMIT)
         return fail(GDN_EINVAL, "cache or table too large");
     if ((double)s->N * s->S * s->H * (s->dl + s->dr) >= LIMIT ||
@@ -447,7 +450,7 @@ gdn_status_t gdn_page_plan(int32_t N, int32_t max_pages, int32_t n_pages, int32_
                            int32_t *starts, int32_t *slots, int32_t *positions, void *stream) {
     if (N < 0 || max_pages < 1 || n_pages < 1 || page_size < 1 || max_tokens < 0)
         return fail(GDN_EINVAL, "N, max_tokens must be >= 0, max_pages, n_pages and page_size >= 1");
-    if ((double)N * max_pages >= LIMIT || max_tokens > 2147483647 - 255)
+    if ((double)N * max_pages > LIMIT - AHEAD || max_tokens > 2147483647 - 255)
         return fail(GDN_EINVAL, "table or token count too large");
     const size_t n = (size_t)N * 4;
     const Buf b[] = {{lens, n, "lens", 4, false, true},

@@ -275,8 +275,8 @@ gdn_status_t gdn_mla_bwd(const gdn_mla_shape_t *s, const void *q, const void *k,
  * int32 (page of each page_size tokens of a sequence), lens [N] int32 (cached
  * tokens, the S new ones included), o [N,S,H,dl], lse [N,S,H] fp32. dl: a
  * multiple of 16 up to 512; dr: one of 8 up to 64. pages * page_size and
- * max_pages * page_size stay below 2^31 (the cache itself may be larger than
- * 2^32 bytes). */
+ * N * max_pages stay below 2^31, max_pages * page_size is at most 2^31 - 2048
+ * (the cache itself may be larger than 2^32 bytes). */
 typedef struct {
     int32_t N, S, H, dl, dr, dtype, pages, page_size, max_pages;
     float scale;
@@ -345,7 +345,8 @@ gdn_status_t gdn_mla_write(int64_t n, int32_t dl, int32_t dr, int32_t dtype, uin
  *   lens_out [N]       lengths afterwards (may be lens)
  *   n_free_out [1]     free pages afterwards (may be n_free)
  * block_table and free_pages are updated in place; with separate lens_out and
- * n_free_out the same call again gives the same result. All int32. */
+ * n_free_out the same call again gives the same result. All int32;
+ * N * max_pages is at most 2^31 - 2048. */
 gdn_status_t gdn_page_plan(int32_t N, int32_t max_pages, int32_t n_pages, int32_t page_size, int32_t max_tokens,
                            const int32_t *lens, const int32_t *new_lens, int32_t *block_table, int32_t *free_pages,
                            const int32_t *n_free, int32_t *lens_out, int32_t *n_free_out, int32_t *granted,

@@ -97,6 +97,19 @@ def test_step_rejects_bad_buffers(L):  # noqa: F811
     assert step(L, N=0, over=none) == 0 and step(L, S=0, over=none) == 0
 
 
+def test_sizes_next_to_int32_are_refused(L):  # noqa: F811
+    """Positions are looked up a few tiles ahead, in int32: a context next to 2^31 would wrap there."""
+    ok = dict(N=1, H=1)
+    for page, cols, code in ((1024, 2 ** 21 - 2, EWORKSPACE), (1024, 2 ** 21 - 1, EINVAL)):
+        assert step(L, max_pages=cols, page_size=page, **ok) == code, cols
+        s = gdn.MlaStepShape(1, 1, 1, 32, 8, 1, 10, page, cols, 0.1)
+        assert (L.gdn_mla_step_workspace_size(ctypes.byref(s)) > 0) == (code == EWORKSPACE)
+    far = [ctypes.c_void_p((i + 1) << 40) for i in range(11)]  # (no two of them overlap)
+    for cols in (2 ** 31 - 1, 2 ** 31 - 2047):
+        assert L.gdn_page_plan(1, cols, 20, 16, 64, *far, None) == EINVAL
+        assert b"too large" in L.gdn_last_error_detail()
+
+
 def test_norm_rope_validation(L):  # noqa: F811
     def call(M=4, H=2, d=16, r=8, dtype=1, flags=1, eps=1e-6, x=fake(1), w=fake(2), pos=fake(3), fr=fake(4), y=fake(5)):
         return L.gdn_norm_rope(M, H, d, r, dtype, flags, eps, x, w, pos, fr, y, None)
