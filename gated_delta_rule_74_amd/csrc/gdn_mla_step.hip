@@ -466,7 +466,7 @@ template <bool BF> __global__ __launch_bounds__(256) void mla_join_kernel(MlaSte
         ms[tid] = m;
         ls[tid] = l;
         __syncthreads();
-        if (grp != 0) return;
+        if (grp != 0 || !on) return; // (threads left over have no parts, and none to read behind them)
         float mm = m;
         for (int k = 1; k < groups; ++k) mm = fmaxf(mm, ms[tid + k * wide]);
         f32x4 sum = zero4();

@@ -276,6 +276,18 @@ def test_step(case, dtype):
     assert torch.equal(again[0], o) and torch.equal(again[1], lse)
 
 
+@pytest.mark.parametrize("dl,H", [(48, 3), (80, 1), (112, 2), (176, 5), (336, 1), (496, 3)])
+def test_step_joins_widths_that_leave_threads_over(dl, H):
+    """One long sequence in many parts, its columns dealt to a number of threads that does not divide the workgroup."""
+    say(f"paged step, many parts of {dl} columns")
+    case = (1, 1, H, dl, 8, 64, 120, [7600])
+    q, qf, c, cf, table, scale = paged(case, "fp32", 7913)
+    o, lse = gdn.mla_step(q, c, ints(table), ints(case[-1]), dl, scale=scale)
+    wo, to, wl, tl = step(qf, cf, table, case[-1], dl, scale, "fp32")
+    within("o", o, wo, to)
+    within("lse", lse, wl, tl)
+
+
 def test_step_masks_pages_outside_the_pool():
     say("paged step, bad table entries inside the length")
     case = (2, 2, 4, 64, 8, 8, 12, [90, 33])
