@@ -28,7 +28,8 @@ gdn_status_t hip_status(hipError_t e, const char *what) {
 
 size_t align_up(size_t x) { return (x + 255) & ~(size_t)255; }
 size_t esize(int dtype) { return dtype == GDN_BF16 ? 2 : 4; }
-constexpr double LIMIT = 2147483648.0; // elements of a tensor, workgroups of a launch
+constexpr double LIMIT = 2147483648.0; // elements of a tensor
+constexpr double THREADS = 4294967296.0; // threads of a launch
 // What the kernels add to a position or a count (a few tiles ahead, a thread's
 // run) must not pass int32: sizes that bound those stay so much below it.
 constexpr double AHEAD = 2048.0;
@@ -77,9 +78,22 @@ gdn_status_t check_mla(const gdn_mla_shape_t *s) {
     if (s->dn % 8 || s->dr % 8 || s->dv % 8 || s->dn > 128 || s->dr > 64 || s->dv > 128)
         return fail(GDN_EUNSUPPORTED, "dn, dv must be multiples of 8 up to 128, dr one up to 64");
     if (!(s->scale > 0.f) || !isfinite(s->scale)) return fail(GDN_EINVAL, "scale must be positive and finite");
-    const double rows = (double)s->B * s->Tk;
-    const int w = s->dn + s->dr > s->dv ? s->dn + s->dr : s->dv;
-    if (rows * s->H * w >= LIMIT) return fail(GDN_EINVAL, "tensor too large");
+    // the elements of q, o, k, k_rope and v, each by itself (H may be many times Hk, Tk many times Tq)
+    const double qrows = (double)s->B * s->Tq * s->H, krows = (double)s->B * s->Tk * s->Hk;
+    const double rrows = s->dr > 0 ? (double)s->B * s->Tk * s->Hr : 0.0;
+    if (qrows * (s->dn + s->dr) >= LIMIT || qrows * s->dv >= LIMIT || krows * s->dn >= LIMIT ||
+        rrows * s->dr >= LIMIT || krows * s->dv >= LIMIT)
+        return fail(GDN_EINVAL, "tensor too large");
+    // threads of a launch: a workgroup for every head and 64 rows where there are many
+    gdn::MlaArgs a = {};
+    a.dn = s->dn;
+    a.dr = s->dr;
+    a.dv = s->dv;
+    const gdn::MlaPad pad = gdn::mla_pad(a);
+    const int wide = s->dtype == GDN_BF16 ? 64 * gdn::mla_waves(pad.d, pad.dv) : 256;
+    if ((double)s->B * s->H * ((s->Tq + 63) / 64) * wide >= THREADS ||
+        (double)s->B * s->Hk * ((s->Tk + 63) / 64) * 256 >= THREADS)
+        return fail(GDN_EINVAL, "too many heads for a launch");
     return GDN_OK;
 }
 

@@ -247,7 +247,8 @@ gdn_status_t gdn_step_tokens(int32_t N, int32_t S, int32_t H, int32_t dk, int32_
  * rotary head h / (H / Hr); Hk divides H and Hr divides Hk. dr = 0: no rotary
  * part (k_rope may be NULL, Hr is not read). dn, dv: multiples of 8 up to
  * 128; dr: one up to 64 (GDN_EUNSUPPORTED else). scale > 0. Tk >= Tq: the
- * queries are the last Tq of the Tk positions (a chunk after cached ones). */
+ * queries are the last Tq of the Tk positions (a chunk after cached ones).
+ * Every tensor has fewer than 2^31 elements. */
 typedef struct {
     int32_t B, Tq, Tk, H, Hk, Hr, dn, dr, dv, dtype;
     float scale;

@@ -115,6 +115,21 @@ def test_attention_beyond_32_bit_offsets():
         within(n, got[n][:, :, -1:], x, tol)
 
 
+def test_a_chunk_of_shared_heads_after_a_long_context():
+    """Few queries of many heads beside many keys of few: every tensor is small, B Tk H D is not."""
+    B, Tq, past, H, Hk, Hr, dn, dr, dv = 1, 24, 131072, 128, 16, 16, 128, 64, 128
+    say(f"attention {Tq} queries after {past} keys, {H} heads on {Hk}, bf16")
+    assert B * (Tq + past) * H * (dn + dr) >= 2 ** 31
+    gen = torch.Generator("cuda").manual_seed(7904)
+    q, k, kr, v, do = (torch.randn(s, device="cuda", generator=gen).bfloat16() for s in (
+        (B, Tq, H, dn + dr), (B, Tq + past, Hk, dn), (B, Tq + past, Hr, dr), (B, Tq + past, Hk, dv), (B, Tq, H, dv)))
+    scale = (dn + dr) ** -0.5
+    got = run_attn([q, k, kr, v, do], None, scale)
+    f = [host(x) for x in (q[:, :, -8:], k[:, :, -1:], kr[:, :, -1:], v[:, :, -1:], do[:, :, -8:])]
+    for n, (x, tol) in attention(*f[:4], None, scale, f[4], "bf16").items():
+        within(n, got[n][:, :, -x.shape[2]:], x, tol)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_attention_with_sharp_scores(dtype):
     """Scores far apart: the maximum moves late, most weights vanish."""

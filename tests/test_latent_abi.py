@@ -46,6 +46,25 @@ def test_attention_rejects_bad_shapes(L, key, val, code):  # noqa: F811
     assert L.gdn_mla_bwd_workspace_size(ctypes.byref(s)) == 0
 
 
+def test_attention_is_limited_by_its_tensors(L):  # noqa: F811
+    """Few key heads and few queries beside many keys: what counts is what each tensor holds."""
+    size = lambda s: L.gdn_mla_bwd_workspace_size(ctypes.byref(s))  # noqa: E731
+    chunk = dict(B=1, Tq=512, Tk=131584, H=128, Hk=16, Hr=1, dn=128, dr=64, dv=128)
+    assert size(mla(**chunk)) >= 4 * 128 * 512
+    assert size(mla(**{**chunk, "Tq": 1, "Tk": (1 << 20) - 1})) > 0
+    # one tensor at a time at its limit: q, o, k, k_rope, v
+    wide, tall = dict(B=1, H=256, Hk=256, Hr=1), dict(B=1, Tq=1, H=256, Hk=256, Hr=256)
+    for n, s in (("q", dict(wide, Tq=1 << 16, Tk=1 << 16, Hk=1, dn=64, dr=64, dv=8)),
+                 ("o", dict(wide, Tq=1 << 16, Tk=1 << 16, Hk=1, dn=8, dr=0, dv=128)),
+                 ("k", dict(tall, Tk=1 << 16, dn=128, dr=0, dv=8)), ("v", dict(tall, Tk=1 << 16, dn=8, dr=0, dv=128)),
+                 ("k_rope", dict(tall, Tk=1 << 17, dn=8, dr=64, dv=8))):
+        assert size(mla(**s)) == 0 and b"too large" in L.gdn_last_error_detail(), n
+        fewer = {k: s[k] - 1 for k in ("Tq", "Tk") if s.get(k, 0) > 1}
+        assert size(mla(**{**s, **fewer})) > 0, n
+    # more heads than a launch has workgroups
+    assert size(mla(B=1 << 20, H=16, Hk=16, Tq=1, Tk=1, dn=8, dr=0, dv=8)) == 0
+
+
 def test_attention_rejects_null_misaligned_aliased_and_small_workspaces(L):  # noqa: F811
     s = mla()
     need = L.gdn_mla_bwd_workspace_size(ctypes.byref(s))
