@@ -155,6 +155,7 @@ struct MlaPad {
 };
 MlaPad mla_pad(const MlaArgs &s);
 void mla_step_plan(MlaStepArgs &a, bool bf16, int cus); // sets mt and units from the sizes
+long long mla_step_groups(const MlaStepArgs &a);        // workgroups of the step's larger launch
 
 // workgroups of the backward of norm_rope: one row of dw partial sums each
 int norm_rope_blocks(long long rows, int d);

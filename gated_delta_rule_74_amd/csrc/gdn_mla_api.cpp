@@ -140,6 +140,22 @@ size_t mla_part_bytes(const gdn_mla_shape_t *s) {
     return s->dr > 0 && s->Hr < s->Hk ? align_up((size_t)s->B * s->Tk * s->Hk * s->dr * 4) : 0;
 }
 
+gdn::MlaStepArgs step_args(const gdn_mla_step_shape_t *s) {
+    gdn::MlaStepArgs a = {};
+    a.N = s->N;
+    a.S = s->S;
+    a.H = s->H;
+    a.dl = s->dl;
+    a.dr = s->dr;
+    a.pages = s->pages;
+    a.page = s->page_size;
+    a.cols = s->max_pages;
+    a.scale = s->scale;
+    if (s->N > 0 && s->S > 0) gdn::mla_step_plan(a, s->dtype == GDN_BF16, CUS);
+    else a.mt = a.units = 0;
+    return a;
+}
+
 gdn_status_t check_step(const gdn_mla_step_shape_t *s) {
     if (!s) return fail(GDN_EINVAL, "shape is NULL");
     if (s->N < 0 || s->S < 0 || s->H < 1) return fail(GDN_EINVAL, "N, S must be >= 0 and H >= 1");
@@ -156,22 +172,9 @@ gdn_status_t check_step(const gdn_mla_step_shape_t *s) {
         (double)s->N * s->max_pages * s->page_size / 32 + s->N >= LIMIT / 2)
         return fail(GDN_EINVAL, "tokens too large");
     if (!(s->scale > 0.f) || !isfinite(s->scale)) return fail(GDN_EINVAL, "scale must be positive and finite");
+    if ((double)gdn::mla_step_groups(step_args(s)) * 256 >= THREADS)
+        return fail(GDN_EINVAL, "too many tokens for a launch");
     return GDN_OK;
-}
-gdn::MlaStepArgs step_args(const gdn_mla_step_shape_t *s) {
-    gdn::MlaStepArgs a = {};
-    a.N = s->N;
-    a.S = s->S;
-    a.H = s->H;
-    a.dl = s->dl;
-    a.dr = s->dr;
-    a.pages = s->pages;
-    a.page = s->page_size;
-    a.cols = s->max_pages;
-    a.scale = s->scale;
-    if (s->N > 0 && s->S > 0) gdn::mla_step_plan(a, s->dtype == GDN_BF16, CUS);
-    else a.mt = a.units = 0;
-    return a;
 }
 size_t step_part_bytes(const gdn::MlaStepArgs &a) {
     return align_up((size_t)2 * a.units * a.S * a.H * a.dl * 4);
@@ -306,7 +309,6 @@ gdn_status_t gdn_mla_step(const gdn_mla_step_shape_t *s, const void *q, const vo
     if (need && (!ws || ws_bytes < need))
         return fail(GDN_EWORKSPACE, "gdn_mla_step needs %zu bytes of workspace, got %zu", need, ws ? ws_bytes : 0);
     if (need && (uintptr_t)ws % 256) return fail(GDN_EINVAL, "workspace must be 256-byte aligned");
-    if ((double)rows >= LIMIT) return fail(GDN_EINVAL, "too many tokens");
     a.q = q;
     a.cache = cache;
     a.table = block_table;

@@ -517,9 +517,11 @@ void mla_step_plan(MlaStepArgs &a, bool bf16, int cus) {
     a.units = n < 1 ? 1 : (int)n;
 }
 
+static long long step_grid(const MlaStepArgs &a) { // (eight shares side by side, see the kernel)
+    return ((long long)a.units + 7) / 8 * 8 * (((long long)a.S * a.H + 16 * a.mt - 1) / (16 * a.mt));
+}
 template <bool BF, int DLP, int MT> static hipError_t step_run(const MlaStepArgs &a, hipStream_t st) {
-    const long long rb = ((long long)a.S * a.H + MT * 16 - 1) / (MT * 16), units = ((long long)a.units + 7) / 8 * 8;
-    hipLaunchKernelGGL((mla_step_kernel<BF, DLP, MT>), dim3((unsigned)(units * rb)), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((mla_step_kernel<BF, DLP, MT>), dim3((unsigned)step_grid(a)), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 template <bool BF, int DLP> static hipError_t step_rows(const MlaStepArgs &a, hipStream_t st) {
@@ -541,13 +543,27 @@ hipError_t launch_mla_step(const MlaStepArgs &a, bool bf16, hipStream_t st) {
     return bf16 ? step_launch<true>(a, st) : step_launch<false>(a, st);
 }
 
-hipError_t launch_mla_join(const MlaStepArgs &a, bool bf16, hipStream_t st) {
-    // parts of an average sequence decide how many threads share them
+// Launch of the join. The parts of an average sequence decide how many threads share them.
+struct JoinGrid {
+    int groups, wide;
+    long long x;
+};
+static JoinGrid join_grid(const MlaStepArgs &a) {
     int groups = 1;
-    while (groups < 16 && groups * 8 * a.N < a.units) groups *= 2;
-    const int rows = a.S * a.H, cols = a.dl / 4, wide = cols < 256 / groups ? cols : 256 / groups,
-              mine = 256 / (wide * groups);
-    const dim3 grid((unsigned)((long long)a.N * ((rows + mine - 1) / mine)), (unsigned)((cols + wide - 1) / wide));
+    while (groups < 16 && groups * 8LL * a.N < a.units) groups *= 2;
+    const int cols = a.dl / 4, wide = cols < 256 / groups ? cols : 256 / groups, mine = 256 / (wide * groups);
+    return {groups, wide, a.N * (((long long)a.S * a.H + mine - 1) / mine)};
+}
+long long mla_step_groups(const MlaStepArgs &a) {
+    if (a.units == 0) return 0;
+    const long long x = step_grid(a), y = join_grid(a).x;
+    return x > y ? x : y;
+}
+
+hipError_t launch_mla_join(const MlaStepArgs &a, bool bf16, hipStream_t st) {
+    const JoinGrid j = join_grid(a);
+    const int groups = j.groups, cols = a.dl / 4;
+    const dim3 grid((unsigned)j.x, (unsigned)((cols + j.wide - 1) / j.wide));
     if (bf16) hipLaunchKernelGGL(mla_join_kernel<true>, grid, dim3(256), 0, st, a, groups);
     else hipLaunchKernelGGL(mla_join_kernel<false>, grid, dim3(256), 0, st, a, groups);
     return hipGetLastError();

@@ -65,6 +65,13 @@ def test_attention_is_limited_by_its_tensors(L):  # noqa: F811
     assert size(mla(B=1 << 20, H=16, Hk=16, Tq=1, Tk=1, dn=8, dr=0, dv=8)) == 0
 
 
+def test_step_refuses_more_workgroups_than_a_launch_holds(L):  # noqa: F811
+    for shape in (dict(N=1 << 24, S=1, H=1), dict(N=1, S=1 << 23, H=8)):
+        s = gdn.MlaStepShape(shape["N"], shape["S"], shape["H"], 16, 0, 1, 10, 4, 5, 0.1)
+        assert L.gdn_mla_step_workspace_size(ctypes.byref(s)) == 0
+        assert b"launch" in L.gdn_last_error_detail()
+
+
 def test_attention_rejects_null_misaligned_aliased_and_small_workspaces(L):  # noqa: F811
     s = mla()
     need = L.gdn_mla_bwd_workspace_size(ctypes.byref(s))
