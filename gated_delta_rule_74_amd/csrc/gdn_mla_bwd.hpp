@@ -28,8 +28,8 @@
 
 namespace gdn {
 
-// Blocks that see at most so many keys form delta from the products, at the
-// price of a second walk over them.
+// Blocks with a row that sees at most so many keys form delta from the products,
+// at the price of a second walk over them.
 constexpr int MLA_EXACT = 256;
 
 // dq of block qb of the queries of head bh, and their delta.
@@ -93,8 +93,8 @@ __device__ __forceinline__ void mla_bwd_q_block(const MlaBwdArgs a, int bh, int 
     const int wlast = min(q0 + QT * 16 - 1 + off, n - 1), wfirst = q0 + off;
     // Where a row sees few keys, dP - delta cancels, and do . o with o rounded
     // to bf16 is not near enough: a first walk forms delta = sum_j P_ij dP_ij
-    // from the products themselves.
-    if (BF && nt * BT <= MLA_EXACT) {
+    // from the products themselves. The block's first row sees the fewest.
+    if (BF && qb * QB + off < MLA_EXACT) {
         float sum[QT] = {};
         for (int kb = 0; kb < nt; ++kb) {
             const int key0 = kb * BT, next = kb + 1 < nt ? key0 + BT : 0; // (0: for the walk below)

@@ -154,6 +154,56 @@ def test_rising_scores_move_the_maximum_in_every_tile():
         within(n, got[n], x, tol)
 
 
+def fp32_delta(q, k, kr, v, scale, do):
+    """fp64 dq and dk of one sequence of unshared heads, and bounds of latent_util's kind. Rows that see up to
+    256 keys: without the rounding of o to bf16, delta being sum P dP, formed in fp32 from the products. Rows
+    after them may take delta = do . o, whose o carries the two roundings of its bound there (P as an operand:
+    h sum P |v|; the output: h |o|), so edl grows by |do| . (h sum P |v| + h |o|) (1 + rel)."""
+    dq, dk, _, _ = ref.attn_bwd(q, k, kr, v, None, scale, do)
+    o, _, P = ref.attn_fwd(q, k, kr, v, None, scale)
+    D, dv, tq, tk = q.shape[3], v.shape[3], np.zeros_like(dq), np.zeros_like(dk)
+    for h in range(q.shape[2]):
+        kk, vv, p, g = ref._keys(k, kr, 0, h, q.shape[2]), v[0, :, h], P[0, h], do[0, :, h]
+        n = (p > 0).sum(1, keepdims=True)
+        ez = ((D + 8) * U * scale * np.abs(q[0, :, h]) @ np.abs(kk).T * (p > 0)).max(1, keepdims=True)
+        rel = np.expm1(2 * ez + (n + 16) * U)
+        dp, adp = g @ vv.T, np.abs(g) @ np.abs(vv).T
+        dl = (p * dp).sum(1, keepdims=True)
+        edl = ((rel + n * U) * np.abs(dp) * p + (dv + 4) * U * adp * p * (1 + rel)).sum(1, keepdims=True)
+        eo = (rel + n * U) * (p @ np.abs(vv)) + H16 * (p @ np.abs(vv) + np.abs(o[0, :, h])) * (1 + rel)
+        edl += np.where(n > 256, (np.abs(g) * eo).sum(1, keepdims=True), 0.0)
+        ds = p * (dp - dl)
+        eds = rel * np.abs(ds) + p * ((dv + 4) * U * adp + edl + 4 * U * (np.abs(dp) + np.abs(dl))) * (1 + rel)
+        eds = eds + H16 * (np.abs(ds) + eds)  # an operand in bf16
+        m = (p > 0).sum(0)[:, None]
+        tq[0, :, h] = scale * (eds @ np.abs(kk) + (n + 4) * U * np.abs(ds) @ np.abs(kk))
+        tk[0, :, h] = scale * (eds.T @ np.abs(q[0, :, h]) + (m + 4) * U * np.abs(ds).T @ np.abs(q[0, :, h]))[
+            :, :k.shape[3]]
+    return {n: (x, t * (1 + H16) + (H16 + 8 * U) * np.abs(x)) for n, x, t in (("dq", dq, tq), ("dk", dk, tk))}
+
+
+@pytest.mark.parametrize("B,H,Tq,past,dn,dr,dv", [
+    (16, 32, 256, 0, 128, 64, 128), (16, 32, 256, 1, 128, 64, 128), (16, 32, 256, 30, 128, 64, 128),
+    (16, 32, 250, 255, 128, 64, 128), (32, 32, 128, 140, 56, 32, 56), (3, 4, 70, 1, 56, 32, 56),
+    (3, 4, 70, 230, 56, 32, 56)])
+def test_gradients_of_rows_that_see_few_keys(B, H, Tq, past, dn, dr, dv):
+    """Values one bf16 step apart: dP - delta is as small as the rounding of o, and is kept free of it in
+    every size of block, wherever the cached keys let the block begin."""
+    say(f"attention backward, B {B} H {H} Tq {Tq} after {past}, values a step apart, bf16")
+    gen = torch.Generator("cuda").manual_seed(7905)
+    r = lambda *s: torch.randn(s, device="cuda", generator=gen)  # noqa: E731
+    Tk = Tq + past
+    q, do = (0.05 * r(B, Tq, H, dn + dr)).bfloat16(), r(B, Tq, H, dv).bfloat16()
+    k, kr = (1 + 0.25 * r(B, Tk, H, dn)).bfloat16(), (1 + 0.25 * r(B, Tk, H, dr)).bfloat16()
+    v = torch.where(r(B, Tk, H, dv) > 0, 1.0, 1.0 + 2.0 ** -7).bfloat16()
+    scale = (dn + dr) ** -0.5
+    got = run_attn([q, k, kr, v, do], None, scale)
+    for b, h in ((0, 0), (B - 1, H - 1)):
+        f = [host(x[b:b + 1, :, h:h + 1]) for x in (q, k, kr, v, do)]
+        for n, (x, tol) in fp32_delta(*f[:4], scale, f[4]).items():
+            within(f"{n} of sequence {b}, head {h}", got[n][b:b + 1, :, h:h + 1], x, tol)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_padding_is_not_read_and_its_gradients_are_zero(dtype):
     """NaN past the lengths changes nothing; padded rows get zeros."""
