@@ -236,10 +236,12 @@ gdn_status_t gdn_step_tokens(int32_t N, int32_t S, int32_t H, int32_t dk, int32_
  * The rules at the top of this file hold (ownership, streams, errors, no
  * allocation, bitwise reproducible results). Tensors are contiguous; q, k, v,
  * o, c, x, cache and their gradients are fp32 or bf16 as the call's dtype
- * says, sums and softmax statistics fp32. NaN/Inf in rows that take part
- * propagate (and within a tile of up to 128 keys may reach queries before them);
- * rows at or past a length, and cache rows no table entry in use names, are
- * not read.
+ * says, sums and softmax statistics fp32. Rows at or past a length, and cache
+ * rows no table entry in use names, are not read. NaN/Inf in rows that take
+ * part propagate, and as 0 * NaN within a tile also to masked neighbours: from
+ * a key or value row to o and dq of queries up to 160 positions before it, from
+ * a row of q or dout to dk, dk_rope and dv of keys up to 160 positions after
+ * it, from a cache row to all S tokens of a gdn_mla_step.
  */
 
 /* q [B,Tq,H,dn+dr], k [B,Tk,Hk,dn], k_rope [B,Tk,Hr,dr], v [B,Tk,Hk,dv],

@@ -225,6 +225,38 @@ def test_padding_is_not_read_and_its_gradients_are_zero(dtype):
         assert (dirty["lse"][b, max(0, n - 20):] == -float("inf")).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,T,past,H,dn,dr,dv", [(1, 700, 0, 2, 56, 32, 56), (1, 500, 130, 16, 16, 16, 16),
+                                                 (4, 520, 40, 64, 56, 32, 56), (16, 600, 0, 64, 128, 64, 128)])
+def test_how_far_a_nan_reaches(B, T, past, H, dn, dr, dv, dtype):
+    """NaN in a key's and value's row leaves queries more than 160 positions before it as they were, NaN in a
+    query's and its gradient's row the gradients of keys more than 160 after it and all other queries."""
+    say(f"attention, one NaN row, B {B} T {T} after {past} H {H} {dn} + {dr} | {dv} {dtype}")
+    t, _, lens, scale = attn_inputs((B, T, past, H, H, H, dn, dr, dv, None), dtype, 7906)
+    clean = run_attn(t, lens, scale)
+    at, i = past + 333, 333  # position of the row, its query
+    others = torch.arange(T, device="cuda") != i
+    for x, name in enumerate(("q", "k", "k_rope", "v", "do")):
+        of_query = name in ("q", "do")
+        row = i if of_query else at
+        keep = t[x][0, row].clone()
+        t[x][0, row] = float("nan")
+        dirty = run_attn(t, lens, scale)
+        t[x][0, row] = keep
+        for n in clean:
+            assert torch.equal(dirty[n][1:], clean[n][1:]), (name, n)
+        if not of_query:
+            assert dirty["dq"][0, i:].isnan().any()
+            for n in ("o", "lse", "dq"):
+                assert torch.equal(dirty[n][0, :i - 160], clean[n][0, :i - 160]), (name, n)
+        else:
+            assert dirty["dk"][0, at].isnan().any()
+            for n in ("dk", "dkr", "dv"):
+                assert torch.equal(dirty[n][0, at + 161:], clean[n][0, at + 161:]), (name, n)
+            for n in ("o", "lse", "dq"):
+                assert torch.equal(dirty[n][0, others], clean[n][0, others]), (name, n)
+
+
 def test_attention_is_reproducible_and_keeps_to_its_buffers():
     say("attention twice, guard rows around every output")
     case = (2, 100, 0, 4, 2, 1, 56, 32, 56, [100, 77])
