@@ -236,6 +236,9 @@ __global__ __launch_bounds__(NR_THREADS) void norm_rope_kernel(NormRopeArgs a, i
             }
             const float2 *t = cs[buf] + (a.r / 2) * ((in ? row : row0) / (unsigned)a.H - token0);
             turn_row<BF, VEC>(a, tn, v, ov, (const S *)a.x + (size_t)(in ? row : 0) * d, inv, a.w, sub, lpr, 1.f, t, in);
+            // y may be x: where a column's partner is read from memory, every lane of the row has read before
+            // any writes (a row's lanes are in one wave)
+            if (!VEC) __builtin_amdgcn_wave_barrier();
             if (in) store_row<BF, VEC>((S *)a.y + (size_t)row * d, sub, lpr, d, v);
         }
     }
