@@ -431,14 +431,23 @@ __device__ __forceinline__ void mla_bwd_k_block(const MlaBwdArgs a, int bh, int 
     }
 }
 
-// Waves per SIMD: two need the operands and both accumulators of a wave in 256
-// registers (96 | 64: 0.87 ms with two, 1.43 with one at the layer shape);
-// wider pairs of key tiles take up to 512 and run one (192 | 128 with one pair
-// per wave: 3.2 ms at T 16384, one tile and two waves 3.8).
-constexpr int mla_bwd_k_waves(int kt, int dp, int dvp) { return kt == 1 || dp + dvp <= 160 ? 2 : 1; }
+// Waves per SIMD. Two leave a wave 256 registers for its operands and both
+// accumulators, one 512. bf16: pairs of key tiles beyond 96 | 64 run one (96 |
+// 64: 0.87 ms with two, 1.43 with one at the layer shape; 192 | 128, T 16384:
+// 3.2 ms as pairs with one wave, 3.8 as single tiles with two); two waves of
+// single tiles spill a little at 192 | 128 and are still ahead (B1 T2048, 8
+// heads: 65 us, 68 with one). fp32 holds twice the registers, single tiles
+// throughout: up to 192 columns in all two waves, with what they spill, are
+// ahead (B4 T2048 H16, 56 + 32 | 56: 0.72 ms, 0.82 with one; 96 + 32 | 64: 0.89
+// and 0.97), beyond that one (128 | 128: 1.51 ms with two, 1.27 with one; B2
+// T700, 8 heads: 140 and 72 us; 192 | 64: 1.51 and 1.27; 96 | 128: 1.26, 1.12).
+template <bool BF> constexpr int mla_bwd_k_waves(int kt, int dp, int dvp) {
+    if (!BF) return dp + dvp <= 192 ? 2 : 1;
+    return kt == 1 || dp + dvp <= 160 ? 2 : 1;
+}
 
 template <bool BF, int DP, int DVP, int NW, int KT, int WS>
-__global__ __launch_bounds__(NW * 64, WS == 4 ? 1 : mla_bwd_k_waves(KT, DP, DVP)) void mla_bwd_k_kernel(MlaBwdArgs a) {
+__global__ __launch_bounds__(NW * 64, WS == 4 ? 1 : mla_bwd_k_waves<BF>(KT, DP, DVP)) void mla_bwd_k_kernel(MlaBwdArgs a) {
     using S = typename Op<BF>::S;
     constexpr int KB = NW / WS * KT * 16, BT = mla_tile(WS);
     __shared__ __align__(16) S Qs[BT * (DP + MLA_PAD<BF>)];
@@ -478,7 +487,7 @@ template <bool BF, int DP, int DVP, int NW, int KT, int WS> hipError_t mla_bwd_k
 template <bool BF, int DP, int DVP> hipError_t mla_bwd_k_run(const MlaBwdArgs &a, hipStream_t st) {
     const long long heads = (long long)a.s.B * a.s.Hk;
     if constexpr (BF)
-        if (mla_large(heads, a.s.Tk, 128, mla_bwd_k_waves(2, DP, DVP)))
+        if (mla_large(heads, a.s.Tk, 128, mla_bwd_k_waves<BF>(2, DP, DVP)))
             return mla_bwd_k_start<BF, DP, DVP, 4, 2, 1>(a, st);
     const int split = mla_split<BF>(heads, a.s.Tk, (long long)a.s.Tq * (a.s.H / a.s.Hk), DP, DVP);
     if constexpr (mla_fits4<BF>(DP, DVP))

@@ -1,5 +1,5 @@
-"""Wait states behind the matrix instructions of the built library (CPU: the
-code is read, not run). The hardware does not hold back an instruction that
+"""The built library's code (CPU: it is read, not run): wait states behind its
+matrix instructions, and spilled registers. The hardware does not hold back an instruction that
 uses the result of an MFMA too early; the compiler has to put enough
 instructions or s_nop between the two on every path, and it has been seen not
 to where a conditional block follows the MFMA at once. So the paths are walked
@@ -15,7 +15,7 @@ import pytest
 
 import gated_delta_rule_74_amd as gdn
 
-OBJDUMP = "/opt/rocm/llvm/bin/llvm-objdump"
+OBJDUMP, READOBJ = ("/opt/rocm/llvm/bin/" + t for t in ("llvm-objdump", "llvm-readobj"))
 REG = re.compile(r"\b([va])\[(\d+):(\d+)\]|\b([va])(\d+)\b")
 
 
@@ -113,13 +113,29 @@ def test_the_walk_finds_an_early_use_behind_a_branch():
     assert not early_uses(kernels(acc)["kernel"])
 
 
-@pytest.mark.skipif(not os.path.exists(OBJDUMP), reason="no llvm-objdump")
-def test_no_mfma_result_is_used_too_early(tmp_path):
+def code_objects(tmp_path):
+    """The library's gfx950 code objects, one per source."""
     gdn.lib()  # (raises if it has not been built)
     shutil.copy(gdn.LIB_PATH, tmp_path / "lib.so")
     subprocess.run([OBJDUMP, "--offloading", "lib.so"], cwd=tmp_path, check=True, capture_output=True)
+    return sorted(tmp_path.glob("lib.so.*gfx950*"))
+
+
+@pytest.mark.skipif(not os.path.exists(READOBJ), reason="no llvm-readobj")
+def test_attention_backward_keeps_its_registers(tmp_path):
+    """What the key-gradient kernels spill stays where two waves per SIMD were measured to be worth it."""
+    spilled = {}
+    for f in code_objects(tmp_path):
+        notes = subprocess.run([READOBJ, "--notes", str(f)], check=True, capture_output=True, text=True).stdout
+        spilled.update(re.findall(r"\.name: +(\S*mla_bwd_k_kernel\S*)\n\s+\.private_segment_fixed_size: (\d+)", notes))
+    assert len(spilled) > 20
+    assert max(int(n) for n in spilled.values()) <= 160, spilled
+
+
+@pytest.mark.skipif(not os.path.exists(OBJDUMP), reason="no llvm-objdump")
+def test_no_mfma_result_is_used_too_early(tmp_path):
     products, bad = 0, []
-    for f in sorted(tmp_path.glob("lib.so.*gfx950*")):
+    for f in code_objects(tmp_path):
         listing = subprocess.run([OBJDUMP, "-d", "--mcpu=gfx950", str(f)], check=True, capture_output=True,
                                  text=True).stdout
         for name, code in kernels(listing).items():
