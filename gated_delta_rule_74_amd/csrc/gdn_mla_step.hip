@@ -100,12 +100,9 @@ template <int NJ> __device__ __forceinline__ f32x4 mma_rows(const Frag<true> &a,
                                                      __builtin_shufflevector(y, y, 0, 1, 2, 3), c, 0, 0, 0);
 }
 template <int NJ> __device__ __forceinline__ f32x4 mma_rows(const Frag<false> &a, const Frag<false> &b, f32x4 c) {
+    static_assert(NJ == 1, "an fp32 wave takes 16 rows");
 #pragma unroll
     for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.lo[j], b.lo[j], c, 0, 0, 0);
-    if (NJ == 2) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.hi[j], b.hi[j], c, 0, 0, 0);
-    }
     return c;
 }
 template <int NJ> __device__ __forceinline__ Frag<true> col_rows(const u16 *X, int ld, int k0, int m0, int lane) {
@@ -118,10 +115,6 @@ template <int NJ> __device__ __forceinline__ Frag<false> col_rows(const float *X
     Frag<false> f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) f.lo[e] = p[e * ld];
-    if (NJ == 2) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f.hi[e] = p[(16 + e) * ld];
-    }
     return f;
 }
 
