@@ -4,9 +4,11 @@
 //   lse_i = log sum_j exp z_ij   over the keys j <= i + Tk - Tq, j < len_b
 //
 // in one pass over the keys with the running maximum and sum of the softmax.
-// A workgroup takes NW * QT * 16 queries of one head and walks the keys in
-// tiles of 64 that all its waves share in LDS; a wave holds its QT * 16
-// queries in registers for the whole walk. The products are formed
+// A workgroup takes NW / WS * QT * 16 queries of one head and walks the keys in
+// tiles of 64 (128 with WS = 4) that all its waves share in LDS; a wave holds
+// its QT * 16 queries in registers for the whole walk. WS waves hold the same
+// queries where there are too few to fill the chip: each takes every WS-th 32
+// keys of a tile, and their sums are joined at the end. The products are formed
 // transposed, S^T = K Q^T and O^T = V^T P^T: then a lane owns one query
 // (column), the maximum and the rescaling are per-lane scalars, and the
 // probabilities leave the first product in exactly the lanes and K order that

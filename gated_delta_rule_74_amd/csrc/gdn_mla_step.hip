@@ -10,10 +10,11 @@
 //
 // A workgroup takes MT * 16 queries and an equal share of the cached rows; the
 // parts of a sequence are joined by mla_join_kernel. Rows go through registers
-// (requested one tile ahead, the table entries two) into an LDS tile of
-// 32 * WK rows; the four waves split it into WK groups of 32 keys times
-// 4 / WK groups of latent columns, each wave with a running softmax of its own
-// over its keys, so a tile costs two barriers and no exchange. As in the
+// (requested one tile ahead, the table entries two) into an LDS tile of 64 rows
+// (32 beyond 256 latent columns); the four waves split it into WK groups of KW
+// keys (16 or 32, see StepShape) times 4 / WK groups of latent columns, each
+// wave with a running softmax of its own over its keys, so a tile costs two
+// barriers and no exchange. As in the
 // forward pass over expanded heads the products are formed transposed: a lane
 // owns one query, and the probabilities are at once the operand of the second
 // product, whose other operand is read from the same tile by transposing reads.
@@ -77,6 +78,7 @@ __device__ __forceinline__ int part_slot(int w, int begin, int share) { return 2
 // form each score once (8 sequences of 30000 rows of 256 + 64, 32 queries: 104
 // us with two groups, 85 with four); beyond, the accumulators of all columns do
 // not fit a wave.
+constexpr int step_tile(int dlp) { return dlp <= 256 ? 6 : 5; } // log2 of a tile's rows, by padded columns
 template <bool BF, int DLP, int MT> struct StepShape {
     using S = typename Op<BF>::S;
     static constexpr int WK = !BF && DLP <= 256 ? 4 : 2, WR = 4 / WK, KW = BF && DLP <= 256 ? 32 : 16, KT = KW * WK,
@@ -88,6 +90,7 @@ template <bool BF, int DLP, int MT> struct StepShape {
     // above: 56 us in registers, 36 in LDS; 512 + 64, 16 queries, 200 sequences
     // up to 1000 rows: 53 and 49).
     static constexpr bool QL = !BF || DLP * MT >= 256;
+    static_assert(KT == 1 << step_tile(DLP), "shares are cut between tiles");
 };
 
 typedef short short8_t __attribute__((ext_vector_type(8)));
@@ -483,9 +486,6 @@ static int step_class(int dl) {
     return dl <= 64 ? 64 : dl <= 128 ? 128 : dl <= 192 ? 192 : dl <= 256 ? 256 : dl <= 384 ? 384 : 512;
 }
 
-// log2 of a tile's rows (StepShape::KT)
-static int step_tile(int dl) { return step_class(dl) <= 256 ? 6 : 5; }
-
 // workgroups a CU holds at once, by their registers and LDS
 static int step_per_cu(const MlaStepArgs &a, bool bf16) {
     const int c = step_class(a.dl);
@@ -495,7 +495,7 @@ static int step_per_cu(const MlaStepArgs &a, bool bf16) {
 
 void mla_step_plan(MlaStepArgs &a, bool bf16, int cus) {
     const long long rows = (long long)a.S * a.H, cap = (long long)a.cols * a.page;
-    a.tile = step_tile(a.dl);
+    a.tile = step_tile(step_class(a.dl));
     const long long most = a.N * ((cap + (1 << a.tile) - 1) >> a.tile); // tiles there may be
     // Query blocks per workgroup: two where the registers hold them and there may
     // be twelve tiles for each CU, which pays for a longer start and end (fp32,
