@@ -67,6 +67,7 @@ def _mla_shape(q, k, v, k_rope, lens, scale):
         if not isinstance(k_rope, torch.Tensor) or k_rope.dim() != 4:
             raise ValueError("k_rope must be [B, T, heads, dr]")
         Hr = k_rope.shape[2]
+        _int32(k_rope=k_rope.numel())
     _need(q, "q", q.dtype, (B, Tq, H, D))
     _need(k, "k", q.dtype, (B, Tk, Hk, dn), dev)
     _need(v, "v", q.dtype, (B, Tk, Hk, dv), dev)
@@ -195,6 +196,7 @@ def _rope_args(x, weight, positions, freqs, norm, interleaved):
         if positions is None:
             raise ValueError("freqs need positions")
         r = 2 * freqs.numel()
+        _int32(r=r)
         _need(freqs, "freqs", torch.float64, (r // 2,), dev)
         _need(positions, "positions", torch.int32, lead, dev)
     M = 1

@@ -802,3 +802,11 @@ def test_refusals_on_the_device():
     assert e.value.status == 2
     with pytest.raises(ValueError):
         gdn.norm_rope(q, None, None, torch.ones(4, dtype=torch.float64, device="cuda"))
+
+
+def test_more_turned_columns_than_int32_holds_are_refused():
+    """(2^32 + 8 turned columns would have been taken for eight.)"""
+    x, pos = torch.zeros(3, 2, 16, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+    far = torch.ones(1, dtype=torch.float64, device="cuda").expand(2 ** 31 + 4)
+    with pytest.raises(ValueError, match="too large"):
+        gdn.norm_rope(x, None, pos, far)

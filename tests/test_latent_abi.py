@@ -238,3 +238,11 @@ def test_binding_refuses_what_int32_does_not_hold_and_missing_tensors():
         gdn.mla_step(torch.zeros(1, 1, 24), torch.zeros(1, 2, 24), torch.zeros(1, 2, **i32), None, 16, scale=1.0)
     with pytest.raises(ValueError):
         gdn.mla_write(torch.zeros(1, 16), None, None, torch.zeros(1, 2, 16))
+
+
+def test_binding_refuses_more_rotary_heads_than_int32_holds():
+    """(2^32 + 1 rotary heads would have been taken for one.)"""
+    wide = torch.zeros(1, dtype=torch.bfloat16)
+    q, k = torch.zeros(1, 1, 2, 24, dtype=torch.bfloat16), torch.zeros(1, 1, 2, 16, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="too large"):
+        gdn.mla_fwd(q, k, k, wide.expand(1, 1, 2 ** 32 + 1, 8))
