@@ -236,12 +236,18 @@ gdn_status_t gdn_step_tokens(int32_t N, int32_t S, int32_t H, int32_t dk, int32_
  * The rules at the top of this file hold (ownership, streams, errors, no
  * allocation, bitwise reproducible results). Tensors are contiguous; q, k, v,
  * o, c, x, cache and their gradients are fp32 or bf16 as the call's dtype
- * says, sums and softmax statistics fp32. Rows at or past a length, and cache
- * rows no table entry in use names, are not read. NaN/Inf in rows that take
- * part propagate, and as 0 * NaN within a tile also to masked neighbours: from
- * a key or value row to o and dq of queries up to 160 positions before it, from
- * a row of q or dout to dk, dk_rope and dv of keys up to 160 positions after
- * it, from a cache row to all S tokens of a gdn_mla_step.
+ * says, sums and softmax statistics fp32. fp32 calls round nothing below that.
+ * bf16 calls round, besides their outputs, what the next matrix product takes:
+ * the probabilities (for o and dv) and dS = P (dP - delta) (for dq, dk and
+ * dk_rope), to nearest even; and delta = dout . o uses the bf16 o it is given,
+ * except in rows that see at most 256 keys, where it is formed anew in fp32.
+ * A caller who needs less rounding calls with fp32 tensors. Rows at or past a
+ * length, and cache rows no table entry in use names, are not read. NaN/Inf in
+ * rows that take part propagate, and as 0 * NaN within a tile also to masked
+ * neighbours: from a key or value row to o and dq of queries up to 160
+ * positions before it, from a row of q or dout to dk, dk_rope and dv of keys up
+ * to 160 positions after it, from a cache row to all S tokens of a
+ * gdn_mla_step.
  */
 
 /* q [B,Tq,H,dn+dr], k [B,Tk,Hk,dn], k_rope [B,Tk,Hr,dr], v [B,Tk,Hk,dv],
