@@ -427,17 +427,17 @@ template <bool BF, int UN> __global__ __launch_bounds__(NR_THREADS) void mla_wri
         const int at = a.slots[i], p = e % hp;
         const int ca = a.inter ? 2 * p : p, cb = a.inter ? 2 * p + 1 : p + hp;
         const S *kr = (const S *)a.kr + (size_t)i * a.dr;
+        S ka = kr[ca], kb = kr[cb];
+        if (a.freqs) { // (else as they are: a turn by no angle would make inf * 0 of a partner)
+            const float x = to_f(ka), y = to_f(kb);
+            const float2 t = turn_of(a.pos[i], a.freqs[p]);
+            ka = from_f<BF>(x * t.x - y * t.y);
+            kb = from_f<BF>(y * t.x + x * t.y);
+        }
         if (at < 0 || at >= a.n_slots) continue;
         S *row = (S *)a.cache + (size_t)at * d + a.dl;
-        if (!a.freqs) { // as they are (a turn by no angle would make inf * 0 of a partner)
-            row[ca] = kr[ca];
-            row[cb] = kr[cb];
-            continue;
-        }
-        const float x = to_f(kr[ca]), y = to_f(kr[cb]);
-        const float2 t = turn_of(a.pos[i], a.freqs[p]);
-        row[ca] = from_f<BF>(x * t.x - y * t.y);
-        row[cb] = from_f<BF>(y * t.x + x * t.y);
+        row[ca] = ka;
+        row[cb] = kb;
     }
     float w[8];
 #pragma unroll
