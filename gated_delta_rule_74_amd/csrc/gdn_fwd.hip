@@ -179,12 +179,12 @@ __global__ __launch_bounds__(NTHR, 8) void fwd_prep_kernel(PrepArgs a) {
     f32x4 accU[Tiles<4, DT>::PW], accN[Tiles<4, DT>::PW];
 #pragma unroll
     for (int i = 0; i < Tiles<4, DT>::PW; ++i) accU[i] = accN[i] = zero4();
-    // Up to 32 columns N comes first: behind a block that may be jumped over
+    // Up to 32 bf16 columns N comes first: behind a block that may be jumped over
     // right after U's product, the compiler (ROCm 7.2) leaves six wait states
     // before U is used where eight are needed. Wider heads use U later than that
     // and keep the order that is faster there (D = 64, the layer shape: 0.105 ms
     // with U first, 0.107 with N first).
-    constexpr bool n_first = D <= 32;
+    constexpr bool n_first = BF && D <= 32;
     if (n_first && !s.additive) gemm<BF, 4, DT, C, false, true>(Tb, LDC, Ks, LDD, accN, wave, lane);
     gemm<BF, 4, DT, C, false, true>(Tb, LDC, Vs, LDD, accU, wave, lane);
     if (!n_first && !s.additive) gemm<BF, 4, DT, C, false, true>(Tb, LDC, Ks, LDD, accN, wave, lane);
