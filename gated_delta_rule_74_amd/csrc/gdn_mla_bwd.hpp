@@ -20,8 +20,8 @@
 // S and dP are formed in both kernels: seven products instead of five, for
 // which no sum needs atomics or a second pass. Bound by the matrix products
 // and, at narrow heads, as much by the exponentials and the reads of LDS:
-// B8 H16 T4096 56 + 32 | 56 0.68 + 0.83 ms (0.6 of the rate a large product
-// reaches), T16384 16 heads on 4, 128 + 64 | 128 2.10 + 3.06 ms (0.77 of it).
+// B8 H16 T4096 56 + 32 | 56 0.65 + 0.81 ms (0.62 of the rate a large product
+// reaches), T16384 16 heads on 4, 128 + 64 | 128 2.11 + 3.00 ms (0.79 of it).
 #pragma once
 
 #include "gdn_mla.hpp"

@@ -20,10 +20,11 @@
 // loss; this keeps the cross-lane maximum and the rescaling of O out of almost
 // every tile.
 // Wide heads (192 | 128) run at 0.8 of the rate a large matrix product reaches
-// (T 16384, 16 heads on 4: 1.41 ms); at 96 | 64 the exponentials and the mask
-// take as long as the products (B8 H16 T4096: 0.47 ms, 0.53 of that rate). More
-// waves per SIMD (three, four) or value operands requested ahead do not change
-// either.
+// (T 16384, 16 heads on 4: 1.39 ms); at 96 | 64 the vector unit (exponentials,
+// their sums and the mask: busy half of the time) adds to the matrix unit (a
+// third) more than it runs beside it (B8 H16 T4096: 0.46 ms, 0.54 of that rate).
+// More waves per SIMD (three, four) or value operands requested ahead do not
+// change either. (Times here and in the backward: between events, warm.)
 #pragma once
 
 #include "gdn_mla.hpp"

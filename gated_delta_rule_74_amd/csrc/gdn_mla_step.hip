@@ -20,8 +20,8 @@
 // product, whose other operand is read from the same tile by transposing reads.
 // Bound by the cache's bytes with what a workgroup has in flight (two or three
 // waves per SIMD, a tile each): 256 sequences of 0 to 4096 rows of 128 + 32
-// bf16 in 36 us and 6 us for the join, 4.7 TB/s where a large copy reaches 5.6;
-// one of 131072 rows of 512 + 64 in 34 us and 12 us, 4.5 TB/s. In fp32 by the
+// bf16 in 34 us and 6 us for the join, 4.9 TB/s where a large copy reaches 5.6;
+// one of 131072 rows of 512 + 64 in 32 us and 12 us, 4.7 TB/s. In fp32 by the
 // matrix products (48 drafts of three tokens up to 1500 rows, 8 heads of
 // 256 + 64: 38 us).
 #include "gdn_mla.hpp"
