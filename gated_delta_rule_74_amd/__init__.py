@@ -27,6 +27,16 @@ The latent-attention layers of the hybrid stack, and their paged cache
     plan      = page_plan(lens, new_lens, block_table, free_pages, n_free, page_size, max_tokens)
     cache     = mla_write(c, k_rope, plan["slots"], cache, weight, plan["positions"], freqs)
     o, lse    = mla_step(q, cache, block_table, plan["lens"], dl, scale=scale)
+
+Serving beside the plain step (serving.py): prefixes that a batch shares,
+drafts, and caches that may not grow:
+
+    o, lse    = mla_step_shared(q, cache, block_table, lens, dl, prefix_table, prefix_lens, starts, scale=scale)
+    accepted, tokens, logprobs = draft_verify(logits, draft, uniforms, draft_logits)
+    h         = step_commit(k, v, g, beta, A_log, counts, h_in)  # the state after the accepted tokens
+    n_free    = page_trim(lens, new_lens, block_table, free_pages, n_free, page_size)
+    weights   = mla_weights(q, cache, block_table, lens, lse, weights, scale=scale)
+    lens      = mla_evict(weights, cache, block_table, lens, keep, first=4, recent=64)
 """
 from __future__ import annotations
 
@@ -38,7 +48,8 @@ import torch
 __all__ = ["fwd", "fwd_noalloc", "bwd", "step", "step_tokens", "GatedDeltaRule", "GdnError", "lib", "EXPORTS",
            "LIB_PATH", "context_size", "context_states", "fwd_workspace_size", "bwd_workspace_size",
            "LaunchTimer", "NOALLOC_SCRATCH_BYTES", "mla_fwd", "mla_bwd", "LatentAttention", "mla_step", "norm_rope",
-           "norm_rope_bwd", "NormRope", "mla_write", "page_plan"]
+           "norm_rope_bwd", "NormRope", "mla_write", "page_plan", "mla_step_shared", "mla_weights", "mla_evict", "page_trim",
+           "draft_verify", "step_commit"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn.so")
@@ -46,7 +57,9 @@ EXPORTS = ["gdn_fwd", "gdn_bwd", "gdn_step", "gdn_step_tokens", "gdn_fwd_workspa
            "gdn_fwd_context_size", "gdn_time_launches", "gdn_launch_kind", "gdn_status_string",
            "gdn_last_error_detail", "gdn_fwd_noalloc", "gdn_mla_fwd", "gdn_mla_bwd", "gdn_mla_bwd_workspace_size",
            "gdn_mla_step", "gdn_mla_step_workspace_size", "gdn_norm_rope", "gdn_norm_rope_bwd",
-           "gdn_norm_rope_bwd_workspace_size", "gdn_mla_write", "gdn_page_plan"]
+           "gdn_norm_rope_bwd_workspace_size", "gdn_mla_write", "gdn_page_plan", "gdn_mla_step_shared",
+           "gdn_mla_step_shared_workspace_size", "gdn_mla_weights", "gdn_mla_evict", "gdn_mla_evict_workspace_size",
+           "gdn_page_trim", "gdn_draft_verify", "gdn_draft_verify_workspace_size", "gdn_step_commit"]
 
 GDN_F32, GDN_BF16 = 0, 1
 NOALLOC_SCRATCH_BYTES = 64 << 20  # GDN_NOALLOC_SCRATCH_BYTES of include/gdn.h
@@ -108,13 +121,25 @@ def lib():
         L.gdn_norm_rope_bwd.argtypes = [I64, I32, I32, I32, I32, U32, F, P, P, P, P, P, P, P, P, Z, P]
         L.gdn_mla_write.argtypes = [I64, I32, I32, I32, U32, F, P, P, P, P, P, P, P, I64, P]
         L.gdn_page_plan.argtypes = [I32, I32, I32, I32, I32] + [P] * 12
+        L.gdn_mla_step_shared.argtypes = [D, I32, I32] + [P] * 10 + [Z, P]
+        L.gdn_mla_weights.argtypes = [D, F] + [P] * 8
+        L.gdn_mla_evict.argtypes = [I32] * 7 + [P] * 7 + [Z, P]
+        L.gdn_page_trim.argtypes = [I32] * 4 + [P] * 7
+        L.gdn_draft_verify.argtypes = [I32] * 4 + [P] * 10 + [Z, P]
+        L.gdn_step_commit.argtypes = [I32] * 6 + [U32] + [P] * 9
         for f in (L.gdn_mla_fwd, L.gdn_mla_bwd, L.gdn_mla_step, L.gdn_norm_rope, L.gdn_norm_rope_bwd,
-                  L.gdn_mla_write, L.gdn_page_plan):
+                  L.gdn_mla_write, L.gdn_page_plan, L.gdn_mla_step_shared, L.gdn_mla_weights, L.gdn_mla_evict,
+                  L.gdn_page_trim, L.gdn_draft_verify, L.gdn_step_commit):
             f.restype = ctypes.c_int
         L.gdn_mla_bwd_workspace_size.argtypes = [A]
         L.gdn_mla_step_workspace_size.argtypes = [D]
         L.gdn_norm_rope_bwd_workspace_size.argtypes = [I64, I32, I32]
-        for f in (L.gdn_mla_bwd_workspace_size, L.gdn_mla_step_workspace_size, L.gdn_norm_rope_bwd_workspace_size):
+        L.gdn_mla_step_shared_workspace_size.argtypes = [D, I32, I32]
+        L.gdn_mla_evict_workspace_size.argtypes = [I32] * 4
+        L.gdn_draft_verify_workspace_size.argtypes = [I32] * 4
+        for f in (L.gdn_mla_bwd_workspace_size, L.gdn_mla_step_workspace_size, L.gdn_norm_rope_bwd_workspace_size,
+                  L.gdn_mla_step_shared_workspace_size, L.gdn_mla_evict_workspace_size,
+                  L.gdn_draft_verify_workspace_size):
             f.restype = Z
         L.gdn_time_launches.argtypes = [P, I32]
         L.gdn_time_launches.restype = I32
@@ -416,7 +441,8 @@ class LaunchTimer:
 
     KINDS = ("fwd_prep", "fwd_chain", "bwd_chain", "bwd_local", "dA_reduce", "step", "fwd_scan", "bwd_scan",
              "mla_fwd", "mla_bwd_q", "mla_bwd_k", "mla_rope_sum", "mla_step", "mla_join", "norm_rope",
-             "norm_rope_bwd", "norm_sum", "mla_write", "page_plan", "page_fill")
+             "norm_rope_bwd", "norm_sum", "mla_write", "page_plan", "page_fill", "mla_prefix", "mla_weights",
+             "evict_choose", "evict_move", "page_trim", "verify_sums", "verify_left", "verify_draw", "step_commit")
 
     def kinds(self):
         """Kernel name of every bracketed launch, in launch order."""
@@ -453,3 +479,4 @@ class GatedDeltaRule(torch.autograd.Function):
 
 from .latent import (LatentAttention, NormRope, mla_bwd, mla_fwd, mla_step, mla_write, norm_rope,  # noqa: E402
                      norm_rope_bwd, page_plan)
+from .serving import (draft_verify, mla_evict, mla_step_shared, mla_weights, page_trim, step_commit)  # noqa: E402

@@ -16,7 +16,9 @@ LIB = os.path.join(HERE, "libgdn.so")
 OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["gdn_fwd.hip", "gdn_bwd.hip", "gdn_bwd128.hip", "gdn_step.hip", "gdn_util.hip", "gdn_noalloc.hip", "gdn_api.cpp",
            "gdn_mla_fwd_bf16.hip", "gdn_mla_fwd_f32.hip", "gdn_mla_bwd_q_bf16.hip", "gdn_mla_bwd_k_bf16.hip",
-           "gdn_mla_bwd_f32.hip", "gdn_mla_step.hip", "gdn_norm_rope.hip", "gdn_pages.hip", "gdn_mla_api.cpp"]
+           "gdn_mla_bwd_f32.hip", "gdn_mla_step.hip", "gdn_norm_rope.hip", "gdn_pages.hip", "gdn_mla_api.cpp",
+           "gdn_mla_prefix_bf16.hip", "gdn_mla_prefix_f32.hip", "gdn_weights.hip", "gdn_evict.hip", "gdn_drafts.hip",
+           "gdn_commit.hip", "gdn_serve_api.cpp"]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -65,6 +65,8 @@ struct MlaStepArgs {
     int tile;       // log2 of a tile's rows; a share is a whole number of tiles
     float *part;    // workspace [2 * units][S * H][dl]
     float *part_ml; // workspace [2 * units][S * H][2]
+    // Beside a shared prefix (launch_mla_step_parts) every piece is left as a
+    // part, at place (share + sequence): [units + N] of them.
 };
 
 struct NormRopeArgs {
@@ -154,6 +156,7 @@ struct MlaPad {
     int d, dv;
 };
 MlaPad mla_pad(const MlaArgs &s);
+int step_class(int dl); // latent columns, padded to what the paged kernels are built for
 void mla_step_plan(MlaStepArgs &a, bool bf16, int cus); // sets mt and units from the sizes
 long long mla_step_groups(const MlaStepArgs &a);        // workgroups of the step's larger launch
 
@@ -168,6 +171,7 @@ hipError_t launch_mla_bwd_k_bf16(const MlaBwdArgs &a, hipStream_t st);
 hipError_t launch_mla_bwd_k_f32(const MlaBwdArgs &a, hipStream_t st);
 hipError_t launch_mla_rope_sum(const MlaBwdArgs &a, bool bf16, hipStream_t st);
 hipError_t launch_mla_step(const MlaStepArgs &a, bool bf16, hipStream_t st);
+hipError_t launch_mla_step_parts(const MlaStepArgs &a, bool bf16, hipStream_t st);
 hipError_t launch_mla_join(const MlaStepArgs &a, bool bf16, hipStream_t st);
 hipError_t launch_norm_rope(const NormRopeArgs &a, bool bf16, hipStream_t st);
 hipError_t launch_norm_rope_bwd(const NormRopeArgs &a, bool bf16, hipStream_t st);
@@ -342,6 +346,37 @@ template <bool BF, int N> struct Frags {
         for (int v = 0; v < N; ++v) f[v] = col8(X, ld, k0, m0 + 16 * v, lane);
     }
 };
+
+// A sequence's cached rows and their tiles.
+__device__ __forceinline__ int seq_rows(const MlaStepArgs &a, int n) {
+    return (int)min((long long)max(a.lens[n], 0), (long long)a.cols * a.page);
+}
+__device__ __forceinline__ int seq_tiles(const MlaStepArgs &a, int n) {
+    return n < a.N ? (int)(((long long)seq_rows(a, n) + (1 << a.tile) - 1) >> a.tile) : 0;
+}
+// A batch's tiles shared out: see the step kernel.
+struct Share {
+    int share; // tiles per workgroup
+    int total; // tiles of all sequences
+    int per, before, mine; // sequences per lane; tiles before this lane's and in them
+};
+// Every wave forms it for itself: lane l sums the sequences l * per .. + per - 1.
+__device__ __forceinline__ Share share_out(const MlaStepArgs &a, int lane) {
+    Share s;
+    s.per = (a.N + 63) / 64;
+    s.mine = 0;
+    for (int i = 0; i < s.per; ++i) s.mine += seq_tiles(a, lane * s.per + i);
+    int x = s.mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int y = __shfl_up(x, o, 64);
+        if (lane >= o) x += y;
+    }
+    s.before = x - s.mine;
+    s.total = __builtin_amdgcn_readlane(x, 63);
+    s.share = max((s.total + a.units - 1) / a.units, 1);
+    return s;
+}
 
 // Rows of a sequence, NR at a time, from global memory over registers into an
 // LDS tile [NR][ld]: columns 0 .. d0 - 1 from x0, d0 .. d0 + d1 - 1 from x1

@@ -6,65 +6,13 @@
 #include <hip/hip_runtime.h>
 
 #include <math.h>
-#include <stdarg.h>
-#include <stdio.h>
 
-#include "gdn_mla.hpp"
+#include "gdn_check.hpp"
+#include "gdn_serve.hpp"
+
+using namespace gdn::check;
 
 namespace {
-
-gdn_status_t fail(gdn_status_t st, const char *fmt, ...) {
-    char text[256];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(text, sizeof text, fmt, ap);
-    va_end(ap);
-    return gdn::fail_detail(st, text);
-}
-gdn_status_t ok() { return gdn::fail_detail(GDN_OK, ""); }
-gdn_status_t hip_status(hipError_t e, const char *what) {
-    return e == hipSuccess ? ok() : fail(GDN_EHIP, "%s: %s", what, hipGetErrorString(e));
-}
-
-size_t align_up(size_t x) { return (x + 255) & ~(size_t)255; }
-size_t esize(int dtype) { return dtype == GDN_BF16 ? 2 : 4; }
-constexpr double LIMIT = 2147483648.0; // elements of a tensor
-constexpr double THREADS = 4294967296.0; // threads of a launch
-// What the kernels add to a position or a count (a few tiles ahead, a thread's
-// run) must not pass int32: sizes that bound those stay so much below it.
-constexpr double AHEAD = 2048.0;
-constexpr int CUS = 256;               // compute units of the chip the kernels are built for
-
-// One buffer of a call.
-struct Buf {
-    const void *p;
-    size_t n;
-    const char *name;
-    size_t align;
-    bool out, need;
-};
-
-// Required pointers, alignment, and no output over another buffer. `same`:
-// index pair of an input and an output that may be one buffer (-1: none).
-gdn_status_t check_bufs(const Buf *b, int n, const int (*same)[2] = nullptr, int nsame = 0) {
-    for (int i = 0; i < n; ++i) {
-        if (b[i].need && b[i].n && !b[i].p) return fail(GDN_EINVAL, "%s is NULL", b[i].name);
-        if (b[i].p && (uintptr_t)b[i].p % b[i].align)
-            return fail(GDN_EINVAL, "%s must be %zu-byte aligned", b[i].name, b[i].align);
-    }
-    for (int i = 0; i < n; ++i)
-        for (int j = 0; j < n; ++j) {
-            if (!b[i].out || i == j || (b[j].out && j > i)) continue;
-            if (!b[i].p || !b[j].p || !b[i].n || !b[j].n) continue;
-            bool may = false;
-            for (int k = 0; k < nsame; ++k)
-                may |= same[k][0] == j && same[k][1] == i && b[i].p == b[j].p;
-            const char *x = (const char *)b[i].p, *y = (const char *)b[j].p;
-            if (!may && x < y + b[j].n && y < x + b[i].n)
-                return fail(GDN_EINVAL, "output %s overlaps %s", b[i].name, b[j].name);
-        }
-    return GDN_OK;
-}
 
 gdn_status_t check_mla(const gdn_mla_shape_t *s) {
     if (!s) return fail(GDN_EINVAL, "shape is NULL");
@@ -181,6 +129,42 @@ size_t step_part_bytes(const gdn::MlaStepArgs &a) {
 }
 size_t step_ml_bytes(const gdn::MlaStepArgs &a) {
     return align_up((size_t)2 * a.units * a.S * a.H * 8);
+}
+
+// A call with shared prefixes: own rows' parts, then the prefixes'.
+gdn::PrefixArgs prefix_args(const gdn_mla_step_shape_t *s, int32_t G, int32_t prefix_pages) {
+    gdn::PrefixArgs p = {};
+    p.N = s->N;
+    p.S = s->S;
+    p.H = s->H;
+    p.dl = s->dl;
+    p.dr = s->dr;
+    p.pages = s->pages;
+    p.page = s->page_size;
+    p.cols = prefix_pages;
+    p.G = G;
+    p.scale = s->scale;
+    gdn::mla_prefix_plan(p, s->dtype == GDN_BF16, CUS);
+    return p;
+}
+gdn_status_t check_shared(const gdn_mla_step_shape_t *s, int32_t G, int32_t prefix_pages) {
+    const gdn_status_t st = check_step(s);
+    if (st != GDN_OK) return st;
+    if (G < 0 || (G > 0 && prefix_pages < 1)) return fail(GDN_EINVAL, "G must be >= 0, prefix_pages >= 1");
+    if (G > 0 && ((double)prefix_pages * s->page_size > LIMIT - AHEAD || (double)G * prefix_pages >= LIMIT))
+        return fail(GDN_EINVAL, "prefix table too large");
+    if (G > 0 && s->N > 0 && s->S > 0 && (double)gdn::mla_shared_join_groups(step_args(s)) * 256 >= THREADS)
+        return fail(GDN_EINVAL, "too many tokens for a launch");
+    return GDN_OK;
+}
+struct SharedSpace {
+    size_t part, ml, prefix, prefix_ml;
+    size_t all() const { return part + ml + prefix + prefix_ml; }
+};
+SharedSpace shared_space(const gdn::MlaStepArgs &a, const gdn::PrefixArgs &p) {
+    const size_t own = ((size_t)a.units + a.N) * a.S * a.H;
+    const size_t front = ((size_t)p.units + (size_t)gdn::mla_prefix_blocks(p)) * 64 * p.qt;
+    return {align_up(own * a.dl * 4), align_up(own * 8), align_up(front * p.dl * 4), align_up(front * 8)};
 }
 
 constexpr uint32_t ROPE_FLAGS = GDN_ROPE_NORM | GDN_ROPE_INTERLEAVED;
@@ -323,6 +307,113 @@ gdn_status_t gdn_mla_step(const gdn_mla_step_shape_t *s, const void *q, const vo
     if (he == hipSuccess)
         he = gdn::bracketed(gdn::K_MLA_JOIN, [&] { return gdn::launch_mla_join(a, bf, strm); }, strm);
     return hip_status(he, "gdn_mla_step launch");
+}
+
+size_t gdn_mla_step_shared_workspace_size(const gdn_mla_step_shape_t *s, int32_t G, int32_t prefix_pages) {
+    if (check_shared(s, G, prefix_pages) != GDN_OK) return 0;
+    if (G == 0) return gdn_mla_step_workspace_size(s);
+    if (s->N == 0 || s->S == 0) return 0;
+    return shared_space(step_args(s), prefix_args(s, G, prefix_pages)).all();
+}
+
+gdn_status_t gdn_mla_step_shared(const gdn_mla_step_shape_t *s, int32_t G, int32_t prefix_pages, const void *q,
+                                 const void *cache, const int32_t *block_table, const int32_t *lens,
+                                 const int32_t *prefix_table, const int32_t *prefix_lens, const int32_t *starts, void *o,
+                                 float *lse, void *ws, size_t ws_bytes, void *stream) {
+    gdn_status_t st = check_shared(s, G, prefix_pages);
+    if (st != GDN_OK) return st;
+    if (G == 0) return gdn_mla_step(s, q, cache, block_table, lens, o, lse, ws, ws_bytes, stream);
+    const size_t e = esize(s->dtype), rows = (size_t)s->N * s->S * s->H;
+    const size_t need = gdn_mla_step_shared_workspace_size(s, G, prefix_pages);
+    const bool some = rows > 0;
+    const Buf b[] = {{q, rows * (s->dl + s->dr) * e, "q", 16, false, true},
+                     {cache, (size_t)s->pages * s->page_size * (s->dl + s->dr) * e, "cache", 16, false, some},
+                     {block_table, (size_t)s->N * s->max_pages * 4, "block_table", 4, false, some},
+                     {lens, (size_t)s->N * 4, "lens", 4, false, some},
+                     {prefix_table, (size_t)G * prefix_pages * 4, "prefix_table", 4, false, some},
+                     {prefix_lens, (size_t)G * 4, "prefix_lens", 4, false, some},
+                     {starts, ((size_t)G + 1) * 4, "starts", 4, false, some},
+                     {o, rows * s->dl * e, "o", 16, true, true},
+                     {lse, rows * 4, "lse", 4, true, false},
+                     {ws, need, "workspace", 1, true, false}};
+    st = check_bufs(b, 10);
+    if (st != GDN_OK) return st;
+    if (!some) return ok();
+    if (!ws || ws_bytes < need)
+        return fail(GDN_EWORKSPACE, "gdn_mla_step_shared needs %zu bytes of workspace, got %zu", need, ws ? ws_bytes : 0);
+    if ((uintptr_t)ws % 256) return fail(GDN_EINVAL, "workspace must be 256-byte aligned");
+    gdn::MlaStepArgs a = step_args(s);
+    gdn::PrefixArgs p = prefix_args(s, G, prefix_pages);
+    const SharedSpace z = shared_space(a, p);
+    char *at = (char *)ws;
+    a.q = q;
+    a.cache = cache;
+    a.table = block_table;
+    a.lens = lens;
+    a.o = o;
+    a.lse = lse;
+    a.part = (float *)at;
+    a.part_ml = (float *)(at += z.part);
+    p.part = (float *)(at += z.ml);
+    p.part_ml = (float *)(at += z.prefix);
+    p.q = q;
+    p.cache = cache;
+    p.table = prefix_table;
+    p.plens = prefix_lens;
+    p.starts = starts;
+    const bool bf = s->dtype == GDN_BF16;
+    hipStream_t strm = (hipStream_t)stream;
+    hipError_t he = gdn::bracketed(
+        gdn::K_MLA_PREFIX, [&] { return bf ? gdn::launch_mla_prefix_bf16(p, strm) : gdn::launch_mla_prefix_f32(p, strm); },
+        strm);
+    if (he == hipSuccess)
+        he = gdn::bracketed(gdn::K_MLA_STEP, [&] { return gdn::launch_mla_step_parts(a, bf, strm); }, strm);
+    if (he == hipSuccess)
+        he = gdn::bracketed(gdn::K_MLA_JOIN, [&] { return gdn::launch_mla_shared_join(a, p, bf, strm); }, strm);
+    return hip_status(he, "gdn_mla_step_shared launch");
+}
+
+gdn_status_t gdn_mla_weights(const gdn_mla_step_shape_t *s, float decay, const void *q, const void *cache,
+                             const int32_t *block_table, const int32_t *lens, const float *lse, const int32_t *known,
+                             float *weights, void *stream) {
+    gdn_status_t st = check_step(s);
+    if (st != GDN_OK) return st;
+    if (!(decay >= 0.f && decay <= 1.f)) return fail(GDN_EINVAL, "decay must be in [0, 1]");
+    const size_t e = esize(s->dtype), rows = (size_t)s->N * s->S * s->H, slots = (size_t)s->pages * s->page_size;
+    const bool some = s->N > 0;
+    gdn::MlaWeightsArgs a;
+    a.N = s->N;
+    a.S = s->S;
+    a.H = s->H;
+    a.d = s->dl + s->dr;
+    a.pages = s->pages;
+    a.page = s->page_size;
+    a.cols = s->max_pages;
+    a.scale = s->scale;
+    a.decay = decay;
+    if ((double)gdn::mla_weights_groups(a) * 256 >= THREADS) return fail(GDN_EINVAL, "too many rows for a launch");
+    const Buf b[] = {{q, rows * a.d * e, "q", 16, false, true},
+                     {cache, slots * a.d * e, "cache", 16, false, some},
+                     {block_table, (size_t)s->N * s->max_pages * 4, "block_table", 4, false, true},
+                     {lens, (size_t)s->N * 4, "lens", 4, false, true},
+                     {lse, rows * 4, "lse", 4, false, true},
+                     {known, (size_t)s->N * 4, "known", 4, false, false},
+                     {weights, slots * 4, "weights", 4, true, some}};
+    st = check_bufs(b, 7);
+    if (st != GDN_OK) return st;
+    if (!some) return ok();
+    a.q = q;
+    a.cache = cache;
+    a.table = block_table;
+    a.lens = lens;
+    a.known = known;
+    a.lse = lse;
+    a.weights = weights;
+    hipStream_t strm = (hipStream_t)stream;
+    return hip_status(gdn::bracketed(
+                          gdn::K_MLA_WEIGHTS,
+                          [&] { return gdn::launch_mla_weights(a, s->dtype == GDN_BF16, strm); }, strm),
+                      "gdn_mla_weights launch");
 }
 
 gdn_status_t gdn_norm_rope(int64_t M, int32_t H, int32_t d, int32_t r, int32_t dtype, uint32_t flags, float eps,

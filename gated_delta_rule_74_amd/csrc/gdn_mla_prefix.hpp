@@ -1,0 +1,296 @@
+// Attention of a serving batch against prefixes that groups of its sequences
+// share, and the join with their own rows.
+//
+// A prefix's rows are seen by every query of its group, thousands of them, so
+// this is a matrix product as in the attention of a prompt, without a mask: S^T =
+// K Q^T and O^T = V^T P^T over tiles of cached rows in LDS, a lane owning one
+// query, the probabilities at once the operand of the second product, V read
+// from the same tile by transposing reads. A workgroup takes 64 * QT queries
+// of a group (wave w the next 16 * QT of them, which stay in registers) and walks
+// tiles of rows that its four waves share, two tiles in LDS, the next one requested before
+// this one is used.
+// The walks of all blocks of queries, end to end, are cut into equal shares,
+// one for each workgroup the chip holds, whatever the groups' sizes and
+// lengths. Every piece leaves its sums as a part, at place (share + block): both
+// only grow from one piece to the next, and one of them does. The join adds a query's parts and those of its own
+// rows (mla_step_kernel's, at place share + sequence).
+#pragma once
+
+#include "gdn_serve.hpp"
+
+namespace gdn {
+
+constexpr float PREFIX_RAISE = 8.f; // lazy maximum, as in the forward over expanded heads
+
+template <bool BF, int DLP, int KS, int QT> struct PrefixShape {
+    using S = typename Op<BF>::S;
+    static constexpr int NT = 256, V = Op<BF>::VEC, DP = 32 * KS, LD = DP + MLA_PAD<BF>, MV = DLP / 16, QB = 64 * QT,
+                         KT = BF && DLP <= 256 ? 64 : 32, RP = NT / (DP / V) > 0 ? NT / (DP / V) : 1,
+                         NIT = (KT + RP - 1) / RP, TILE = KT * LD;
+};
+constexpr int prefix_tile(bool bf, int dlp) { return bf && dlp <= 256 ? 64 : 32; } // rows of a tile
+
+// The groups, shared out: lane l holds groups l * per .. + per - 1.
+struct Line {
+    int per, most;          // groups per lane; largest start before this lane's
+    int blocks0, blocks;    // blocks of queries before this lane's, in them
+    long long tiles0, tiles; // their walks' tiles
+    long long total, share; // tiles of all walks, of a workgroup's share
+};
+struct Group {
+    int lo, hi;        // its sequences
+    int rows, blocks, tiles; // its queries, their blocks, the tiles of its prefix
+};
+__device__ __forceinline__ int prefix_rows(const PrefixArgs &a, int g) {
+    return (int)min((long long)max(a.plens[g], 0), (long long)a.cols * a.page);
+}
+__device__ __forceinline__ int start_of(const PrefixArgs &a, int g) { return min(max(a.starts[g], 0), a.N); }
+// most: the largest start before (starts that go back count as that)
+__device__ __forceinline__ Group group_of(const PrefixArgs &a, int g, int &most, int kt) {
+    Group x;
+    x.lo = max(most, start_of(a, g));
+    x.hi = max(x.lo, start_of(a, g + 1));
+    most = x.lo;
+    x.rows = (x.hi - x.lo) * a.S * a.H;
+    x.blocks = (x.rows + 64 * a.qt - 1) / (64 * a.qt);
+    x.tiles = (prefix_rows(a, g) + kt - 1) / kt;
+    return x;
+}
+__device__ __forceinline__ Line line_of(const PrefixArgs &a, int lane, int kt) {
+    Line s;
+    s.per = (a.G + 63) / 64;
+    int m = 0;
+    for (int i = 0; i < s.per; ++i)
+        if (lane * s.per + i < a.G) m = max(m, start_of(a, lane * s.per + i));
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int y = __shfl_up(m, o, 64);
+        if (lane >= o) m = max(m, y);
+    }
+    const int up = __shfl_up(m, 1, 64);
+    s.most = lane ? up : 0;
+    s.blocks = 0;
+    s.tiles = 0;
+    int most = s.most;
+    for (int i = 0; i < s.per; ++i) {
+        if (lane * s.per + i >= a.G) break;
+        const Group x = group_of(a, lane * s.per + i, most, kt);
+        s.blocks += x.blocks;
+        s.tiles += (long long)x.blocks * x.tiles;
+    }
+    int b = s.blocks;
+    long long t = s.tiles;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int y = __shfl_up(b, o, 64);
+        const long long z = __shfl_up(t, o, 64);
+        if (lane >= o) {
+            b += y;
+            t += z;
+        }
+    }
+    s.blocks0 = b - s.blocks;
+    s.tiles0 = t - s.tiles;
+    s.total = __shfl(t, 63, 64);
+    // at least four tiles: a part costs as much to write as so many rows to read
+    s.share = max((s.total + a.units - 1) / a.units, 4LL);
+    return s;
+}
+
+// Tiles [t0, t1) of group g's prefix for the queries row0 .. of its `rows`; the sums go to part `slot`.
+template <bool BF, int DLP, int KS, int QT, class S>
+__device__ __forceinline__ void prefix_piece(const PrefixArgs a, int g, int lo, int rows, int row0, int t0, int t1,
+                                             int slot, S *T0, float *bias0) {
+    using P = PrefixShape<BF, DLP, KS, QT>;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15,
+              gr = lane >> 4;
+    const int d = a.dl + a.dr, ng = d / P::V, rp = P::NT / ng, n = prefix_rows(a, g);
+    const int *tb = a.table + (size_t)g * a.cols;
+    // the table entry and the cache row of tile row `lane`, requested two tiles and known one tile ahead
+    int entry = -1, row = -1;
+    auto ask = [&](int tile) {
+        if (lane < P::KT) entry = tb[(unsigned)min(tile * P::KT + lane, n - 1) / (unsigned)a.page];
+    };
+    auto place = [&](int tile) {
+        const int pos = tile * P::KT + lane;
+        row = lane < P::KT && pos < n && (unsigned)entry < (unsigned)a.pages
+                  ? entry * a.page + (int)((unsigned)pos % (unsigned)a.page)
+                  : -1;
+    };
+    // a thread loads one 16-byte column of every rp-th row of a tile
+    const int j0 = tid < rp * ng ? tid / ng : P::KT, c0 = (tid % ng) * P::V;
+    u32x4 reg[P::NIT];
+    auto fetch = [&] {
+#pragma unroll
+        for (int m = 0; m < P::NIT; ++m) {
+            const int j = j0 + m * rp, p = __shfl(row, j & 63, 64);
+            const S *src = (const S *)a.cache + (size_t)(unsigned)p * (unsigned)d + c0;
+            reg[m] = load16(j < P::KT && p >= 0 ? src : (const S *)&mla_zeros);
+        }
+    };
+    auto stash = [&](int buf) {
+        S *T = T0 + buf * P::TILE;
+#pragma unroll
+        for (int m = 0; m < P::NIT; ++m) {
+            const int j = j0 + m * rp;
+            if (j < P::KT) *reinterpret_cast<u32x4 *>(T + j * P::LD + c0) = reg[m];
+        }
+        if (wave == 0 && lane < P::KT) bias0[buf * P::KT + lane] = row >= 0 ? 0.f : -INFINITY;
+    };
+    ask(t0);
+    place(t0);
+    fetch();
+    Frag<BF> Q[QT][KS];
+    const S *qp = (const S *)a.q + ((size_t)lo * a.S * a.H) * d;
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        const int i = row0 + (wave * QT + t) * 16 + r;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            const int c = 32 * k + 8 * gr;
+            Q[t][k] = row8_if(i < rows && c < d, qp + (size_t)i * d + c);
+        }
+    }
+    lds_barrier(); // (the previous piece's readers are done)
+    // columns past d are never stored below: zero once
+    for (int w = (P::DP - d) / P::V, e = tid; e < 2 * P::KT * w; e += P::NT)
+        *reinterpret_cast<u32x4 *>(T0 + e / w * P::LD + d + e % w * P::V) = u32x4{0u, 0u, 0u, 0u};
+    f32x4 O[QT][P::MV];
+    float m[QT], l[QT];
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        m[t] = -INFINITY;
+        l[t] = 0.f;
+#pragma unroll
+        for (int v = 0; v < P::MV; ++v) O[t][v] = zero4();
+    }
+    const float c2 = a.scale * (float)LOG2E;
+    stash(0);
+    if (t0 + 1 < t1) ask(t0 + 1);
+    lds_barrier();
+    wait_vmem(); // (the queries are there: else their first use in the loop waits for the tile in flight)
+    for (int tile = t0; tile < t1; ++tile) {
+        const int buf = (tile - t0) & 1;
+        const S *T = T0 + buf * P::TILE;
+        const float *bias = bias0 + buf * P::KT;
+        if (tile + 1 < t1) {
+            place(tile + 1);
+            if (tile + 2 < t1) ask(tile + 2);
+            fetch();
+        }
+#pragma unroll 1
+        for (int u = 0; u < P::KT / 32; ++u) {
+            // absent rows: scores of -inf from the start (their keys are zero)
+            f32x4 X[QT][2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const f32x4 bj = *reinterpret_cast<const f32x4 *>(bias + 32 * u + 16 * j + 4 * gr);
+#pragma unroll
+                for (int t = 0; t < QT; ++t) X[t][j] = bj;
+            }
+            const S *kr = T + (32 * u + r) * P::LD + 8 * gr;
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const Frag<BF> kf = row8(kr + 16 * j * P::LD + 32 * k);
+#pragma unroll
+                    for (int t = 0; t < QT; ++t) X[t][j] = mma8(kf, Q[t][k], X[t][j]);
+                }
+            bool raise = false;
+            float mx[QT];
+#pragma unroll
+            for (int t = 0; t < QT; ++t) {
+                float x = X[t][0][0];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x = fmaxf(x, X[t][j][e]);
+                mx[t] = x * c2;
+                raise |= mx[t] > m[t] + PREFIX_RAISE;
+            }
+            if (__any(raise)) {
+#pragma unroll
+                for (int t = 0; t < QT; ++t) {
+                    const float mn = fmaxf(m[t], max4g(mx[t]));
+                    const float f = mn == -INFINITY ? 1.f : exp2_fast(m[t] - mn);
+                    m[t] = mn;
+                    l[t] *= f;
+#pragma unroll
+                    for (int v = 0; v < P::MV; ++v) O[t][v] *= f;
+                }
+            }
+            Frag<BF> pf[QT];
+#pragma unroll
+            for (int t = 0; t < QT; ++t) {
+                const float mt = m[t] == -INFINITY ? 0.f : m[t];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) X[t][j][e] = exp2_fast(fmaf(X[t][j][e], c2, -mt));
+                const f32x4 sum = X[t][0] + X[t][1];
+                l[t] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                pf[t] = acc8<BF>(X[t][0], X[t][1]);
+            }
+#pragma unroll
+            for (int v = 0; v < P::MV; ++v) {
+                const Frag<BF> vf = col8(T, P::LD, 32 * u, 16 * v, lane);
+#pragma unroll
+                for (int t = 0; t < QT; ++t) O[t][v] = mma8(vf, pf[t], O[t][v]);
+            }
+        }
+        if (tile + 1 < t1) stash(buf ^ 1); // (its last readers passed the barrier before this tile)
+        lds_barrier();
+    }
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        const int in = (wave * QT + t) * 16 + r;
+        const float sum = sum4g(l[t]);
+        if (row0 + in >= rows) continue;
+        const size_t at = (size_t)slot * P::QB + in;
+#pragma unroll
+        for (int v = 0; v < P::MV; ++v) {
+            const int c = 16 * v + 4 * gr;
+            if (c < a.dl) store4(a.part + at * a.dl + c, O[t][v]);
+        }
+        if (gr == 0) *reinterpret_cast<f32x2 *>(a.part_ml + at * 2) = f32x2{m[t], sum};
+    }
+}
+
+// waves per SIMD that the registers of a wave allow
+template <bool BF> constexpr int prefix_waves(int dlp, int qt) { return dlp <= (BF && qt == 2 ? 256 : BF ? 384 : 128) ? 2 : 1; }
+
+template <bool BF, int DLP, int KS, int QT>
+__global__ __launch_bounds__(256, prefix_waves<BF>(DLP, QT)) void mla_prefix_kernel(PrefixArgs a) {
+    using P = PrefixShape<BF, DLP, KS, QT>;
+    __shared__ __align__(16) typename P::S T[2 * P::TILE];
+    __shared__ __align__(16) float bias[2 * P::KT];
+    const int lane = threadIdx.x & 63, unit = blockIdx.x;
+    const Line s = line_of(a, lane, P::KT);
+    const long long from = unit * s.share, to = min(from + s.share, s.total);
+    if (from >= to) return;
+    // the group the share begins in
+    int owner = __builtin_ctzll(__ballot(s.tiles0 + s.tiles > from));
+    int g = owner * s.per, most = __shfl(s.most, owner, 64), block0 = __shfl(s.blocks0, owner, 64);
+    long long begin = __shfl(s.tiles0, owner, 64);
+    Group x = group_of(a, g, most, P::KT);
+    for (long long at = from; at < to;) {
+        while (begin + (long long)x.blocks * x.tiles <= at) {
+            begin += (long long)x.blocks * x.tiles;
+            block0 += x.blocks;
+            x = group_of(a, ++g, most, P::KT);
+        }
+        const int block = (int)((at - begin) / x.tiles);
+        const long long first = begin + (long long)block * x.tiles, stop = min(first + x.tiles, to);
+        prefix_piece<BF, DLP, KS, QT>(a, g, x.lo, x.rows, block * P::QB, (int)(at - first), (int)(stop - first),
+                                      unit + block0 + block, T, bias);
+        at = stop;
+    }
+}
+
+template <bool BF, int DLP, int KS, int QT> hipError_t prefix_run(const PrefixArgs &a, hipStream_t st) {
+    hipLaunchKernelGGL((mla_prefix_kernel<BF, DLP, KS, QT>), dim3((unsigned)a.units), dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+} // namespace gdn

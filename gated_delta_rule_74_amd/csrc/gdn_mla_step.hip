@@ -38,34 +38,6 @@ constexpr float STEP_RAISE = 8.f; // lazy maximum, as in the forward over expand
 // whole it finishes, of others it leaves a part. Only the first and the last
 // piece of a share can be parts, which gives each workgroup two places to
 // leave them.
-__device__ __forceinline__ int seq_rows(const MlaStepArgs &a, int n) {
-    return (int)min((long long)max(a.lens[n], 0), (long long)a.cols * a.page);
-}
-__device__ __forceinline__ int seq_tiles(const MlaStepArgs &a, int n) {
-    return n < a.N ? (int)(((long long)seq_rows(a, n) + (1 << a.tile) - 1) >> a.tile) : 0;
-}
-struct Share {
-    int share; // tiles per workgroup
-    int total; // tiles of all sequences
-    int per, before, mine; // sequences per lane; tiles before this lane's and in them
-};
-// Every wave forms it for itself: lane l sums the sequences l * per .. + per - 1.
-__device__ __forceinline__ Share share_out(const MlaStepArgs &a, int lane) {
-    Share s;
-    s.per = (a.N + 63) / 64;
-    s.mine = 0;
-    for (int i = 0; i < s.per; ++i) s.mine += seq_tiles(a, lane * s.per + i);
-    int x = s.mine;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int y = __shfl_up(x, o, 64);
-        if (lane >= o) x += y;
-    }
-    s.before = x - s.mine;
-    s.total = __builtin_amdgcn_readlane(x, 63);
-    s.share = max((s.total + a.units - 1) / a.units, 1);
-    return s;
-}
 // where workgroup w leaves its part of a sequence whose tiles begin at `begin`
 __device__ __forceinline__ int part_slot(int w, int begin, int share) { return 2 * w + (begin > w * share ? 1 : 0); }
 
@@ -373,7 +345,9 @@ __device__ __forceinline__ void step_piece(const MlaStepArgs a, int nq, int k0, 
     }
 }
 
-template <bool BF, int DLP, int MT>
+// PARTS: every piece is left as a part, at place unit + sequence (both only grow from
+// one piece to the next, and one of them does)
+template <bool BF, int DLP, int MT, bool PARTS = false>
 __global__ __launch_bounds__(256, (DLP <= 128 && MT == 1 ? 3 : !BF && DLP == 256 ? 1 : 2)) void mla_step_kernel(MlaStepArgs a) {
     using P = StepShape<BF, DLP, MT>;
     using S = typename P::S;
@@ -401,8 +375,9 @@ __global__ __launch_bounds__(256, (DLP <= 128 && MT == 1 ? 3 : !BF && DLP == 256
         }
         const int stop = min(begin + tiles, to);
         step_piece<BF, DLP, MT>(a, nq, (at - begin) << a.tile, (stop - begin) << a.tile, row0,
-                                at == begin && stop == begin + tiles ? -1 : part_slot(unit, begin, sh.share), smem, Qs,
-                                bias, Ms, Ss);
+                                PARTS                                           ? unit + nq
+                                : at == begin && stop == begin + tiles ? -1 : part_slot(unit, begin, sh.share),
+                                smem, Qs, bias, Ms, Ss);
         at = stop;
     }
 }
@@ -482,7 +457,7 @@ template <bool BF> __global__ __launch_bounds__(256) void mla_join_kernel(MlaSte
     if (a.lse && c == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
 }
 
-static int step_class(int dl) {
+int step_class(int dl) {
     return dl <= 64 ? 64 : dl <= 128 ? 128 : dl <= 192 ? 192 : dl <= 256 ? 256 : dl <= 384 ? 384 : 512;
 }
 
@@ -513,27 +488,30 @@ void mla_step_plan(MlaStepArgs &a, bool bf16, int cus) {
 static long long step_grid(const MlaStepArgs &a) { // (eight shares side by side, see the kernel)
     return ((long long)a.units + 7) / 8 * 8 * (((long long)a.S * a.H + 16 * a.mt - 1) / (16 * a.mt));
 }
-template <bool BF, int DLP, int MT> static hipError_t step_run(const MlaStepArgs &a, hipStream_t st) {
-    hipLaunchKernelGGL((mla_step_kernel<BF, DLP, MT>), dim3((unsigned)step_grid(a)), dim3(256), 0, st, a);
+template <bool BF, int DLP, int MT, bool PARTS> static hipError_t step_run(const MlaStepArgs &a, hipStream_t st) {
+    hipLaunchKernelGGL((mla_step_kernel<BF, DLP, MT, PARTS>), dim3((unsigned)step_grid(a)), dim3(256), 0, st, a);
     return hipGetLastError();
 }
-template <bool BF, int DLP> static hipError_t step_rows(const MlaStepArgs &a, hipStream_t st) {
+template <bool BF, int DLP, bool PARTS> static hipError_t step_rows(const MlaStepArgs &a, hipStream_t st) {
     if constexpr (DLP > 64 && DLP <= 256)
-        if (a.mt == 2) return step_run<BF, DLP, 2>(a, st);
-    return step_run<BF, DLP, 1>(a, st);
+        if (a.mt == 2) return step_run<BF, DLP, 2, PARTS>(a, st);
+    return step_run<BF, DLP, 1, PARTS>(a, st);
 }
-template <bool BF> static hipError_t step_launch(const MlaStepArgs &a, hipStream_t st) {
+template <bool BF, bool PARTS> static hipError_t step_launch(const MlaStepArgs &a, hipStream_t st) {
     switch (step_class(a.dl)) {
-    case 64: return step_rows<BF, 64>(a, st);
-    case 128: return step_rows<BF, 128>(a, st);
-    case 192: return step_rows<BF, 192>(a, st);
-    case 256: return step_rows<BF, 256>(a, st);
-    case 384: return step_rows<BF, 384>(a, st);
-    default: return step_rows<BF, 512>(a, st);
+    case 64: return step_rows<BF, 64, PARTS>(a, st);
+    case 128: return step_rows<BF, 128, PARTS>(a, st);
+    case 192: return step_rows<BF, 192, PARTS>(a, st);
+    case 256: return step_rows<BF, 256, PARTS>(a, st);
+    case 384: return step_rows<BF, 384, PARTS>(a, st);
+    default: return step_rows<BF, 512, PARTS>(a, st);
     }
 }
 hipError_t launch_mla_step(const MlaStepArgs &a, bool bf16, hipStream_t st) {
-    return bf16 ? step_launch<true>(a, st) : step_launch<false>(a, st);
+    return bf16 ? step_launch<true, false>(a, st) : step_launch<false, false>(a, st);
+}
+hipError_t launch_mla_step_parts(const MlaStepArgs &a, bool bf16, hipStream_t st) {
+    return bf16 ? step_launch<true, true>(a, st) : step_launch<false, true>(a, st);
 }
 
 // Launch of the join. The parts of an average sequence decide how many threads share them.

@@ -12,7 +12,7 @@
 // sums (256 sequences: 8 us); with more tokens than FILL_ONE a second launch does that, and
 // the moves of new pages with it, over the whole chip (1024 prompts of 400
 // tokens, 26000 pages: 39 us in one workgroup, 16 + 13 us so).
-#include "gdn_mla.hpp"
+#include "gdn_serve.hpp"
 
 namespace gdn {
 
@@ -217,6 +217,41 @@ hipError_t launch_page_plan(const PagePlanArgs &a, hipStream_t st) {
 }
 hipError_t launch_page_fill(const PagePlanArgs &a, hipStream_t st) {
     hipLaunchKernelGGL(page_fill_kernel, dim3((unsigned)((a.cap + FT - 1) / FT)), dim3(FT), 0, st, a);
+    return hipGetLastError();
+}
+
+// Pages behind shortened sequences, pushed on the stack: page_plan's first
+// half, with the columns between two lengths. One workgroup, bound by its chain
+// of sums; the pages are spread over the threads, found by a binary search.
+__global__ __launch_bounds__(PL) void page_trim_kernel(PageTrimArgs a) {
+    __shared__ int ends[PL], from_s[PL];
+    __shared__ int w1[PL / 64][1];
+    const int tid = threadIdx.x, page = a.page;
+    const int room = (int)min((long long)a.cols * page, 2147483647LL); // tokens a table row holds
+    int top = min(max(*a.n_free, 0), a.F);
+    for (int c = 0; c < a.N; c += PL) {
+        const int i = c + tid;
+        const int len = i < a.N ? min(max(a.lens[i], 0), room) : 0;
+        const int left = i < a.N ? pages_of(min(max(a.fresh[i], 0), len), page) : 0;
+        const int back = pages_of(len, page) - left;
+        if (!__syncthreads_or(back > 0)) continue;
+        int x[1] = {back}, total[1];
+        scan<PL>(x, w1, total);
+        ends[tid] = x[0];
+        from_s[tid] = left - (x[0] - back); // first column, less the pages before this sequence's
+        __syncthreads();
+        for (int k = tid; k < total[0]; k += PL) {
+            const int o = owner(ends, PL, k);
+            if (k < a.F - top) a.stack[top + k] = a.table[(size_t)(c + o) * a.cols + from_s[o] + k];
+        }
+        top = (int)min((long long)top + total[0], (long long)a.F);
+        __syncthreads();
+    }
+    if (tid == 0) *a.n_free_out = top;
+}
+
+hipError_t launch_page_trim(const PageTrimArgs &a, hipStream_t st) {
+    hipLaunchKernelGGL(page_trim_kernel, dim3(1), dim3(PL), 0, st, a);
     return hipGetLastError();
 }
 

@@ -220,6 +220,17 @@ gdn_status_t gdn_step_tokens(int32_t N, int32_t S, int32_t H, int32_t dk, int32_
                              const float *g, const float *beta, const float *A_log, const float *D,
                              const float *h_in, float *h_out, void *o, void *stream);
 
+/* The states after the accepted tokens of a draft: the recurrence of
+ * gdn_step_tokens over the first counts[n] tokens of sequence n (values
+ * outside [0, S] are clamped), without their outputs, so without q. Layouts,
+ * flags and h_in / h_out (NULL: zero state; the same buffer: in place) as in
+ * gdn_step_tokens; k [N,S,H,dk], v [N,S,H,dv], g, beta [N,S,H], counts [N]
+ * int32. Tokens past a count are not read. The state is read and written once;
+ * a sequence whose count is 0 keeps its state. */
+gdn_status_t gdn_step_commit(int32_t N, int32_t S, int32_t H, int32_t dk, int32_t dv, int32_t dtype, uint32_t flags,
+                             const void *k, const void *v, const float *g, const float *beta, const float *A_log,
+                             const int32_t *counts, const float *h_in, float *h_out, void *stream);
+
 /* ---------------------------------------------------------------------------
  * Latent attention and its paged cache: the softmax-attention layers that sit
  * between GDN layers in the hybrid stack ("HyMo-434M documentation portal",
@@ -361,6 +372,101 @@ gdn_status_t gdn_page_plan(int32_t N, int32_t max_pages, int32_t n_pages, int32_
                            const int32_t *n_free, int32_t *lens_out, int32_t *n_free_out, int32_t *granted,
                            int32_t *starts, int32_t *slots, int32_t *positions, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Serving beside the plain step: prefixes that a batch shares, caches that may
+ * not grow, drafts. The rules at the top of this file hold.
+ */
+
+/* gdn_mla_step for sequences that share long prefixes: sequences starts[g] ..
+ * starts[g + 1] - 1 (starts [G+1] int32, non-decreasing, clamped to [0, N])
+ * have the prefix_lens[g] rows of prefix_table row g ([G,prefix_pages] int32,
+ * pages of the same cache) before their own, so that token s of sequence n
+ * sees those rows and its own rows j <= lens[n] - S + s (block_table, lens).
+ * Sequences of no group have no prefix. A token at a position before 0
+ * (lens[n] - S + s < 0: padding) sees nothing: o = 0, lse = -inf. The prefix's
+ * rows are read once for many of the group's queries instead of once for each
+ * sequence. s->N, max_pages and the limits of gdn_mla_step; prefix_pages *
+ * page_size at most 2^31 - 2048, G * prefix_pages below 2^31. G = 0: no prefix
+ * (the last three arrays are not read). lse may be NULL. ws:
+ * gdn_mla_step_shared_workspace_size() bytes, 256-byte aligned. */
+size_t gdn_mla_step_shared_workspace_size(const gdn_mla_step_shape_t *s, int32_t G, int32_t prefix_pages);
+gdn_status_t gdn_mla_step_shared(const gdn_mla_step_shape_t *s, int32_t G, int32_t prefix_pages, const void *q,
+                                 const void *cache, const int32_t *block_table, const int32_t *lens,
+                                 const int32_t *prefix_table, const int32_t *prefix_lens, const int32_t *starts, void *o,
+                                 float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/* Attention weight of every cached row, added up over steps (what gdn_mla_evict
+ * goes by). q, cache, block_table, lens as in gdn_mla_step, lse its result:
+ *   weights[slot of row j] = (j < known[n] ? decay * weights[slot of row j] : 0)
+ *       + sum over the tokens s that see row j, and heads h, of
+ *         exp(scale q_{n,s,h} . row_j - lse_{n,s,h})
+ * weights [pages,page_size] fp32, known [N] int32 or NULL (lens[n] - S: the new
+ * tokens' rows begin at 0, whatever their slots held). Rows of no sequence keep
+ * their weights; a row in two tables ends up with either's. decay in [0, 1].
+ * Tokens with lse = -inf add nothing. Shape limits of gdn_mla_step. */
+gdn_status_t gdn_mla_weights(const gdn_mla_step_shape_t *s, float decay, const void *q, const void *cache,
+                             const int32_t *block_table, const int32_t *lens, const float *lse, const int32_t *known,
+                             float *weights, void *stream);
+
+/* Drops the cached rows of least weight. Sequence n keeps k = min(keep[n],
+ * lens[n]) rows (at least 0): the first min(first, k), of what is left of k up
+ * to `recent` of the last, and then those of the highest weight (equal ones:
+ * the lowest positions; a NaN counts as the highest, -0 as 0). They move to the
+ * front in their order, rows of cache [pages,page_size,d] and weights
+ * [pages,page_size] fp32 alike, in place, and lens_out[n] = k; what stands
+ * behind them in the sequence's pages stays as it was. Sequences with keep[n]
+ * >= lens[n] are not touched. Pages are not given back here (several layers
+ * may share a table): gdn_page_trim does that. Rows whose table entry lies outside
+ * [0, pages) count as lighter than any other and are neither read nor written.
+ * A page may be in use by one sequence only. row_bytes: bytes of a cache row, a
+ * multiple of 16 up to 2304; first, recent >= 0. ws:
+ * gdn_mla_evict_workspace_size() bytes, 256-byte aligned. */
+size_t gdn_mla_evict_workspace_size(int32_t N, int32_t max_pages, int32_t page_size, int32_t row_bytes);
+gdn_status_t gdn_mla_evict(int32_t N, int32_t max_pages, int32_t pages, int32_t page_size, int32_t row_bytes,
+                           int32_t first, int32_t recent, const int32_t *block_table, const int32_t *lens,
+                           const int32_t *keep, float *weights, void *cache, int32_t *lens_out, void *ws,
+                           size_t ws_bytes, void *stream);
+
+/* Pages behind sequences that became shorter (rejected drafts, evicted rows)
+ * back on the stack of free pages: in order of the sequences and then of their
+ * columns, the pages of columns ceil(new_lens[n] / page_size) ..
+ * ceil(lens[n] / page_size) - 1 of block_table [N,max_pages] are pushed on
+ * free_pages [n_pages], of which n_free are free before and n_free_out
+ * afterwards (may be the same). Lengths are clamped to what a row holds,
+ * new_lens to [0, lens]; pages for which the stack has no room are lost. The
+ * table is not changed (entries behind a length are not in use). All int32. */
+gdn_status_t gdn_page_trim(int32_t N, int32_t max_pages, int32_t n_pages, int32_t page_size, const int32_t *lens,
+                           const int32_t *new_lens, const int32_t *block_table, int32_t *free_pages,
+                           const int32_t *n_free, int32_t *n_free_out, void *stream);
+
+/* Drafted tokens against the target's distributions, from given random numbers,
+ * so that what is emitted is distributed as if the target had drawn it alone.
+ *   logits       [N,S+1,V] the target's, row i where draft[n,i] is to stand
+ *   draft        [N,S] int32, of which draft_lens[n] (NULL: S; clamped) count
+ *   draft_logits [N,S,V] what the draft was drawn from, or NULL: drafts without
+ *                a distribution (q = 1 at the drafted token)
+ *   temperature  [N] fp32 or NULL (1); T <= 0 (or NaN): greedy
+ *   uniforms     [N,S+1] fp32 in [0, 1) (clamped to it; NaN is 0)
+ * With p_i = softmax(logits[n,i] / T), q_i likewise: draft x = draft[n,i] is
+ * accepted while uniforms[n,i] q_i(x) < p_i(x). At the first one that is not,
+ * a token is drawn from max(p_i - q_i, 0); after the last one from p_i of the
+ * next row: the lowest v with C(v) > uniforms[n,S] C(V-1), C the running sum.
+ * Greedy: a draft is accepted when it is the row's first largest logit, which is
+ * also the token drawn. Logits of -inf have probability 0.
+ *   accepted [N] int32   drafts accepted
+ *   tokens [N,S+1] int32 those, then the token drawn, then -1
+ *   logprobs [N,S+1] fp32 or NULL: log p_i of each token (at T = 1 where greedy), 0 behind them
+ * A target row without a distribution (a NaN, +inf, nothing above -inf)
+ * accepts nothing and draws -1 (with logprob 0). A draft outside [0, V), or whose row of
+ * draft_logits has no distribution, is not accepted and the token is drawn from p_i.
+ * Sums run in fp64. N, S >= 0, V >= 1; each tensor below 2^31 elements; ws:
+ * gdn_draft_verify_workspace_size() bytes, 256-byte aligned. */
+size_t gdn_draft_verify_workspace_size(int32_t N, int32_t S, int32_t V, int32_t dtype);
+gdn_status_t gdn_draft_verify(int32_t N, int32_t S, int32_t V, int32_t dtype, const void *logits, const int32_t *draft,
+                              const int32_t *draft_lens, const void *draft_logits, const float *temperature,
+                              const float *uniforms, int32_t *accepted, int32_t *tokens, float *logprobs, void *ws,
+                              size_t ws_bytes, void *stream);
+
 /* Timing aid for benchmarks (no effect on results). While `events` is
  * non-NULL, every kernel the library launches from this thread is bracketed
  * by hipEventRecord calls on the launch's stream: events[2i] before launch i
@@ -378,7 +484,11 @@ int32_t gdn_time_launches(void *const *events, int32_t n);
  * key and value gradients), 11 sum of the shared rotary key's gradient, 12
  * attention against the paged cache, 13 join of its parts, 14 norm and
  * rotation, 15 their backward, 16 sum of the norm weight's gradient, 17 cache
- * write, 18 page plan, 19 slots of a page plan; -1 when i is out of range. A
+ * write, 18 page plan, 19 slots of a page plan, 20 attention against shared
+ * prefixes, 21 attention weights of cached rows, 22 choice of the rows that an
+ * eviction keeps, 23 their move, 24 pages given back, 25 sums of draft and
+ * target distributions, 26 sums of what is left of a rejected draft's, 27 the
+ * tokens drawn, 28 state after accepted tokens; -1 when i is out of range. A
  * forward call may launch its two kernels several times each, over
  * consecutive chunk ranges (prep of the next range runs on a second stream
  * while the serial pass works on the current one), and a serial pass run as a
