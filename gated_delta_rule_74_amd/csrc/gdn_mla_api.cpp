@@ -163,7 +163,7 @@ struct SharedSpace {
 };
 SharedSpace shared_space(const gdn::MlaStepArgs &a, const gdn::PrefixArgs &p) {
     const size_t own = ((size_t)a.units + a.N) * a.S * a.H;
-    const size_t front = ((size_t)p.units + (size_t)gdn::mla_prefix_blocks(p)) * 64 * p.qt;
+    const size_t front = ((size_t)p.units + (size_t)gdn::mla_prefix_blocks(p)) * p.qb;
     return {align_up(own * a.dl * 4), align_up(own * 8), align_up(front * p.dl * 4), align_up(front * 8)};
 }
 

@@ -5,9 +5,8 @@
 // this is a matrix product as in the attention of a prompt, without a mask: S^T =
 // K Q^T and O^T = V^T P^T over tiles of cached rows in LDS, a lane owning one
 // query, the probabilities at once the operand of the second product, V read
-// from the same tile by transposing reads. A workgroup takes 64 * QT queries
-// of a group (wave w the next 16 * QT of them, which stay in registers) and walks
-// tiles of rows that its four waves share, two tiles in LDS, the next one requested before
+// from the same tile by transposing reads. A wave takes 16 * QT queries
+// of a group, which stay in registers; the waves of a workgroup walk tiles of rows that they share, two tiles in LDS, the next one requested before
 // this one is used.
 // The walks of all blocks of queries, end to end, are cut into equal shares,
 // one for each workgroup the chip holds, whatever the groups' sizes and
@@ -22,13 +21,21 @@ namespace gdn {
 
 constexpr float PREFIX_RAISE = 8.f; // lazy maximum, as in the forward over expanded heads
 
+// Waves of a workgroup, and rows of a tile, by the padded latent columns: beyond 256 the
+// operands of 16 queries fill what two waves per SIMD have of registers, so
+// eight waves share a tile (what one wave per SIMD would hold for 32 the compiler spills).
+__host__ __device__ constexpr int prefix_nw(bool bf, int dlp) { return bf && dlp > 256 ? 8 : 4; }
+__host__ __device__ constexpr int prefix_tile(bool bf, int dlp) { return bf && (dlp <= 128 || dlp > 256) ? 64 : 32; }
+// A tile in LDS: rows of RU 16-byte units, unit u of row j at place u ^ (j & XM) of
+// its row, so that what a read takes of eight (sixteen) rows at once lies in different banks without padding.
 template <bool BF, int DLP, int KS, int QT> struct PrefixShape {
     using S = typename Op<BF>::S;
-    static constexpr int NT = 256, V = Op<BF>::VEC, DP = 32 * KS, LD = DP + MLA_PAD<BF>, MV = DLP / 16, QB = 64 * QT,
-                         KT = BF && DLP <= 256 ? 64 : 32, RP = NT / (DP / V) > 0 ? NT / (DP / V) : 1,
-                         NIT = (KT + RP - 1) / RP, TILE = KT * LD;
+    static constexpr int NW = prefix_nw(BF, DLP), NT = 64 * NW, V = Op<BF>::VEC, MV = DLP / 16, QB = 16 * NW * QT,
+                         KT = prefix_tile(BF, DLP),
+                         RU = (32 * KS / V + 7) / 8 * 8, XM = RU % 16 ? 7 : 15, TILE = KT * RU, // (units)
+                         NL = TILE / NT; // loads of a thread
+    static_assert(TILE % NT == 0 && KT % NW == 0, "every load moves 64 units of a wave's rows");
 };
-constexpr int prefix_tile(bool bf, int dlp) { return bf && dlp <= 256 ? 64 : 32; } // rows of a tile
 
 // The groups, shared out: lane l holds groups l * per .. + per - 1.
 struct Line {
@@ -52,7 +59,7 @@ __device__ __forceinline__ Group group_of(const PrefixArgs &a, int g, int &most,
     x.hi = max(x.lo, start_of(a, g + 1));
     most = x.lo;
     x.rows = (x.hi - x.lo) * a.S * a.H;
-    x.blocks = (x.rows + 64 * a.qt - 1) / (64 * a.qt);
+    x.blocks = (x.rows + a.qb - 1) / a.qb;
     x.tiles = (prefix_rows(a, g) + kt - 1) / kt;
     return x;
 }
@@ -97,14 +104,75 @@ __device__ __forceinline__ Line line_of(const PrefixArgs &a, int lane, int kt) {
     return s;
 }
 
+// Sixteen bytes of every lane from global memory to 64 units of LDS that follow each other
+// (dst, the same for all lanes). Counted as a vector memory load: a wait for
+// those and a barrier make it visible. Written by hand, since the compiler would
+// have every LDS read behind it wait for it, the other tile's as well. (m0: the compiler
+// keeps nothing there, it writes it before each use of its own, of which there are none here.)
+__device__ __forceinline__ void load_to_lds(const void *src, const u32x4 *dst) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) u32x4 *)dst);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src));
+}
+
+// Where a lane reads its operands in a tile: u ^ x for units u that differ by
+// constants is a constant away from one of a few places, so those are formed once
+// and every read has its distance in the instruction.
+template <class P> struct TileReads {
+    // steps of the rows' units (two bits of a unit choose the lane group, bf16), of the columns'
+    static constexpr bool BF = P::V == 8;
+    static constexpr int RB = BF ? (P::XM + 1) / 4 : (P::XM + 1) / 8, CB = BF ? (P::XM + 1) / 2 : (P::XM + 1) / 4;
+    int row[RB][BF ? 1 : 2], col[CB][BF ? 1 : 4]; // bytes
+    __device__ __forceinline__ void init(int lane) {
+        const int r = lane & 15, g = lane >> 4, x = r & P::XM;
+#pragma unroll
+        for (int k = 0; k < RB; ++k)
+#pragma unroll
+            for (int h = 0; h < (BF ? 1 : 2); ++h)
+                row[k][h] = 16 * (r * P::RU + ((BF ? 4 * k + g : 8 * k + 2 * g + h) ^ x));
+#pragma unroll
+        for (int v = 0; v < CB; ++v)
+#pragma unroll
+            for (int e = 0; e < (BF ? 1 : 4); ++e) {
+                const int j = BF ? 4 * g + (r >> 2) : 4 * g + e, y = j & P::XM;
+                const int u = BF ? 2 * v + (r >> 1 & 1) : 4 * v + (r >> 2);
+                col[v][e] = 16 * (j * P::RU + (u ^ y)) + (BF ? 8 * (r & 1) : 4 * (r & 3));
+            }
+    }
+    // eight values of row j0 + lane % 16 (j0 a multiple of 16) in step k of 32 columns
+    __device__ __forceinline__ Frag<BF> rows(const u32x4 *T, int j0, int k) const {
+        const char *p = (const char *)(T + j0 * P::RU + k / RB * RB * (BF ? 4 : 8));
+        if constexpr (BF) return {*reinterpret_cast<const bf16x8 *>(p + row[k % RB][0])};
+        else return {*reinterpret_cast<const f32x4 *>(p + row[k % RB][0]), *reinterpret_cast<const f32x4 *>(p + row[k % RB][1])};
+    }
+    // operand column 16 v + lane % 16 over the 32 rows from j0, in the K order of two accumulator tiles (as col8)
+    __device__ __forceinline__ Frag<BF> cols(const u32x4 *T, int j0, int v) const {
+        const char *p = (const char *)(T + j0 * P::RU + v / CB * CB * (BF ? 2 : 4));
+        if constexpr (BF) {
+            auto half = [&](int j) {
+                return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(p + j * P::RU * 16 + col[v % CB][0]));
+            };
+            return {join8(half(0), half(16))};
+        } else {
+            Frag<false> f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                f.lo[e] = *reinterpret_cast<const float *>(p + col[v % CB][e]);
+                f.hi[e] = *reinterpret_cast<const float *>(p + 16 * P::RU * 16 + col[v % CB][e]);
+            }
+            return f;
+        }
+    }
+};
+
 // Tiles [t0, t1) of group g's prefix for the queries row0 .. of its `rows`; the sums go to part `slot`.
-template <bool BF, int DLP, int KS, int QT, class S>
+template <bool BF, int DLP, int KS, int QT>
 __device__ __forceinline__ void prefix_piece(const PrefixArgs a, int g, int lo, int rows, int row0, int t0, int t1,
-                                             int slot, S *T0, float *bias0) {
+                                             int slot, u32x4 *T0, float *bias0) {
     using P = PrefixShape<BF, DLP, KS, QT>;
+    using S = typename P::S;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15,
               gr = lane >> 4;
-    const int d = a.dl + a.dr, ng = d / P::V, rp = P::NT / ng, n = prefix_rows(a, g);
+    const int d = a.dl + a.dr, n = prefix_rows(a, g);
     const int *tb = a.table + (size_t)g * a.cols;
     // the table entry and the cache row of tile row `lane`, requested two tiles and known one tile ahead
     int entry = -1, row = -1;
@@ -117,29 +185,28 @@ __device__ __forceinline__ void prefix_piece(const PrefixArgs a, int g, int lo, 
                   ? entry * a.page + (int)((unsigned)pos % (unsigned)a.page)
                   : -1;
     };
-    // a thread loads one 16-byte column of every rp-th row of a tile
-    const int j0 = tid < rp * ng ? tid / ng : P::KT, c0 = (tid % ng) * P::V;
-    u32x4 reg[P::NIT];
-    auto fetch = [&] {
+    // A tile goes from memory to LDS without passing registers: a wave's load
+    // takes 64 units that follow each other in LDS, each lane from where its unit stands in
+    // the cache (rows that are none, and columns past d: from the zeros).
+    auto fetch = [&](int buf) {
+        int ln = lane;
+        asm volatile("" : "+v"(ln)); // (formed anew for each tile: kept, these places would take thirty registers)
 #pragma unroll
-        for (int m = 0; m < P::NIT; ++m) {
-            const int j = j0 + m * rp, p = __shfl(row, j & 63, 64);
-            const S *src = (const S *)a.cache + (size_t)(unsigned)p * (unsigned)d + c0;
-            reg[m] = load16(j < P::KT && p >= 0 ? src : (const S *)&mla_zeros);
-        }
-    };
-    auto stash = [&](int buf) {
-        S *T = T0 + buf * P::TILE;
-#pragma unroll
-        for (int m = 0; m < P::NIT; ++m) {
-            const int j = j0 + m * rp;
-            if (j < P::KT) *reinterpret_cast<u32x4 *>(T + j * P::LD + c0) = reg[m];
+        for (int i = 0; i < P::NL; ++i) {
+            // where unit 64 i + lane of the wave's rows is: row jj of them, place c
+            const int jj = (64 * i + ln) / P::RU, c = (64 * i + ln) % P::RU, j = wave * (P::KT / P::NW) + jj;
+            const int at = (c ^ (j & P::XM)) * P::V, p = __shfl(row, j, 64);
+            const S *src = (const S *)a.cache + (size_t)(unsigned)p * (unsigned)d + at;
+            load_to_lds(p >= 0 && at < d ? (const void *)src : (const void *)&mla_zeros,
+                        T0 + buf * P::TILE + (wave * P::NL + i) * 64);
         }
         if (wave == 0 && lane < P::KT) bias0[buf * P::KT + lane] = row >= 0 ? 0.f : -INFINITY;
     };
+    lds_barrier(); // (the previous piece's readers are done)
     ask(t0);
     place(t0);
-    fetch();
+    fetch(0);
+    if (t0 + 1 < t1) ask(t0 + 1);
     Frag<BF> Q[QT][KS];
     const S *qp = (const S *)a.q + ((size_t)lo * a.S * a.H) * d;
 #pragma unroll
@@ -151,10 +218,6 @@ __device__ __forceinline__ void prefix_piece(const PrefixArgs a, int g, int lo, 
             Q[t][k] = row8_if(i < rows && c < d, qp + (size_t)i * d + c);
         }
     }
-    lds_barrier(); // (the previous piece's readers are done)
-    // columns past d are never stored below: zero once
-    for (int w = (P::DP - d) / P::V, e = tid; e < 2 * P::KT * w; e += P::NT)
-        *reinterpret_cast<u32x4 *>(T0 + e / w * P::LD + d + e % w * P::V) = u32x4{0u, 0u, 0u, 0u};
     f32x4 O[QT][P::MV];
     float m[QT], l[QT];
 #pragma unroll
@@ -165,18 +228,18 @@ __device__ __forceinline__ void prefix_piece(const PrefixArgs a, int g, int lo, 
         for (int v = 0; v < P::MV; ++v) O[t][v] = zero4();
     }
     const float c2 = a.scale * (float)LOG2E;
-    stash(0);
-    if (t0 + 1 < t1) ask(t0 + 1);
+    TileReads<P> at;
+    at.init(lane);
+    wait_vmem(); // the first tile, and the queries
     lds_barrier();
-    wait_vmem(); // (the queries are there: else their first use in the loop waits for the tile in flight)
     for (int tile = t0; tile < t1; ++tile) {
         const int buf = (tile - t0) & 1;
-        const S *T = T0 + buf * P::TILE;
+        const u32x4 *T = T0 + buf * P::TILE;
         const float *bias = bias0 + buf * P::KT;
         if (tile + 1 < t1) {
             place(tile + 1);
+            fetch(buf ^ 1); // (its last readers passed the barrier before this tile)
             if (tile + 2 < t1) ask(tile + 2);
-            fetch();
         }
 #pragma unroll 1
         for (int u = 0; u < P::KT / 32; ++u) {
@@ -188,15 +251,36 @@ __device__ __forceinline__ void prefix_piece(const PrefixArgs a, int g, int lo, 
 #pragma unroll
                 for (int t = 0; t < QT; ++t) X[t][j] = bj;
             }
-            const S *kr = T + (32 * u + r) * P::LD + 8 * gr;
+            // Operands are requested a group ahead of the products that take them, and no further: left
+            // to itself the compiler requests all of them at once and spills what it holds.
+            constexpr int KG = BF && DLP <= 256 ? 2 : 1, NK = (KS + KG - 1) / KG, VG = 2 * KG, NV = P::MV / VG;
+            Frag<BF> kf[2][KG][2], vf[2][VG];
+            auto keys = [&](int i) {
 #pragma unroll
-            for (int k = 0; k < KS; ++k)
+                for (int k = 0; k < KG; ++k)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const Frag<BF> kf = row8(kr + 16 * j * P::LD + 32 * k);
+                    for (int j = 0; j < 2; ++j)
+                        if (i * KG + k < KS) kf[i & 1][k][j] = at.rows(T, 32 * u + 16 * j, i * KG + k);
+            };
+            auto values = [&](int i) {
 #pragma unroll
-                    for (int t = 0; t < QT; ++t) X[t][j] = mma8(kf, Q[t][k], X[t][j]);
-                }
+                for (int v = 0; v < VG; ++v) vf[i & 1][v] = at.cols(T, 32 * u, i * VG + v);
+            };
+            keys(0);
+#pragma unroll
+            for (int i = 0; i < NK; ++i) {
+                if (i + 1 < NK) keys(i + 1);
+                else values(0);
+                in_flight();
+#pragma unroll
+                for (int k = 0; k < KG; ++k)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int t = 0; t < QT; ++t)
+                            if (i * KG + k < KS) X[t][j] = mma8(kf[i & 1][k][j], Q[t][i * KG + k], X[t][j]);
+                in_flight();
+            }
             bool raise = false;
             float mx[QT];
 #pragma unroll
@@ -217,7 +301,10 @@ __device__ __forceinline__ void prefix_piece(const PrefixArgs a, int g, int lo, 
                     m[t] = mn;
                     l[t] *= f;
 #pragma unroll
-                    for (int v = 0; v < P::MV; ++v) O[t][v] *= f;
+                    for (int v = 0; v < P::MV; ++v) {
+                        O[t][v] *= f;
+                        if (v % 4 == 3) in_flight();
+                    }
                 }
             }
             Frag<BF> pf[QT];
@@ -232,14 +319,19 @@ __device__ __forceinline__ void prefix_piece(const PrefixArgs a, int g, int lo, 
                 l[t] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 pf[t] = acc8<BF>(X[t][0], X[t][1]);
             }
+            in_flight();
 #pragma unroll
-            for (int v = 0; v < P::MV; ++v) {
-                const Frag<BF> vf = col8(T, P::LD, 32 * u, 16 * v, lane);
+            for (int i = 0; i < NV; ++i) {
+                if (i + 1 < NV) values(i + 1);
+                in_flight();
 #pragma unroll
-                for (int t = 0; t < QT; ++t) O[t][v] = mma8(vf, pf[t], O[t][v]);
+                for (int v = 0; v < VG; ++v)
+#pragma unroll
+                    for (int t = 0; t < QT; ++t) O[t][i * VG + v] = mma8(vf[i & 1][v], pf[t], O[t][i * VG + v]);
+                in_flight();
             }
         }
-        if (tile + 1 < t1) stash(buf ^ 1); // (its last readers passed the barrier before this tile)
+        wait_vmem(); // the next tile is in LDS
         lds_barrier();
     }
 #pragma unroll
@@ -247,23 +339,23 @@ __device__ __forceinline__ void prefix_piece(const PrefixArgs a, int g, int lo, 
         const int in = (wave * QT + t) * 16 + r;
         const float sum = sum4g(l[t]);
         if (row0 + in >= rows) continue;
-        const size_t at = (size_t)slot * P::QB + in;
+        const size_t to = (size_t)slot * P::QB + in;
 #pragma unroll
         for (int v = 0; v < P::MV; ++v) {
             const int c = 16 * v + 4 * gr;
-            if (c < a.dl) store4(a.part + at * a.dl + c, O[t][v]);
+            if (c < a.dl) store4(a.part + to * a.dl + c, O[t][v]);
         }
-        if (gr == 0) *reinterpret_cast<f32x2 *>(a.part_ml + at * 2) = f32x2{m[t], sum};
+        if (gr == 0) *reinterpret_cast<f32x2 *>(a.part_ml + to * 2) = f32x2{m[t], sum};
     }
 }
 
-// waves per SIMD that the registers of a wave allow
-template <bool BF> constexpr int prefix_waves(int dlp, int qt) { return dlp <= (BF && qt == 2 ? 256 : BF ? 384 : 128) ? 2 : 1; }
+// workgroups a CU holds, by registers and LDS
+__host__ __device__ constexpr int prefix_per_cu(bool bf, int dlp) { return bf ? dlp <= 256 ? 2 : 1 : dlp <= 128 ? 2 : 1; }
 
 template <bool BF, int DLP, int KS, int QT>
-__global__ __launch_bounds__(256, prefix_waves<BF>(DLP, QT)) void mla_prefix_kernel(PrefixArgs a) {
+__global__ __launch_bounds__(64 * prefix_nw(BF, DLP), prefix_per_cu(BF, DLP) * prefix_nw(BF, DLP) / 4) void mla_prefix_kernel(PrefixArgs a) {
     using P = PrefixShape<BF, DLP, KS, QT>;
-    __shared__ __align__(16) typename P::S T[2 * P::TILE];
+    __shared__ u32x4 T[2 * P::TILE];
     __shared__ __align__(16) float bias[2 * P::KT];
     const int lane = threadIdx.x & 63, unit = blockIdx.x;
     const Line s = line_of(a, lane, P::KT);
@@ -289,7 +381,7 @@ __global__ __launch_bounds__(256, prefix_waves<BF>(DLP, QT)) void mla_prefix_ker
 }
 
 template <bool BF, int DLP, int KS, int QT> hipError_t prefix_run(const PrefixArgs &a, hipStream_t st) {
-    hipLaunchKernelGGL((mla_prefix_kernel<BF, DLP, KS, QT>), dim3((unsigned)a.units), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((mla_prefix_kernel<BF, DLP, KS, QT>), dim3((unsigned)a.units), dim3(64 * prefix_nw(BF, DLP)), 0, st, a);
     return hipGetLastError();
 }
 

@@ -4,7 +4,8 @@
 namespace gdn {
 
 template <int DLP, int KS> static hipError_t rows_bf16(const PrefixArgs &a, hipStream_t st) {
-    return a.qt == 2 ? prefix_run<true, DLP, KS, 2>(a, st) : prefix_run<true, DLP, KS, 1>(a, st);
+    if constexpr (DLP > 256) return prefix_run<true, DLP, KS, 1>(a, st);
+    else return a.qt == 2 ? prefix_run<true, DLP, KS, 2>(a, st) : prefix_run<true, DLP, KS, 1>(a, st);
 }
 // (a rotary part of 32 columns or less needs one step of the product less)
 template <int DLP> static hipError_t steps_bf16(const PrefixArgs &a, hipStream_t st) {
@@ -23,13 +24,14 @@ hipError_t launch_mla_prefix_bf16(const PrefixArgs &a, hipStream_t st) {
 
 long long mla_prefix_blocks(const PrefixArgs &a) {
     const long long rows = (long long)a.N * a.S * a.H;
-    return rows / (64 * a.qt) + (a.G < a.N ? a.G : a.N); // (every group may leave its last block unfilled)
+    return rows / a.qb + (a.G < a.N ? a.G : a.N); // (every group may leave its last block unfilled)
 }
 void mla_prefix_plan(PrefixArgs &a, bool bf16, int cus) {
     const int c = step_class(a.dl);
     // two blocks of queries a wave where a group has them: each tile read from LDS then serves twice as many products
-    a.qt = bf16 && (long long)a.N * a.S * a.H >= 96LL * (a.G < a.N ? a.G : a.N) ? 2 : 1;
-    a.units = cus * (bf16 ? prefix_waves<true>(c, a.qt) : prefix_waves<false>(c, a.qt));
+    a.qt = bf16 && c <= 256 && (long long)a.N * a.S * a.H >= 96LL * (a.G < a.N ? a.G : a.N) ? 2 : 1;
+    a.qb = 16 * prefix_nw(bf16, c) * a.qt;
+    a.units = cus * prefix_per_cu(bf16, c);
     // no more than there may be shares of four tiles
     const int kt = prefix_tile(bf16, c);
     const long long most = mla_prefix_blocks(a) * (((long long)a.cols * a.page + kt - 1) / kt);
@@ -82,7 +84,7 @@ template <bool BF> __global__ __launch_bounds__(256) void mla_shared_join_kernel
     }
     if (q >= mine || i0 >= rows) return;
     const size_t row = (size_t)nq * rows + i0;
-    const int qb = 64 * p.qt, in = (nq - first) * rows + i0, block = in / qb;
+    const int qb = p.qb, in = (nq - first) * rows + i0, block = in / qb;
     const long long pb = at0 + (long long)block * ptiles;
     const int u0 = ptiles ? (int)(pb / s.share) : 0, parts = ptiles ? (int)((pb + ptiles - 1) / s.share) - u0 + 1 : 0;
     const bool real = seq_rows(a, nq) - a.S + i0 / a.H >= 0; // (a token before position 0 is padding)

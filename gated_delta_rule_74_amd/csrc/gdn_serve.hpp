@@ -26,12 +26,12 @@ struct PrefixArgs {
     const int *table, *plens, *starts; // [G,cols], [G], [G+1]
     int N, S, H, dl, dr, pages, page, cols, G;
     float scale;
-    int qt;        // blocks of 16 queries a wave: a workgroup takes 64 * qt queries
+    int qt, qb;    // blocks of 16 queries a wave; queries of a workgroup
     int units;     // workgroups: shares the blocks' walks are cut into
-    float *part;   // workspace [units + blocks][64 * qt][dl]
-    float *part_ml; // workspace [units + blocks][64 * qt][2]
+    float *part;   // workspace [units + blocks][qb][dl]
+    float *part_ml; // workspace [units + blocks][qb][2]
 };
-void mla_prefix_plan(PrefixArgs &a, bool bf16, int cus); // sets qt and units
+void mla_prefix_plan(PrefixArgs &a, bool bf16, int cus); // sets qt, qb and units
 long long mla_prefix_blocks(const PrefixArgs &a);        // blocks of queries there may be
 hipError_t launch_mla_prefix_bf16(const PrefixArgs &a, hipStream_t st);
 hipError_t launch_mla_prefix_f32(const PrefixArgs &a, hipStream_t st);
