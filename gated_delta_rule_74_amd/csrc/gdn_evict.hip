@@ -1,28 +1,31 @@
 // Eviction of cached rows by weight: which rows a sequence keeps, and their
 // move to the front of its pages.
 //
-// choose, one workgroup per sequence: the weight of the lightest row kept is
-// found digit by digit, eleven, eleven and ten bits of the weights' ordered bit patterns at a
-// time, each from a histogram in LDS of the rows that agree in the digits
-// before (whole numbers: no order changes them). A last pass counts, for every
-// segment of the sequence, the rows above that weight and of exactly that weight, and
-// prefix sums of those tell every segment where its rows go and how many of
-// the equal ones come before it.
+// choose: the weight of the lightest row kept is found digit by digit, eleven,
+// eleven and ten bits of the weights' ordered bit patterns at a time, each from
+// a histogram of the rows that agree in the digits before (whole numbers: no
+// order changes them). Then every segment of the sequence counts its rows above that
+// weight and of exactly that weight, and prefix sums of those tell a segment
+// where its rows go and how many of the equal ones come before it. A sequence
+// of up to 32768 rows is one workgroup's, which holds the weights in registers
+// throughout; longer ones are cut into chunks, a launch to a digit, each
+// workgroup adding up its sequence's histograms of the digit before for itself (131072
+// rows: 270 us in one workgroup that read the weights again for every digit).
 //
-// move, one workgroup per segment: reads its kept rows into registers, and
-// writes them to the front once every segment that still holds rows in their new places
-// has been read. Bytes bound it: each kept row is read and written once, in place. A
-// segment goes by the ticket that its workgroup draws from its sequence's
-// counter and waits for segments of lower tickets alone. Those
-// workgroups are running, and set their flag before they wait for anything, so every wait ends.
+// move: a workgroup reads the kept rows of a segment into registers, and
+// writes them to the front once every segment that still holds rows in their
+// new places has been read. Bytes bound it: each kept row is read and written once, in
+// place. A segment goes by the ticket that its workgroup draws from its
+// sequence's counter and waits for segments of lower tickets alone. Those have
+// been drawn by workgroups that are running, and that set a segment's flag before they wait for
+// anything on its account, so every wait ends.
 #include "gdn_serve.hpp"
 
 namespace gdn {
 
-constexpr int ET = 1024; // threads of both kernels
-
-constexpr int EV = 18;   // 16-byte pieces a thread holds: a segment's rows
-static_assert(evict_segment(72) * 72 <= ET * EV && evict_segment(EVICT_ROW16) * EVICT_ROW16 <= ET * EV, "a segment fits");
+constexpr int ET = 1024, EM = EVICT_MOVE; // threads of the two kernels
+constexpr int EV = EVICT_HELD;
+static_assert(evict_segment(EVICT_ROW16) * EVICT_ROW16 <= EM * EV && evict_segment(1) <= EM, "a segment fits");
 
 // The order of the weights as unsigned numbers: NaN above all, -0 as 0; 0 is left for rows outside the pool.
 __device__ __forceinline__ uint32_t key_of(float w) {
@@ -41,101 +44,113 @@ __device__ __forceinline__ Lot lot_of(const EvictArgs &e, int i) {
     s.b = min(e.recent, s.k - s.a);
     return s;
 }
+// segments of a sequence that gives up rows
+__device__ __forceinline__ int move_segments(const EvictArgs &e, int i, int seg) {
+    const Lot s = lot_of(e, i);
+    return s.k == s.n ? 0 : (s.n + seg - 1) / seg;
+}
 // slot of a row, -1: its table entry lies outside the pool
-__device__ __forceinline__ int slot_of(const EvictArgs &e, const int *tb, int pos) {
-    const int entry = tb[(unsigned)pos / (unsigned)e.page];
+__device__ __forceinline__ int slot_in(const EvictArgs &e, int entry, int pos) {
     return (unsigned)entry < (unsigned)e.pages ? entry * e.page + (int)((unsigned)pos % (unsigned)e.page) : -1;
 }
-__device__ __forceinline__ uint32_t row_key(const EvictArgs &e, const int *tb, int pos) {
-    const int s = slot_of(e, tb, pos);
-    return s < 0 ? 0u : key_of(e.weights[s]);
-}
 
-__global__ __launch_bounds__(ET) void evict_choose_kernel(EvictArgs e) {
-    __shared__ int hist[2048];
-    __shared__ int waves[ET / 64][2];
-    __shared__ int pick[2]; // the digit, and the rows above it
-    const int n = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const Lot s = lot_of(e, n);
-    const int seg = evict_segment(e.row16), nseg = (s.n + seg - 1) / seg;
-    if (tid == 0) {
-        e.lens_out[n] = s.k;
-        e.ticket[n] = 0;
-    }
-    if (s.k == s.n) return; // (the move leaves such a sequence alone too)
-    int *done = e.done + (size_t)n * e.segs;
-    for (int i = tid; i < nseg; i += ET) done[i] = 0;
-    const int *tb = e.table + (size_t)n * e.cols;
-    const int lo = s.a, hi = s.n - s.b; // the rows to choose among
-    int want = s.k - s.a - s.b;         // of which so many stay
-    // the key of the lightest that stays: digit by digit, the largest with enough rows at or above it
-    uint32_t prefix = 0;
-    if (want > 0) {
-        for (int shift = 21; shift >= 0; shift = shift == 21 ? 10 : shift == 10 ? 0 : -1) {
-            const int bits = shift ? 11 : 10, above = shift + bits;
-            for (int i = tid; i < 2048; i += ET) hist[i] = 0;
-            __syncthreads();
-            for (int p = lo + tid; p < hi; p += ET) {
-                const uint32_t key = row_key(e, tb, p);
-                if (above == 32 || key >> above == prefix >> above) atomicAdd(&hist[key >> shift & ((1u << bits) - 1)], 1);
-            }
-            __syncthreads();
-            // suffix sums: thread t owns digits 2t and 2t + 1 from the top
-            const int top = (1 << bits) - 1, d0 = top - 2 * tid, h0 = d0 >= 0 ? hist[d0] : 0, h1 = d0 >= 1 ? hist[d0 - 1] : 0;
-            int x = h0 + h1;
+// The digits of a key, from the top.
+__device__ __forceinline__ int digit_shift(int i) { return i == 0 ? 21 : i == 1 ? 10 : 0; }
+__device__ __forceinline__ int digit_bits(int i) { return i == 2 ? 10 : 11; }
+
+// Keys of KR * ET rows from `base` on, every ET-th one to a thread (so a wave holds 64 rows that follow each other).
+template <int KR> struct Keys {
+    uint32_t k[KR];
+    __device__ __forceinline__ void load(const EvictArgs &e, const int *tb, int base, const Lot &s) {
+        constexpr int B = KR < 8 ? KR : 8; // requested together
 #pragma unroll
-            for (int o = 1; o < 64; o <<= 1) {
-                const int y = __shfl_up(x, o, 64);
-                if (lane >= o) x += y;
+        for (int u0 = 0; u0 < KR; u0 += B) {
+            if (base + u0 * ET >= s.n) break;
+            int at[B];
+            float w[B];
+#pragma unroll
+            for (int u = 0; u < B; ++u)
+                at[u] = tb[(unsigned)min(base + (u0 + u) * ET + (int)threadIdx.x, s.n - 1) / (unsigned)e.page];
+#pragma unroll
+            for (int u = 0; u < B; ++u) {
+                at[u] = slot_in(e, at[u], min(base + (u0 + u) * ET + (int)threadIdx.x, s.n - 1));
+                w[u] = e.weights[max(at[u], 0)];
             }
-            if (lane == 63) waves[wave][0] = x;
-            __syncthreads();
-            for (int w = 0; w < wave; ++w) x += waves[w][0];
-            const int before = x - h0 - h1; // rows above digit d0
-            if (d0 >= 0 && before < want && before + h0 >= want) {
-                pick[0] = d0;
-                pick[1] = before;
-            }
-            if (d0 >= 1 && before + h0 < want && x >= want) {
-                pick[0] = d0 - 1;
-                pick[1] = before + h0;
-            }
-            __syncthreads();
-            prefix |= (uint32_t)pick[0] << shift;
-            want -= pick[1];
-            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < B; ++u) k[u0 + u] = at[u] < 0 ? 0u : key_of(w[u]);
         }
-    } else {
-        prefix = 0xffffffffu; // none of the middle: equal ones (NaN) come to none
     }
-    const uint32_t bar = prefix;
-    const int spare = want;
-    if (tid == 0) {
-        e.bar[n] = bar;
-        e.spare[n] = spare;
+    // rows to choose among that agree with `prefix` in the digits before the i-th, by that digit
+    __device__ __forceinline__ void count(int *hist, int base, const Lot &s, uint32_t prefix, int i) const {
+        const int shift = digit_shift(i), above = shift + digit_bits(i);
+#pragma unroll
+        for (int u = 0; u < KR; ++u) {
+            if (base + u * ET >= s.n) break;
+            const int p = base + u * ET + (int)threadIdx.x;
+            if (p >= s.a && p < s.n - s.b && (i == 0 || k[u] >> above == prefix >> above))
+                atomicAdd(&hist[k[u] >> shift & ((1 << digit_bits(i)) - 1)], 1);
+        }
     }
-    // kept for sure, and of the bar's weight, per segment: a wave counts one after the other
-    int *kept = e.kept + (size_t)n * e.segs, *ties = e.ties + (size_t)n * e.segs;
-    for (int g = wave; g < nseg; g += ET / 64) {
-        int more = 0, same = 0;
-        for (int j = 0; j < seg; j += 64) {
-            const int p = g * seg + j + lane;
-            const bool in = p < s.n, sure = in && (p < lo || p >= hi), mid = in && !sure;
-            const uint32_t key = mid ? row_key(e, tb, p) : 0u;
-            more += __popcll(__ballot(sure || (mid && key > bar)));
-            same += __popcll(__ballot(mid && key == bar));
+    // rows that stay in any case, and those of the bar's weight, of every grain here
+    __device__ __forceinline__ void grains(const EvictArgs &e, int n, int base, const Lot &s, uint32_t bar, int want) const {
+        const int lane = threadIdx.x & 63, grain = evict_grain(e.row16);
+        int *kept = e.kept + (size_t)n * e.grains, *ties = e.ties + (size_t)n * e.grains;
+#pragma unroll
+        for (int u = 0; u < KR; ++u) {
+            const int p0 = base + u * ET + (int)(threadIdx.x & ~63u), p = p0 + lane;
+            if (base + u * ET >= s.n) break;
+            const bool in = p < s.n, mid = in && p >= s.a && p < s.n - s.b;
+            const uint64_t more = __ballot(in && (!mid || (want > 0 && k[u] > bar)));
+            const uint64_t same = __ballot(mid && want > 0 && k[u] == bar);
+            // (a wave holds one grain or two)
+            const int g = lane / grain;
+            const uint64_t mask = grain == 64 ? ~0ull : 0xffffffffull << (32 * g);
+            if (lane % grain == 0 && in) {
+                kept[p0 / grain + g] = __popcll(more & mask);
+                ties[p0 / grain + g] = __popcll(same & mask);
+            }
         }
-        if (lane == 0) {
-            kept[g] = more;
-            ties[g] = same;
-        }
+    }
+};
+
+// The largest digit with at least `want` rows at or above it, and `want` less the rows above it.
+__device__ __forceinline__ int find_digit(const int *hist, int i, int &want, int (*waves)[2], int *pick) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    // thread t owns digits 2t and 2t + 1 from the top
+    const int top = (1 << digit_bits(i)) - 1, d0 = top - 2 * tid, h0 = d0 >= 0 ? hist[d0] : 0, h1 = d0 >= 1 ? hist[d0 - 1] : 0;
+    int x = h0 + h1;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int y = __shfl_up(x, o, 64);
+        if (lane >= o) x += y;
+    }
+    if (lane == 63) waves[wave][0] = x;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) x += waves[w][0];
+    const int before = x - h0 - h1; // rows above digit d0
+    if (d0 >= 0 && before < want && before + h0 >= want) {
+        pick[0] = d0;
+        pick[1] = before;
+    }
+    if (d0 >= 1 && before + h0 < want && x >= want) {
+        pick[0] = d0 - 1;
+        pick[1] = before + h0;
     }
     __syncthreads();
-    // their prefix sums; of the equal ones the first `spare` stay
+    const int digit = pick[0];
+    want -= pick[1];
+    __syncthreads();
+    return digit;
+}
+
+// From the grains' counts to the rows kept and the equal ones before each; of those the first `spare` stay.
+__device__ __forceinline__ void sum_grains(const EvictArgs &e, int n, int num, int spare, int (*waves)[2]) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int *kept = e.kept + (size_t)n * e.grains, *ties = e.ties + (size_t)n * e.grains;
     int more0 = 0, same0 = 0;
-    for (int g0 = 0; g0 < nseg; g0 += ET) {
+    for (int g0 = 0; g0 < num; g0 += ET) {
         const int g = g0 + tid;
-        const int m0 = g < nseg ? kept[g] : 0, t0 = g < nseg ? ties[g] : 0;
+        const int m0 = g < num ? kept[g] : 0, t0 = g < num ? ties[g] : 0;
         int m = m0, t = t0;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
@@ -160,8 +175,8 @@ __global__ __launch_bounds__(ET) void evict_choose_kernel(EvictArgs e) {
             mall += waves[w][0];
             tall += waves[w][1];
         }
-        if (g < nseg) {
-            const int eq = same0 + t - t0; // equal ones before the segment
+        if (g < num) {
+            const int eq = same0 + t - t0; // equal ones before the grain
             ties[g] = eq;
             kept[g] = more0 + m - m0 + min(eq, spare);
         }
@@ -170,104 +185,210 @@ __global__ __launch_bounds__(ET) void evict_choose_kernel(EvictArgs e) {
     }
 }
 
-__global__ __launch_bounds__(ET) void evict_move_kernel(EvictArgs e) {
-    __shared__ int from[256], to[256];
-    __shared__ int counts[4][2], drawn, all;
-    const int n = blockIdx.x / e.segs, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const Lot s = lot_of(e, n);
-    if (s.k == s.n) return;
-    const int seg = evict_segment(e.row16), nseg = (s.n + seg - 1) / seg;
-    if ((int)(blockIdx.x % e.segs) >= nseg) return; // as many workgroups as the sequence has segments draw tickets
-    if (tid == 0) drawn = atomicAdd(&e.ticket[n], 1);
+__device__ __forceinline__ void clear(int *hist) {
+    for (int i = threadIdx.x; i < EVICT_BINS; i += ET) hist[i] = 0;
     __syncthreads();
-    const int g = drawn;
+}
+
+// One workgroup to a sequence.
+template <int KR> __global__ __launch_bounds__(ET) void evict_choose_kernel(EvictArgs e) {
+    __shared__ int hist[EVICT_BINS], waves[ET / 64][2], pick[2];
+    const int n = blockIdx.x, tid = threadIdx.x, seg = evict_segment(e.row16);
+    const Lot s = lot_of(e, n);
+    const int nseg = (s.n + seg - 1) / seg, grain = evict_grain(e.row16);
+    if (tid == 0) {
+        e.lens_out[n] = s.k;
+        e.ticket[n] = 0;
+    }
+    if (s.k == s.n) return; // (the move leaves such a sequence alone too)
+    int *done = e.done + (size_t)n * e.segs;
+    for (int i = tid; i < nseg; i += ET) done[i] = 0;
+    Keys<KR> keys;
+    keys.load(e, e.table + (size_t)n * e.cols, 0, s);
+    int want = s.k - s.a - s.b; // rows that stay of those to choose among
+    uint32_t bar = 0;
+    if (want > 0)
+        for (int i = 0; i < 3; ++i) {
+            clear(hist);
+            keys.count(hist, 0, s, bar, i);
+            __syncthreads();
+            bar |= (uint32_t)find_digit(hist, i, want, waves, pick) << digit_shift(i);
+        }
+    if (tid == 0) {
+        e.bar[n] = bar;
+        e.spare[n] = want;
+    }
+    keys.grains(e, n, 0, s, bar, want);
+    __syncthreads();
+    sum_grains(e, n, (s.n + grain - 1) / grain, want, waves);
+}
+
+// One of a sequence's chunks; pass 0 to 2 for the digits, 3 for the grains.
+__global__ __launch_bounds__(ET) void evict_chunk_kernel(EvictArgs e, int pass) {
+    constexpr int KR = EVICT_CHUNK / ET;
+    __shared__ int hist[EVICT_BINS], waves[ET / 64][2], pick[2];
+    const int n = blockIdx.x % e.N, chunk = blockIdx.x / e.N, base = chunk * EVICT_CHUNK, tid = threadIdx.x;
+    const int seg = evict_segment(e.row16);
+    const Lot s = lot_of(e, n);
+    if (pass == 0 && chunk == 0 && tid == 0) {
+        e.lens_out[n] = s.k;
+        e.ticket[n] = 0;
+        e.arrived[n] = 0;
+    }
+    if (s.k == s.n || base >= s.n) return;
+    const int chunks = (s.n + EVICT_CHUNK - 1) / EVICT_CHUNK, nseg = (s.n + seg - 1) / seg, grain = evict_grain(e.row16);
+    if (pass == 0) {
+        int *done = e.done + (size_t)n * e.segs;
+        for (int i = base / seg + tid; i < min(base / seg + EVICT_CHUNK / seg, nseg); i += ET) done[i] = 0;
+    }
+    Keys<KR> keys;
+    keys.load(e, e.table + (size_t)n * e.cols, base, s);
+    int want = s.k - s.a - s.b;
+    uint32_t bar = 0;
+    if (want > 0) {
+        // the digit before: all chunks' histograms added up
+        if (pass > 0) {
+            if (pass > 1) {
+                bar = e.state[(n * 3 + pass - 2) * 2];
+                want = (int)e.state[(n * 3 + pass - 2) * 2 + 1];
+            }
+            const int *h = e.hist + ((size_t)((pass - 1) & 1) * e.N + n) * e.chunks * EVICT_BINS;
+            for (int i = tid; i < EVICT_BINS; i += ET) {
+                int x = 0;
+#pragma unroll 8
+                for (int c = 0; c < chunks; ++c) x += h[(size_t)c * EVICT_BINS + i];
+                hist[i] = x;
+            }
+            __syncthreads();
+            bar |= (uint32_t)find_digit(hist, pass - 1, want, waves, pick) << digit_shift(pass - 1);
+            if (chunk == 0 && tid == 0) {
+                e.state[(n * 3 + pass - 1) * 2] = bar;
+                e.state[(n * 3 + pass - 1) * 2 + 1] = (uint32_t)want;
+            }
+        }
+        if (pass < 3) {
+            clear(hist);
+            keys.count(hist, base, s, bar, pass);
+            __syncthreads();
+            int *h = e.hist + (((size_t)(pass & 1) * e.N + n) * e.chunks + chunk) * EVICT_BINS;
+            for (int i = tid; i < EVICT_BINS; i += ET) h[i] = hist[i];
+        }
+    }
+    if (pass < 3) return;
+    if (chunk == 0 && tid == 0) {
+        e.bar[n] = bar;
+        e.spare[n] = want;
+    }
+    keys.grains(e, n, base, s, bar, want);
+    // the last of the sequence's workgroups adds up what all have counted
+    __syncthreads();
+    if (tid == 0) pick[0] = __hip_atomic_fetch_add(&e.arrived[n], 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (pick[0] != chunks - 1) return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    sum_grains(e, n, (s.n + grain - 1) / grain, want, waves);
+}
+
+// Segment g of sequence n, for all threads of the workgroup.
+__device__ __forceinline__ void move_segment(const EvictArgs &e, int n, int g, const Lot &s, int *from, int *to, int *counts) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int row16 = e.row16, seg = evict_segment(row16), grain = evict_grain(row16);
     const int *tb = e.table + (size_t)n * e.cols;
     int *done = e.done + (size_t)n * e.segs;
     const uint32_t bar = e.bar[n];
-    const int spare = e.spare[n], base = e.kept[(size_t)n * e.segs + g], ties = e.ties[(size_t)n * e.segs + g];
-    // which rows stay, and where they go
-    bool stay = false;
-    int slot = -1, rank = 0, same = 0;
-    float weight = 0.f;
-    if (tid < seg) {
-        const int p = g * seg + tid;
-        bool sure = false, tie = false;
-        if (p < s.n) {
-            slot = slot_of(e, tb, p);
-            weight = slot < 0 ? 0.f : e.weights[slot];
-            const uint32_t key = slot < 0 ? 0u : key_of(weight);
-            const bool mid = p >= s.a && p < s.n - s.b;
-            sure = !mid || key > bar;
-            tie = mid && key == bar;
-        }
-        const uint64_t eq = __ballot(tie), below = (1ull << lane) - 1;
-        same = __popcll(eq & below);
-        if (lane == 0) counts[wave][0] = __popcll(eq);
-        stay = sure;
-        rank = tie ? 1 : 0;
+    const int spare = e.spare[n];
+    // Which rows stay, and where they go: a thread has a row of the segment, a wave a grain (or two waves'
+    // worth of threads have none).
+    const int p = g * seg + tid;
+    const bool in = tid < seg && p < s.n;
+    const size_t at = (size_t)n * e.grains + (g * seg + (in ? wave * 64 : 0)) / grain;
+    const int first = e.kept[(size_t)n * e.grains + g * seg / grain], before = e.kept[at], ties = e.ties[at];
+    const int slot = in ? slot_in(e, tb[(unsigned)p / (unsigned)e.page], p) : -1;
+    const float weight = slot < 0 ? 0.f : e.weights[slot];
+    const uint32_t key = slot < 0 ? 0u : key_of(weight);
+    const bool mid = in && p >= s.a && p < s.n - s.b, tie = mid && spare > 0 && key == bar;
+    const uint64_t below = (1ull << lane) - 1, eq = __ballot(tie);
+    const bool stay = in && (!mid || (spare > 0 && key > bar) || (tie && ties + __popcll(eq & below) < spare));
+    const uint64_t st = __ballot(stay);
+    const int rank = before - first + __popcll(st & below); // among the segment's
+    int dst = -1;
+    if (stay) {
+        dst = slot_in(e, tb[(unsigned)(first + rank) / (unsigned)e.page], first + rank);
+        from[rank] = slot;
+        to[rank] = dst;
     }
+    if (lane == 0) counts[wave] = __popcll(st);
     __syncthreads();
-    if (tid < seg) {
-        for (int w = 0; w < wave; ++w) same += counts[w][0];
-        if (rank && ties + same < spare) stay = true;
-        const uint64_t st = __ballot(stay), below = (1ull << lane) - 1;
-        rank = __popcll(st & below);
-        if (lane == 0) counts[wave][1] = __popcll(st);
-    }
-    __syncthreads();
-    if (tid < seg) {
-        for (int w = 0; w < wave; ++w) rank += counts[w][1];
-        if (stay) {
-            from[rank] = slot;
-            to[rank] = slot_of(e, tb, base + rank);
-        }
-        if (tid == seg - 1) all = rank + (stay ? 1 : 0);
-    }
-    __syncthreads();
-    const int count = all, row16 = e.row16, pieces = count * row16;
+    const int count = (counts[0] + counts[1]) + (counts[2] + counts[3]), pieces = count * row16;
     // the rows, into registers (a segment whose rows all stay where they are has nothing to read)
-    const bool moves = count > 0 && base < g * seg + min(seg, s.n - g * seg) - count;
+    const bool moves = count > 0 && first < g * seg + min(seg, s.n - g * seg) - count;
     u32x4 x[EV];
     u32x4 *pool = (u32x4 *)e.cache;
     if (moves) {
 #pragma unroll
         for (int v = 0; v < EV; ++v) {
-            if (v * ET >= pieces) continue;
-            const int i = min(tid + v * ET, pieces - 1), row = (unsigned)i / (unsigned)row16;
-            const int src = from[row];
+            if (v * EM >= pieces) continue;
+            const int i = min(tid + v * EM, pieces - 1), row = (unsigned)i / (unsigned)row16, src = from[row];
             x[v] = load16(src < 0 ? (const void *)&mla_zeros
                                   : (const void *)(pool + (size_t)(unsigned)src * row16 + (i - row * row16)));
         }
     }
-    // all of it is here before the flag says so
+    // All of it is here before the flag says so. (What the flag orders are these reads, done by now, and others'
+    // writes: it has nothing to publish, so it needs no release, which would write back the L2.)
     wait_vmem();
     __syncthreads();
-    if (tid == 0) __hip_atomic_store(&done[g], 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_AGENT);
+    if (tid == 0) __hip_atomic_store(&done[g], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (!moves) return;
-    // the rows' new places hold rows of at most two or three segments before this one
+    // the rows' new places hold rows of at most two segments before this one
     if (tid == 0) {
-        const int g0 = base / seg, g1 = min((base + count - 1) / seg, g - 1);
+        const int g0 = first / seg, g1 = min((first + count - 1) / seg, g - 1);
         for (int i = g0; i <= g1; ++i)
-            while (!__hip_atomic_load(&done[i], __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_AGENT)) __builtin_amdgcn_s_sleep(2);
+            while (!__hip_atomic_load(&done[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) __builtin_amdgcn_s_sleep(2);
     }
     __syncthreads();
 #pragma unroll
     for (int v = 0; v < EV; ++v) {
-        const int i = tid + v * ET, row = (unsigned)i / (unsigned)row16;
+        if (v * EM >= pieces) continue;
+        const int i = tid + v * EM, row = (unsigned)min(i, pieces - 1) / (unsigned)row16;
         if (i < pieces && from[row] >= 0 && to[row] >= 0) pool[(size_t)(unsigned)to[row] * row16 + (i - row * row16)] = x[v];
     }
-    if (stay && slot >= 0) {
-        const int dst = to[rank];
-        if (dst >= 0) e.weights[dst] = weight;
+    if (stay && slot >= 0 && dst >= 0) e.weights[dst] = weight;
+}
+
+__global__ __launch_bounds__(EM) void evict_move_kernel(EvictArgs e) {
+    __shared__ int from[EM], to[EM], counts[EM / 64], drawn;
+    const int tid = threadIdx.x, lane = tid & 63, seg = evict_segment(e.row16);
+    // as many tickets of a sequence are drawn as it has segments
+    auto parts = [&](int i) { return move_segments(e, i, seg); };
+    const Pieces pieces = Pieces::of(e.N, parts, lane);
+    for (int b = blockIdx.x; b < pieces.total; b += gridDim.x) {
+        int n, any;
+        pieces.find(parts, b, lane, n, any);
+        if (tid == 0) drawn = atomicAdd(&e.ticket[n], 1);
+        const Lot s = lot_of(e, n);
+        __syncthreads();
+        move_segment(e, n, __builtin_amdgcn_readfirstlane(drawn), s, from, to, counts);
+        __syncthreads(); // (drawn, from and to are read)
     }
 }
 
 hipError_t launch_evict_choose(const EvictArgs &a, hipStream_t st) {
-    hipLaunchKernelGGL(evict_choose_kernel, dim3(a.N), dim3(ET), 0, st, a);
-    return hipGetLastError();
+    if (a.chunks == 1) {
+        if ((long long)a.cols * a.page <= 8 * ET) hipLaunchKernelGGL(evict_choose_kernel<8>, dim3(a.N), dim3(ET), 0, st, a);
+        else hipLaunchKernelGGL(evict_choose_kernel<EVICT_ONE / ET>, dim3(a.N), dim3(ET), 0, st, a);
+        return hipGetLastError();
+    }
+    for (int pass = 0; pass < 4; ++pass) {
+        hipLaunchKernelGGL(evict_chunk_kernel, dim3((unsigned)((long long)a.N * a.chunks)), dim3(ET), 0, st, a, pass);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 hipError_t launch_evict_move(const EvictArgs &a, hipStream_t st) {
-    hipLaunchKernelGGL(evict_move_kernel, dim3((unsigned)((long long)a.N * a.segs)), dim3(ET), 0, st, a);
+    // as many workgroups as the chip holds (five to a CU); how many segments there are is known on the GPU alone
+    const long long most = (long long)a.N * a.segs, held = 5 * MLA_CUS;
+    hipLaunchKernelGGL(evict_move_kernel, dim3((unsigned)(most < held ? most : held)), dim3(EM), 0, st, a);
     return hipGetLastError();
 }
 

@@ -391,7 +391,7 @@ gdn_status_t gdn_mla_weights(const gdn_mla_step_shape_t *s, float decay, const v
     a.cols = s->max_pages;
     a.scale = s->scale;
     a.decay = decay;
-    if ((double)gdn::mla_weights_groups(a) * 256 >= THREADS) return fail(GDN_EINVAL, "too many rows for a launch");
+    if ((double)gdn::mla_weights_groups(a, s->dtype == GDN_BF16) * 256 >= THREADS) return fail(GDN_EINVAL, "too many rows for a launch");
     const Buf b[] = {{q, rows * a.d * e, "q", 16, false, true},
                      {cache, slots * a.d * e, "cache", 16, false, some},
                      {block_table, (size_t)s->N * s->max_pages * 4, "block_table", 4, false, true},

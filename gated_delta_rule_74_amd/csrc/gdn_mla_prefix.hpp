@@ -15,6 +15,7 @@
 // rows (mla_step_kernel's, at place share + sequence).
 #pragma once
 
+#include "gdn_lds_tile.hpp"
 #include "gdn_serve.hpp"
 
 namespace gdn {
@@ -26,13 +27,11 @@ constexpr float PREFIX_RAISE = 8.f; // lazy maximum, as in the forward over expa
 // eight waves share a tile (what one wave per SIMD would hold for 32 the compiler spills).
 __host__ __device__ constexpr int prefix_nw(bool bf, int dlp) { return bf && dlp > 256 ? 8 : 4; }
 __host__ __device__ constexpr int prefix_tile(bool bf, int dlp) { return bf && (dlp <= 128 || dlp > 256) ? 64 : 32; }
-// A tile in LDS: rows of RU 16-byte units, unit u of row j at place u ^ (j & XM) of
-// its row, so that what a read takes of eight (sixteen) rows at once lies in different banks without padding.
 template <bool BF, int DLP, int KS, int QT> struct PrefixShape {
     using S = typename Op<BF>::S;
-    static constexpr int NW = prefix_nw(BF, DLP), NT = 64 * NW, V = Op<BF>::VEC, MV = DLP / 16, QB = 16 * NW * QT,
-                         KT = prefix_tile(BF, DLP),
-                         RU = (32 * KS / V + 7) / 8 * 8, XM = RU % 16 ? 7 : 15, TILE = KT * RU, // (units)
+    using Tile = LdsTile<BF, KS>;
+    static constexpr int NW = prefix_nw(BF, DLP), NT = 64 * NW, V = Tile::V, RU = Tile::RU, XM = Tile::XM, MV = DLP / 16,
+                         QB = 16 * NW * QT, KT = prefix_tile(BF, DLP), TILE = KT * RU, // (units)
                          NL = TILE / NT; // loads of a thread
     static_assert(TILE % NT == 0 && KT % NW == 0, "every load moves 64 units of a wave's rows");
 };
@@ -104,66 +103,6 @@ __device__ __forceinline__ Line line_of(const PrefixArgs &a, int lane, int kt) {
     return s;
 }
 
-// Sixteen bytes of every lane from global memory to 64 units of LDS that follow each other
-// (dst, the same for all lanes). Counted as a vector memory load: a wait for
-// those and a barrier make it visible. Written by hand, since the compiler would
-// have every LDS read behind it wait for it, the other tile's as well. (m0: the compiler
-// keeps nothing there, it writes it before each use of its own, of which there are none here.)
-__device__ __forceinline__ void load_to_lds(const void *src, const u32x4 *dst) {
-    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) u32x4 *)dst);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src));
-}
-
-// Where a lane reads its operands in a tile: u ^ x for units u that differ by
-// constants is a constant away from one of a few places, so those are formed once
-// and every read has its distance in the instruction.
-template <class P> struct TileReads {
-    // steps of the rows' units (two bits of a unit choose the lane group, bf16), of the columns'
-    static constexpr bool BF = P::V == 8;
-    static constexpr int RB = BF ? (P::XM + 1) / 4 : (P::XM + 1) / 8, CB = BF ? (P::XM + 1) / 2 : (P::XM + 1) / 4;
-    int row[RB][BF ? 1 : 2], col[CB][BF ? 1 : 4]; // bytes
-    __device__ __forceinline__ void init(int lane) {
-        const int r = lane & 15, g = lane >> 4, x = r & P::XM;
-#pragma unroll
-        for (int k = 0; k < RB; ++k)
-#pragma unroll
-            for (int h = 0; h < (BF ? 1 : 2); ++h)
-                row[k][h] = 16 * (r * P::RU + ((BF ? 4 * k + g : 8 * k + 2 * g + h) ^ x));
-#pragma unroll
-        for (int v = 0; v < CB; ++v)
-#pragma unroll
-            for (int e = 0; e < (BF ? 1 : 4); ++e) {
-                const int j = BF ? 4 * g + (r >> 2) : 4 * g + e, y = j & P::XM;
-                const int u = BF ? 2 * v + (r >> 1 & 1) : 4 * v + (r >> 2);
-                col[v][e] = 16 * (j * P::RU + (u ^ y)) + (BF ? 8 * (r & 1) : 4 * (r & 3));
-            }
-    }
-    // eight values of row j0 + lane % 16 (j0 a multiple of 16) in step k of 32 columns
-    __device__ __forceinline__ Frag<BF> rows(const u32x4 *T, int j0, int k) const {
-        const char *p = (const char *)(T + j0 * P::RU + k / RB * RB * (BF ? 4 : 8));
-        if constexpr (BF) return {*reinterpret_cast<const bf16x8 *>(p + row[k % RB][0])};
-        else return {*reinterpret_cast<const f32x4 *>(p + row[k % RB][0]), *reinterpret_cast<const f32x4 *>(p + row[k % RB][1])};
-    }
-    // operand column 16 v + lane % 16 over the 32 rows from j0, in the K order of two accumulator tiles (as col8)
-    __device__ __forceinline__ Frag<BF> cols(const u32x4 *T, int j0, int v) const {
-        const char *p = (const char *)(T + j0 * P::RU + v / CB * CB * (BF ? 2 : 4));
-        if constexpr (BF) {
-            auto half = [&](int j) {
-                return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(p + j * P::RU * 16 + col[v % CB][0]));
-            };
-            return {join8(half(0), half(16))};
-        } else {
-            Frag<false> f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                f.lo[e] = *reinterpret_cast<const float *>(p + col[v % CB][e]);
-                f.hi[e] = *reinterpret_cast<const float *>(p + 16 * P::RU * 16 + col[v % CB][e]);
-            }
-            return f;
-        }
-    }
-};
-
 // Tiles [t0, t1) of group g's prefix for the queries row0 .. of its `rows`; the sums go to part `slot`.
 template <bool BF, int DLP, int KS, int QT>
 __device__ __forceinline__ void prefix_piece(const PrefixArgs a, int g, int lo, int rows, int row0, int t0, int t1,
@@ -228,7 +167,7 @@ __device__ __forceinline__ void prefix_piece(const PrefixArgs a, int g, int lo, 
         for (int v = 0; v < P::MV; ++v) O[t][v] = zero4();
     }
     const float c2 = a.scale * (float)LOG2E;
-    TileReads<P> at;
+    TileReads<typename P::Tile> at;
     at.init(lane);
     wait_vmem(); // the first tile, and the queries
     lds_barrier();

@@ -66,7 +66,7 @@ struct MlaWeightsArgs {
     int N, S, H, d, pages, page, cols;
     float scale, decay;
 };
-long long mla_weights_groups(const MlaWeightsArgs &a);
+long long mla_weights_groups(const MlaWeightsArgs &a, bool bf16);
 hipError_t launch_mla_weights(const MlaWeightsArgs &a, bool bf16, hipStream_t st);
 
 // Rows that an eviction keeps, and their move to the front.
@@ -78,15 +78,32 @@ struct EvictArgs {
     int N, cols, pages, page, row16; // row16: 16-byte pieces of a cache row
     int first, recent;
     // workspace, per sequence: ticket counter, threshold; per sequence and
-    // segment: kept rows before it, rows of the threshold's weight before it, done
+    // grain: kept rows before it, rows of the threshold's weight before it; per sequence and segment: done
     int *ticket, *kept, *ties, *done;
     uint32_t *bar; // key of the lightest row kept
     int *spare;    // how many rows of that key are kept
-    int segs;      // segments of a sequence
+    int segs, grains; // segments and grains of a sequence
+    // where several workgroups choose for a sequence (chunks > 1): their histograms, two passes' of them, what the
+    // digits found so far leave, and how many are done
+    int chunks;
+    int *hist;       // [2][N][chunks][EVICT_BINS]
+    uint32_t *state; // [N][3][2]: digits found, rows wanted among those that agree
+    int *arrived;    // [N]
 };
 constexpr int EVICT_ROW16 = 144; // widest row
 // Rows of a segment: what a workgroup of the move holds in registers.
-__host__ __device__ constexpr int evict_segment(int row16) { return row16 <= 72 ? 256 : 128; }
+constexpr int EVICT_MOVE = 256;    // threads of the move
+constexpr int EVICT_HELD = 18;     // 16-byte pieces that each of them holds
+__host__ __device__ constexpr int evict_segment(int row16) {
+    const int most = EVICT_MOVE * EVICT_HELD / row16;
+    return most >= 256 ? 256 : most >= 128 ? 128 : most >= 64 ? 64 : 32;
+}
+// Rows that are counted together: a segment's, or a part of them.
+__host__ __device__ constexpr int evict_grain(int row16) { return evict_segment(row16) < 64 ? evict_segment(row16) : 64; }
+constexpr int EVICT_CHUNK = 8192;  // rows of a workgroup of the choice, where several take a sequence
+constexpr long long EVICT_ONE = 32768; // longest sequence that one takes
+constexpr int EVICT_BINS = 2048;   // values of a digit
+inline int evict_chunks(long long rows) { return rows <= EVICT_ONE ? 1 : (int)((rows + EVICT_CHUNK - 1) / EVICT_CHUNK); }
 hipError_t launch_evict_choose(const EvictArgs &a, hipStream_t st);
 hipError_t launch_evict_move(const EvictArgs &a, hipStream_t st);
 
@@ -109,5 +126,54 @@ int verify_pieces(int V, bool bf16); // pieces of a row
 hipError_t launch_verify_sums(const VerifyArgs &a, bool bf16, hipStream_t st);
 hipError_t launch_verify_left(const VerifyArgs &a, bool bf16, hipStream_t st);
 hipError_t launch_verify_draw(const VerifyArgs &a, bool bf16, hipStream_t st);
+
+// ---------------------------------------------------------------- device code
+
+// Sequences of parts(n) >= 0 equal pieces each, end to end: which sequence
+// holds piece b (n), and which of its pieces that is; false: there is no such piece. So the
+// workgroups with work are the first ones, which spread over the XCDs whatever the
+// lengths are (with a grid of sequences times their longest, every eighth
+// workgroup an XCD: 12 sequences of up to 2000 rows, 32 queries of fp32, 57 us; so 33). Every wave finds out for itself.
+struct Pieces {
+    int N, per, before, mine; // sequences a lane adds up; pieces before its own, and of its own
+    int total;
+    template <class F> __device__ __forceinline__ static Pieces of(int N, F &&parts, int lane) {
+        Pieces s = {N, (N + 63) / 64, 0, 0, 0};
+        const int from = min(lane * s.per, N), to = min(from + s.per, N);
+        for (int i = from; i < to; ++i) s.mine += parts(i);
+        s.sum(lane);
+        return s;
+    }
+    __device__ __forceinline__ void sum(int lane) {
+        int x = mine;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int y = __shfl_up(x, o, 64);
+            if (lane >= o) x += y;
+        }
+        before = x - mine;
+        total = __builtin_amdgcn_readlane(x, 63);
+    }
+    // the sequence of piece b < total, and which of its pieces that is
+    template <class F> __device__ __forceinline__ void find(F &&parts, int b, int lane, int &n, int &piece) const {
+        int l = __builtin_ctzll(__ballot(before + mine > b)), first = l * per, many = min(per, N - first);
+        b -= __builtin_amdgcn_readlane(before, l);
+        while (many > 1) { // (a 64th of them at a time)
+            Pieces s = of(many, [&](int i) { return parts(first + i); }, lane);
+            l = __builtin_ctzll(__ballot(s.before + s.mine > b));
+            b -= __builtin_amdgcn_readlane(s.before, l);
+            first += l * s.per;
+            many = min(s.per, many - l * s.per);
+        }
+        n = first;
+        piece = b;
+    }
+};
+template <class F> __device__ __forceinline__ bool find_piece(int N, F &&parts, int b, int lane, int &n, int &piece) {
+    const Pieces s = Pieces::of(N, parts, lane);
+    if (b >= s.total) return false;
+    s.find(parts, b, lane, n, piece);
+    return true;
+}
 
 } // namespace gdn

@@ -39,23 +39,31 @@ gdn_status_t check_evict(int32_t N, int32_t max_pages, int32_t page_size, int32_
         return fail(GDN_EUNSUPPORTED, "row_bytes must be at most %d", 16 * gdn::EVICT_ROW16);
     if ((double)max_pages * page_size > LIMIT - AHEAD || (double)N * max_pages >= LIMIT)
         return fail(GDN_EINVAL, "table too large");
-    const int seg = gdn::evict_segment(row_bytes / 16);
-    // (a workgroup of 1024 threads for every segment there may be)
-    if ((double)N * (((double)max_pages * page_size + seg - 1) / seg + 1) * 1024 >= THREADS)
+    // (segments are counted in int32; one workgroup of 1024 threads for every chunk)
+    const double rows = (double)max_pages * page_size;
+    if (N * (rows / 32 + 1) >= LIMIT / 2 || N * (rows / gdn::EVICT_CHUNK + 1) * 1024 >= THREADS)
         return fail(GDN_EINVAL, "too many rows for a launch");
     return GDN_OK;
 }
 size_t carve_evict(gdn::EvictArgs &a, void *ws) {
     const int seg = gdn::evict_segment(a.row16);
     a.segs = (int)(((long long)a.cols * a.page + seg - 1) / seg);
-    const size_t n = a.N, all = n * a.segs;
+    const int grain = gdn::evict_grain(a.row16);
+    a.grains = (int)(((long long)a.cols * a.page + grain - 1) / grain);
+    const size_t n = a.N;
     Carve c{(char *)ws};
     a.ticket = c.take<int>(n);
     a.bar = c.take<uint32_t>(n);
     a.spare = c.take<int>(n);
-    a.kept = c.take<int>(all);
-    a.ties = c.take<int>(all);
-    a.done = c.take<int>(all);
+    a.kept = c.take<int>(n * a.grains);
+    a.ties = c.take<int>(n * a.grains);
+    a.done = c.take<int>(n * a.segs);
+    a.chunks = gdn::evict_chunks((long long)a.cols * a.page);
+    if (a.chunks > 1) {
+        a.hist = c.take<int>(2 * n * a.chunks * gdn::EVICT_BINS);
+        a.state = c.take<uint32_t>(n * 3 * 2);
+        a.arrived = c.take<int>(n);
+    }
     return c.used;
 }
 
@@ -164,7 +172,7 @@ gdn_status_t gdn_mla_evict(int32_t N, int32_t max_pages, int32_t pages, int32_t 
     if (!some) return ok();
     st = check_space("gdn_mla_evict", ws, ws_bytes, need);
     if (st != GDN_OK) return st;
-    gdn::EvictArgs a;
+    gdn::EvictArgs a = {};
     a.table = block_table;
     a.lens = lens;
     a.keep = keep;
