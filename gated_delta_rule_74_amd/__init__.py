@@ -442,7 +442,7 @@ class LaunchTimer:
     KINDS = ("fwd_prep", "fwd_chain", "bwd_chain", "bwd_local", "dA_reduce", "step", "fwd_scan", "bwd_scan",
              "mla_fwd", "mla_bwd_q", "mla_bwd_k", "mla_rope_sum", "mla_step", "mla_join", "norm_rope",
              "norm_rope_bwd", "norm_sum", "mla_write", "page_plan", "page_fill", "mla_prefix", "mla_weights",
-             "evict_choose", "evict_move", "page_trim", "verify_sums", "verify_left", "verify_draw", "step_commit")
+             "evict_choose", "evict_move", "page_trim", "verify_sums", "verify_decide", "verify_left", "verify_draw", "step_commit")
 
     def kinds(self):
         """Kernel name of every bracketed launch, in launch order."""

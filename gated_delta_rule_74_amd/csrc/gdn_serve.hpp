@@ -15,6 +15,7 @@ enum ServeKind {
     K_EVICT_MOVE,
     K_PAGE_TRIM,
     K_VERIFY_SUMS,
+    K_VERIFY_DECIDE,
     K_VERIFY_LEFT,
     K_VERIFY_DRAW,
     K_STEP_COMMIT
@@ -115,15 +116,17 @@ struct VerifyArgs {
     float *logprobs; // may be null
     int N, S, V, nch;
     // workspace: rows [N * (S + 1)] of the target, then [N * S] of the draft
-    double *sums; // [rows][nch] sums of a piece, relative to its largest logit
-    float *tops;  // [rows][nch]
+    double *sums; // [rows][nch] sums of a piece's exponentials, relative to
+    float *refs;  // [rows][nch] this logit
+    float *tops;  // [rows][nch] its largest logit
     int *best;    // [rows][nch] first place of the largest
     double *left; // [N][nch] sums of what a rejected draft leaves
     double *pick; // [N][PICK]: what was decided
 };
 constexpr int VERIFY_PICK = 8;
-int verify_pieces(int V, bool bf16); // pieces of a row
+int verify_pieces(int V); // pieces of a row
 hipError_t launch_verify_sums(const VerifyArgs &a, bool bf16, hipStream_t st);
+hipError_t launch_verify_decide(const VerifyArgs &a, bool bf16, hipStream_t st);
 hipError_t launch_verify_left(const VerifyArgs &a, bool bf16, hipStream_t st);
 hipError_t launch_verify_draw(const VerifyArgs &a, bool bf16, hipStream_t st);
 

@@ -70,9 +70,9 @@ size_t carve_evict(gdn::EvictArgs &a, void *ws) {
 gdn_status_t check_verify(int32_t N, int32_t S, int32_t V, int32_t dtype) {
     if (N < 0 || S < 0 || V < 1) return fail(GDN_EINVAL, "N, S must be >= 0 and V >= 1");
     if (dtype != GDN_F32 && dtype != GDN_BF16) return fail(GDN_EINVAL, "unknown dtype %d", dtype);
-    if ((double)N * ((double)S + 1) * V >= LIMIT || V > (1 << 30) || S > (1 << 30))
+    if ((double)N * ((double)S + 1) * V >= LIMIT || V > (1 << 26) || S > (1 << 30))
         return fail(GDN_EINVAL, "logits too large");
-    if ((double)N * (2.0 * S + 1) * gdn::verify_pieces(V, dtype == GDN_BF16) * 256 >= THREADS)
+    if ((double)N * (2.0 * S + 2) * (gdn::verify_pieces(V) + 4.0) * 64 >= THREADS)
         return fail(GDN_EINVAL, "too many rows for a launch");
     return GDN_OK;
 }
@@ -83,6 +83,7 @@ size_t carve_verify(gdn::VerifyArgs &a, void *ws) {
     a.left = c.take<double>((size_t)a.N * a.nch);
     a.pick = c.take<double>((size_t)a.N * gdn::VERIFY_PICK);
     a.tops = c.take<float>(rows * a.nch);
+    a.refs = c.take<float>(rows * a.nch);
     a.best = c.take<int>(rows * a.nch);
     return c.used;
 }
@@ -221,7 +222,7 @@ size_t gdn_draft_verify_workspace_size(int32_t N, int32_t S, int32_t V, int32_t 
     a.N = N;
     a.S = S;
     a.V = V;
-    a.nch = gdn::verify_pieces(V, dtype == GDN_BF16);
+    a.nch = gdn::verify_pieces(V);
     return carve_verify(a, nullptr);
 }
 
@@ -261,12 +262,14 @@ gdn_status_t gdn_draft_verify(int32_t N, int32_t S, int32_t V, int32_t dtype, co
     a.N = N;
     a.S = S;
     a.V = V;
-    a.nch = gdn::verify_pieces(V, dtype == GDN_BF16);
+    a.nch = gdn::verify_pieces(V);
     carve_verify(a, ws);
     const bool bf = dtype == GDN_BF16;
     hipStream_t strm = (hipStream_t)stream;
     hipError_t he = gdn::bracketed(gdn::K_VERIFY_SUMS, [&] { return gdn::launch_verify_sums(a, bf, strm); }, strm);
     if (he == hipSuccess)
+        he = gdn::bracketed(gdn::K_VERIFY_DECIDE, [&] { return gdn::launch_verify_decide(a, bf, strm); }, strm);
+    if (he == hipSuccess && S > 0) // (without drafts none is rejected)
         he = gdn::bracketed(gdn::K_VERIFY_LEFT, [&] { return gdn::launch_verify_left(a, bf, strm); }, strm);
     if (he == hipSuccess)
         he = gdn::bracketed(gdn::K_VERIFY_DRAW, [&] { return gdn::launch_verify_draw(a, bf, strm); }, strm);

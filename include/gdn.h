@@ -459,7 +459,7 @@ gdn_status_t gdn_page_trim(int32_t N, int32_t max_pages, int32_t n_pages, int32_
  * A target row without a distribution (a NaN, +inf, nothing above -inf)
  * accepts nothing and draws -1 (with logprob 0). A draft outside [0, V), or whose row of
  * draft_logits has no distribution, is not accepted and the token is drawn from p_i.
- * Sums run in fp64. N, S >= 0, V >= 1; each tensor below 2^31 elements; ws:
+ * Sums run in fp64. N, S >= 0, 1 <= V <= 2^26; each tensor below 2^31 elements; ws:
  * gdn_draft_verify_workspace_size() bytes, 256-byte aligned. */
 size_t gdn_draft_verify_workspace_size(int32_t N, int32_t S, int32_t V, int32_t dtype);
 gdn_status_t gdn_draft_verify(int32_t N, int32_t S, int32_t V, int32_t dtype, const void *logits, const int32_t *draft,
@@ -487,8 +487,8 @@ int32_t gdn_time_launches(void *const *events, int32_t n);
  * write, 18 page plan, 19 slots of a page plan, 20 attention against shared
  * prefixes, 21 attention weights of cached rows, 22 choice of the rows that an
  * eviction keeps, 23 their move, 24 pages given back, 25 sums of draft and
- * target distributions, 26 sums of what is left of a rejected draft's, 27 the
- * tokens drawn, 28 state after accepted tokens; -1 when i is out of range. A
+ * target distributions, 26 how many drafts are accepted, 27 sums of what is
+ * left of a rejected draft's, 28 the tokens drawn, 29 state after accepted tokens; -1 when i is out of range. A
  * forward call may launch its two kernels several times each, over
  * consecutive chunk ranges (prep of the next range runs on a second stream
  * while the serial pass works on the current one), and a serial pass run as a
