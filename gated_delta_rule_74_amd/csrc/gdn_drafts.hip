@@ -30,10 +30,7 @@ int verify_pieces(int V) { return (V + VPIECE - 1) / VPIECE; }
 // the polynomial that meets it at the Chebyshev points of that interval. Eight terms,
 // 2^-34, for the many logits of a row: a border of the running sum moves by what of that does
 // not average out, far less than tokens' borders lie apart. Ten, 2^-45, elsewhere.
-template <int TERMS> __device__ __forceinline__ double exp2_f64(double t) {
-    t = fmax(t, -1100.0);
-    const double big = 6755399441055744.0, k = t + big; // 1.5 * 2^52: the low bits hold the rounded t
-    const double f = t - (k - big);
+template <int TERMS> __device__ __forceinline__ double exp2_part(double f) {
     double p;
     if constexpr (TERMS == 8) {
         p = 1.5303700711232526e-05;
@@ -56,7 +53,18 @@ template <int TERMS> __device__ __forceinline__ double exp2_f64(double t) {
         p = fma(p, f, 0.6931471805599462);
         p = fma(p, f, 1.0000000000000135);
     }
-    return __builtin_amdgcn_ldexp(p, __double2loint(k));
+    return p;
+}
+template <int TERMS> __device__ __forceinline__ double exp2_f64(double t) {
+    t = fmax(t, -1100.0);
+    const double big = 6755399441055744.0, k = t + big; // 1.5 * 2^52: the low bits hold the rounded t
+    return __builtin_amdgcn_ldexp(exp2_part<TERMS>(t - (k - big)), __double2loint(k));
+}
+// The same for -1000 <= t <= 1000 alone, where the factor 2^k is a sum of exponents.
+__device__ __forceinline__ double exp2_near(double t) {
+    const double big = 6755399441055744.0, k = t + big;
+    const double p = exp2_part<8>(t - (k - big));
+    return __hiloint2double(__double2hiint(p) + (__double2loint(k) << 20), __double2loint(p));
 }
 
 // A row's distribution: log2 p(v) = (z_v - ref) c - sum; sum NaN: it has none. (The difference is exact, however
@@ -152,7 +160,7 @@ template <bool BF> __global__ __launch_bounds__(VT) void verify_sums_kernel(Veri
 #pragma unroll
         for (int e = 0; e < G; ++e) {
             m = max_nan(m, z[e]);
-            sum += exp2_f64<8>((double)z[e] * c);
+            sum += exp2_near(fmax((double)z[e] * c, -1000.0));
         }
     });
 #pragma unroll
@@ -164,7 +172,7 @@ template <bool BF> __global__ __launch_bounds__(VT) void verify_sums_kernel(Veri
         if (m > -INFINITY && m < INFINITY)
             each_group<BF>(z0, a.V, base, end, lane, [&](int, const float(&z)[G]) {
 #pragma unroll
-                for (int e = 0; e < G; ++e) sum += exp2_f64<8>(((double)z[e] - (double)m) * c);
+                for (int e = 0; e < G; ++e) sum += exp2_near(fmax(((double)z[e] - (double)m) * c, -1000.0));
             });
     }
     sum = wave_sum_d(sum);
