@@ -32,10 +32,10 @@ void mla_prefix_plan(PrefixArgs &a, bool bf16, int cus) {
     a.qt = bf16 && c <= 256 && (long long)a.N * a.S * a.H >= 96LL * (a.G < a.N ? a.G : a.N) ? 2 : 1;
     a.qb = 16 * prefix_nw(bf16, c) * a.qt;
     a.units = cus * prefix_per_cu(bf16, c);
-    // no more than there may be shares of four tiles
+    // no more than there may be tiles
     const int kt = prefix_tile(bf16, c);
     const long long most = mla_prefix_blocks(a) * (((long long)a.cols * a.page + kt - 1) / kt);
-    if (most / 4 + 1 < a.units) a.units = (int)(most / 4 + 1);
+    if (most < a.units) a.units = (int)most;
 }
 
 // The parts of a query: its own rows' and its prefix's, added up relative to
