@@ -18,10 +18,13 @@ template <bool BF, int KS> struct LdsTile {
 // those and a barrier make it visible. Written by hand, since the compiler would
 // have every LDS read behind it wait for it, the other tile's as well. (m0: the compiler
 // keeps nothing there, it writes it before each use of its own, of which there are none here.)
-__device__ __forceinline__ void load_to_lds(const void *src, const u32x4 *dst) {
-    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) u32x4 *)dst);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src)
+__device__ __forceinline__ void load_to_lds(const void *src, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(dst), "v"(src)
                  : "memory");
+}
+// where a place in LDS is, as load_to_lds takes it
+__device__ __forceinline__ uint32_t lds_place(const u32x4 *p) {
+    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) u32x4 *)p);
 }
 
 // Where a lane reads its operands in a tile: u ^ x for units u that differ by

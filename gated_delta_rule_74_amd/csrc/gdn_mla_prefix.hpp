@@ -36,6 +36,8 @@ template <bool BF, int DLP, int KS, int QT> struct PrefixShape {
     static_assert(TILE % NT == 0 && KT % NW == 0, "every load moves 64 units of a wave's rows");
 };
 
+__device__ const u32x4 prefix_zeros[576 * 4 / 16] = {}; // a row of them
+
 // The groups, shared out: lane l holds groups l * per .. + per - 1.
 struct Line {
     int per, most;          // groups per lane; largest start before this lane's
@@ -108,39 +110,67 @@ __device__ __forceinline__ Line line_of(const PrefixArgs &a, int lane, int kt) {
 template <bool BF, int DLP, int KS, int QT>
 __device__ __forceinline__ void prefix_piece(const PrefixArgs a, int g, int lo, int rows, int row0, int t0, int t1,
                                              int slot, u32x4 *T0, float *bias0) {
+    // (the same for all lanes)
+    g = __builtin_amdgcn_readfirstlane(g);
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    rows = __builtin_amdgcn_readfirstlane(rows);
+    row0 = __builtin_amdgcn_readfirstlane(row0);
+    t0 = __builtin_amdgcn_readfirstlane(t0);
+    t1 = __builtin_amdgcn_readfirstlane(t1);
+    slot = __builtin_amdgcn_readfirstlane(slot);
     using P = PrefixShape<BF, DLP, KS, QT>;
     using S = typename P::S;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15,
               gr = lane >> 4;
     const int d = a.dl + a.dr, n = prefix_rows(a, g);
+    // Tile row `lane`: its column of the table and its place in that page, of the tile asked for next; the table entry
+    // is requested two tiles ahead, and where the row is known one ahead (none: among zeros).
     const int *tb = a.table + (size_t)g * a.cols;
-    // the table entry and the cache row of tile row `lane`, requested two tiles and known one tile ahead
-    int entry = -1, row = -1;
+    const int over = P::KT % a.page, across = P::KT / a.page;
+    int col = (t0 * P::KT + lane) / a.page, in = t0 * P::KT + lane - col * a.page, entry = -1;
+    uint64_t row = 0;
+    bool some = false;
     auto ask = [&](int tile) {
-        if (lane < P::KT) entry = tb[(unsigned)min(tile * P::KT + lane, n - 1) / (unsigned)a.page];
+        if (lane < P::KT && tile * P::KT + lane < n) entry = tb[col];
     };
     auto place = [&](int tile) {
-        const int pos = tile * P::KT + lane;
-        row = lane < P::KT && pos < n && (unsigned)entry < (unsigned)a.pages
-                  ? entry * a.page + (int)((unsigned)pos % (unsigned)a.page)
-                  : -1;
+        some = lane < P::KT && tile * P::KT + lane < n && (unsigned)entry < (unsigned)a.pages;
+        const S *at = (const S *)a.cache + (uint64_t)((unsigned)entry * (unsigned)a.page + (unsigned)in) * (unsigned)d;
+        row = some ? (uint64_t)at : (uint64_t)&prefix_zeros;
+        in += over;
+        col += across;
+        if (in >= a.page) {
+            in -= a.page;
+            ++col;
+        }
     };
     // A tile goes from memory to LDS without passing registers: a wave's load
-    // takes 64 units that follow each other in LDS, each lane from where its unit stands in
-    // the cache (rows that are none, and columns past d: from the zeros).
+    // takes 64 units that follow each other in LDS, each lane's from where it stands in its
+    // row. Units past the row's end are not loaded (the kernel cleared them). A lane's row and unit are formed anew for each
+    // tile where registers are short.
+    const uint32_t T1 = lds_place(T0 + wave * P::NL * 64);
+    const int row_units = d / P::V;
     auto fetch = [&](int buf) {
-        int ln = lane;
-        asm volatile("" : "+v"(ln)); // (formed anew for each tile: kept, these places would take thirty registers)
+        int jj = lane;
+        if constexpr (DLP > 128) asm volatile("" : "+v"(jj));
+        int u = jj % P::RU;
+        jj /= P::RU;
 #pragma unroll
         for (int i = 0; i < P::NL; ++i) {
-            // where unit 64 i + lane of the wave's rows is: row jj of them, place c
-            const int jj = (64 * i + ln) / P::RU, c = (64 * i + ln) % P::RU, j = wave * (P::KT / P::NW) + jj;
-            const int at = (c ^ (j & P::XM)) * P::V, p = __shfl(row, j, 64);
-            const S *src = (const S *)a.cache + (size_t)(unsigned)p * (unsigned)d + at;
-            load_to_lds(p >= 0 && at < d ? (const void *)src : (const void *)&mla_zeros,
-                        T0 + buf * P::TILE + (wave * P::NL + i) * 64);
+            const int j = wave * (P::KT / P::NW) + jj, at = u ^ (j & P::XM);
+            const uint32_t lo = __builtin_amdgcn_ds_bpermute(4 * j, (int)(uint32_t)row),
+                           hi = __builtin_amdgcn_ds_bpermute(4 * j, (int)(uint32_t)(row >> 32));
+            if (at < row_units)
+                load_to_lds((const char *)((uint64_t)hi << 32 | lo) + 16 * (unsigned)at, T1 + (buf * P::TILE + i * 64) * 16);
+            jj += 64 / P::RU;
+            u += 64 % P::RU;
+            if (u >= P::RU) {
+                u -= P::RU;
+                ++jj;
+            }
+            if (DLP > 128 && i % 2) in_flight(); // (all requested at once would spill)
         }
-        if (wave == 0 && lane < P::KT) bias0[buf * P::KT + lane] = row >= 0 ? 0.f : -INFINITY;
+        if (wave == 0 && lane < P::KT) bias0[buf * P::KT + lane] = some ? 0.f : -INFINITY;
     };
     lds_barrier(); // (the previous piece's readers are done)
     ask(t0);
@@ -276,10 +306,10 @@ __device__ __forceinline__ void prefix_piece(const PrefixArgs a, int g, int lo, 
     }
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
-        const int in = (wave * QT + t) * 16 + r;
+        const int i = (wave * QT + t) * 16 + r;
         const float sum = sum4g(l[t]);
-        if (row0 + in >= rows) continue;
-        const size_t to = (size_t)slot * P::QB + in;
+        if (row0 + i >= rows) continue;
+        const size_t to = (size_t)slot * P::QB + i;
 #pragma unroll
         for (int v = 0; v < P::MV; ++v) {
             const int c = 16 * v + 4 * gr;
@@ -298,6 +328,8 @@ __global__ __launch_bounds__(64 * prefix_nw(BF, DLP), prefix_per_cu(BF, DLP) * p
     __shared__ u32x4 T[2 * P::TILE];
     __shared__ __align__(16) float bias[2 * P::KT];
     const int lane = threadIdx.x & 63, unit = blockIdx.x;
+    if ((a.dl + a.dr) / P::V < P::RU) // units that no row fills
+        for (int i = threadIdx.x; i < 2 * P::TILE; i += P::NT) T[i] = u32x4{0u, 0u, 0u, 0u};
     const Line s = line_of(a, lane, P::KT);
     const long long from = unit * s.share, to = min(from + s.share, s.total);
     if (from >= to) return;

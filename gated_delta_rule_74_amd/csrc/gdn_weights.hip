@@ -184,7 +184,8 @@ template <bool BF, int KS> __global__ __launch_bounds__(WT, !BF && KS > 12 ? 1 :
         for (int j = 0; j < NL; ++j) {
             const int i = min(QS * s + (place[j] >> 16), rows - 1), c = place[j] & 0xffff;
             const S *src = qp + (size_t)(unsigned)i * (unsigned)d + c;
-            load_to_lds(c != 0xffff ? (const void *)src : (const void *)&mla_zeros, T[s & 1] + (wave * NL + j) * 64);
+            load_to_lds(c != 0xffff ? (const void *)src : (const void *)&mla_zeros,
+                        lds_place(T[s & 1] + (wave * NL + j) * 64));
         }
     };
     auto lse_of = [&](int i) { return i < rows ? a.lse[(size_t)n * rows + i] : -INFINITY; };
