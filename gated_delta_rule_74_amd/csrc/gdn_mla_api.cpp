@@ -142,6 +142,7 @@ gdn::PrefixArgs prefix_args(const gdn_mla_step_shape_t *s, int32_t G, int32_t pr
     p.pages = s->pages;
     p.page = s->page_size;
     p.cols = prefix_pages;
+    p.own_cols = s->max_pages;
     p.G = G;
     p.scale = s->scale;
     gdn::mla_prefix_plan(p, s->dtype == GDN_BF16, CUS);
@@ -162,7 +163,7 @@ struct SharedSpace {
     size_t all() const { return part + ml + prefix + prefix_ml; }
 };
 SharedSpace shared_space(const gdn::MlaStepArgs &a, const gdn::PrefixArgs &p) {
-    const size_t own = ((size_t)a.units + a.N) * a.S * a.H;
+    const size_t own = p.own ? ((size_t)p.units + (size_t)p.N * p.own_blocks) * p.own_qb : ((size_t)a.units + a.N) * a.S * a.H;
     const size_t front = ((size_t)p.units + (size_t)gdn::mla_prefix_blocks(p)) * p.qb;
     return {align_up(own * a.dl * 4), align_up(own * 8), align_up(front * p.dl * 4), align_up(front * 8)};
 }
@@ -354,6 +355,10 @@ gdn_status_t gdn_mla_step_shared(const gdn_mla_step_shape_t *s, int32_t G, int32
     a.lse = lse;
     a.part = (float *)at;
     a.part_ml = (float *)(at += z.part);
+    p.own_part = a.part;
+    p.own_part_ml = a.part_ml;
+    p.own_table = block_table;
+    p.lens = lens;
     p.part = (float *)(at += z.ml);
     p.part_ml = (float *)(at += z.prefix);
     p.q = q;
@@ -366,7 +371,7 @@ gdn_status_t gdn_mla_step_shared(const gdn_mla_step_shape_t *s, int32_t G, int32
     hipError_t he = gdn::bracketed(
         gdn::K_MLA_PREFIX, [&] { return bf ? gdn::launch_mla_prefix_bf16(p, strm) : gdn::launch_mla_prefix_f32(p, strm); },
         strm);
-    if (he == hipSuccess)
+    if (he == hipSuccess && !p.own)
         he = gdn::bracketed(gdn::K_MLA_STEP, [&] { return gdn::launch_mla_step_parts(a, bf, strm); }, strm);
     if (he == hipSuccess)
         he = gdn::bracketed(gdn::K_MLA_JOIN, [&] { return gdn::launch_mla_shared_join(a, p, bf, strm); }, strm);

@@ -38,35 +38,48 @@ template <bool BF, int DLP, int KS, int QT> struct PrefixShape {
 
 __device__ const u32x4 prefix_zeros[576 * 4 / 16] = {}; // a row of them
 
-// The groups, shared out: lane l holds groups l * per .. + per - 1.
+// The walks, shared out: lane l holds groups l * per .. + per - 1 of the G groups
+// and, behind them, the sequences' own rows (each a group of its own) where they are walked here.
 struct Line {
-    int per, most;          // groups per lane; largest start before this lane's
-    int blocks0, blocks;    // blocks of queries before this lane's, in them
-    long long tiles0, tiles; // their walks' tiles
-    long long total, share; // tiles of all walks, of a workgroup's share
+    int per, most;           // groups per lane; largest start before this lane's
+    int blocks0, blocks;     // blocks of queries before this lane's, in them
+    long long tiles0, tiles; // their walks' lengths
+    long long total, share;  // length of all walks, of a workgroup's share
 };
 struct Group {
-    int lo, hi;        // its sequences
-    int rows, blocks, tiles; // its queries, their blocks, the tiles of its prefix
+    int lo, hi;                    // its sequences
+    int rows, blocks, tiles, walk; // its queries, their blocks, the tiles of its rows, the length of a block's walk
 };
+// A walk's start (the first tile's wait, the queries) counts as so many tiles.
+constexpr int PREFIX_START = 2;
+
 __device__ __forceinline__ int prefix_rows(const PrefixArgs &a, int g) {
-    return (int)min((long long)max(a.plens[g], 0), (long long)a.cols * a.page);
+    return g < a.G ? (int)min((long long)max(a.plens[g], 0), (long long)a.cols * a.page)
+                   : (int)min((long long)max(a.lens[g - a.G], 0), (long long)a.own_cols * a.page);
 }
+__device__ __forceinline__ int groups_of(const PrefixArgs &a) { return a.G + (a.own ? a.N : 0); }
 __device__ __forceinline__ int start_of(const PrefixArgs &a, int g) { return min(max(a.starts[g], 0), a.N); }
 // most: the largest start before (starts that go back count as that)
 __device__ __forceinline__ Group group_of(const PrefixArgs &a, int g, int &most, int kt) {
     Group x;
-    x.lo = max(most, start_of(a, g));
-    x.hi = max(x.lo, start_of(a, g + 1));
-    most = x.lo;
+    if (g < a.G) {
+        x.lo = max(most, start_of(a, g));
+        x.hi = max(x.lo, start_of(a, g + 1));
+        most = x.lo;
+    } else {
+        x.lo = g - a.G;
+        x.hi = x.lo + 1;
+    }
     x.rows = (x.hi - x.lo) * a.S * a.H;
     x.blocks = (x.rows + a.qb - 1) / a.qb;
-    x.tiles = (prefix_rows(a, g) + kt - 1) / kt;
+    x.tiles = (int)(((long long)prefix_rows(a, g) + kt - 1) / kt);
+    x.walk = x.tiles ? x.tiles + PREFIX_START : 0;
     return x;
 }
 __device__ __forceinline__ Line line_of(const PrefixArgs &a, int lane, int kt) {
     Line s;
-    s.per = (a.G + 63) / 64;
+    const int all = groups_of(a);
+    s.per = (all + 63) / 64;
     int m = 0;
     for (int i = 0; i < s.per; ++i)
         if (lane * s.per + i < a.G) m = max(m, start_of(a, lane * s.per + i));
@@ -81,10 +94,10 @@ __device__ __forceinline__ Line line_of(const PrefixArgs &a, int lane, int kt) {
     s.tiles = 0;
     int most = s.most;
     for (int i = 0; i < s.per; ++i) {
-        if (lane * s.per + i >= a.G) break;
+        if (lane * s.per + i >= all) break;
         const Group x = group_of(a, lane * s.per + i, most, kt);
         s.blocks += x.blocks;
-        s.tiles += (long long)x.blocks * x.tiles;
+        s.tiles += (long long)x.blocks * x.walk;
     }
     int b = s.blocks;
     long long t = s.tiles;
@@ -106,7 +119,7 @@ __device__ __forceinline__ Line line_of(const PrefixArgs &a, int lane, int kt) {
     return s;
 }
 
-// Tiles [t0, t1) of group g's prefix for the queries row0 .. of its `rows`; the sums go to part `slot`.
+// Tiles [t0, t1) of group g's rows for the queries row0 .. of its `rows`; the sums go to part `slot`.
 template <bool BF, int DLP, int KS, int QT>
 __device__ __forceinline__ void prefix_piece(const PrefixArgs a, int g, int lo, int rows, int row0, int t0, int t1,
                                              int slot, u32x4 *T0, float *bias0) {
@@ -125,7 +138,8 @@ __device__ __forceinline__ void prefix_piece(const PrefixArgs a, int g, int lo, 
     const int d = a.dl + a.dr, n = prefix_rows(a, g);
     // Tile row `lane`: its column of the table and its place in that page, of the tile asked for next; the table entry
     // is requested two tiles ahead, and where the row is known one ahead (none: among zeros).
-    const int *tb = a.table + (size_t)g * a.cols;
+    const bool own = g >= a.G;
+    const int *tb = own ? a.own_table + (size_t)(g - a.G) * a.own_cols : a.table + (size_t)g * a.cols;
     const int over = P::KT % a.page, across = P::KT / a.page;
     int col = (t0 * P::KT + lane) / a.page, in = t0 * P::KT + lane - col * a.page, entry = -1;
     uint64_t row = 0;
@@ -188,6 +202,12 @@ __device__ __forceinline__ void prefix_piece(const PrefixArgs a, int g, int lo, 
             Q[t][k] = row8_if(i < rows && c < d, qp + (size_t)i * d + c);
         }
     }
+    // Own rows are seen up to the token's own: rows below `see`, which the tiles before the last tokens' need not ask.
+    int see[QT];
+#pragma unroll
+    for (int t = 0; t < QT; ++t) see[t] = own ? n - a.S + 1 + (row0 + (wave * QT + t) * 16 + r) / a.H : 2147483647;
+    const int all_see = own ? n - a.S + 1 : 2147483647;
+    const bool idle = row0 + wave * QT * 16 >= rows; // (a wave without queries only helps with the loads)
     f32x4 O[QT][P::MV];
     float m[QT], l[QT];
 #pragma unroll
@@ -212,7 +232,7 @@ __device__ __forceinline__ void prefix_piece(const PrefixArgs a, int g, int lo, 
             if (tile + 2 < t1) ask(tile + 2);
         }
 #pragma unroll 1
-        for (int u = 0; u < P::KT / 32; ++u) {
+        for (int u = idle ? P::KT / 32 : 0; u < P::KT / 32; ++u) {
             // absent rows: scores of -inf from the start (their keys are zero)
             f32x4 X[QT][2];
 #pragma unroll
@@ -250,6 +270,22 @@ __device__ __forceinline__ void prefix_piece(const PrefixArgs a, int g, int lo, 
                         for (int t = 0; t < QT; ++t)
                             if (i * KG + k < KS) X[t][j] = mma8(kf[i & 1][k][j], Q[t][i * KG + k], X[t][j]);
                 in_flight();
+            }
+            // What a token does not see is taken out behind the product, as its rows may hold anything. (The products'
+            // results are waited for by hand: the compiler, ROCm 7.2, leaves the wait out behind a conditional block.)
+#pragma unroll
+            for (int t = 0; t < QT; ++t)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) asm volatile("s_nop 15" : "+v"(X[t][j]));
+            const int from = tile * P::KT + 32 * u;
+            if (from + 32 > all_see) {
+#pragma unroll
+                for (int t = 0; t < QT; ++t)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (from + 16 * j + 4 * gr + e >= see[t]) X[t][j][e] = -INFINITY;
             }
             bool raise = false;
             float mx[QT];
@@ -309,13 +345,14 @@ __device__ __forceinline__ void prefix_piece(const PrefixArgs a, int g, int lo, 
         const int i = (wave * QT + t) * 16 + r;
         const float sum = sum4g(l[t]);
         if (row0 + i >= rows) continue;
-        const size_t to = (size_t)slot * P::QB + i;
+        const size_t to = (size_t)slot * (own ? a.own_qb : P::QB) + i;
+        float *part = own ? a.own_part : a.part, *part_ml = own ? a.own_part_ml : a.part_ml;
 #pragma unroll
         for (int v = 0; v < P::MV; ++v) {
             const int c = 16 * v + 4 * gr;
-            if (c < a.dl) store4(a.part + to * a.dl + c, O[t][v]);
+            if (c < a.dl) store4(part + to * a.dl + c, O[t][v]);
         }
-        if (gr == 0) *reinterpret_cast<f32x2 *>(a.part_ml + to * 2) = f32x2{m[t], sum};
+        if (gr == 0) *reinterpret_cast<f32x2 *>(part_ml + to * 2) = f32x2{m[t], sum};
     }
 }
 
@@ -339,15 +376,17 @@ __global__ __launch_bounds__(64 * prefix_nw(BF, DLP), prefix_per_cu(BF, DLP) * p
     long long begin = __shfl(s.tiles0, owner, 64);
     Group x = group_of(a, g, most, P::KT);
     for (long long at = from; at < to;) {
-        while (begin + (long long)x.blocks * x.tiles <= at) {
-            begin += (long long)x.blocks * x.tiles;
+        while (begin + (long long)x.blocks * x.walk <= at) {
+            begin += (long long)x.blocks * x.walk;
             block0 += x.blocks;
             x = group_of(a, ++g, most, P::KT);
         }
-        const int block = (int)((at - begin) / x.tiles);
-        const long long first = begin + (long long)block * x.tiles, stop = min(first + x.tiles, to);
-        prefix_piece<BF, DLP, KS, QT>(a, g, x.lo, x.rows, block * P::QB, (int)(at - first), (int)(stop - first),
-                                      unit + block0 + block, T, bias);
+        const int block = (int)((at - begin) / x.walk);
+        const long long first = begin + (long long)block * x.walk, stop = min(first + x.walk, to);
+        const int t0 = max((int)(at - first) - PREFIX_START, 0), t1 = (int)(stop - first) - PREFIX_START;
+        if (t0 < t1)
+            prefix_piece<BF, DLP, KS, QT>(a, g, x.lo, x.rows, block * P::QB, t0, t1,
+                                          unit + block + (g < a.G ? block0 : x.lo * a.own_blocks), T, bias);
         at = stop;
     }
 }

@@ -32,9 +32,19 @@ void mla_prefix_plan(PrefixArgs &a, bool bf16, int cus) {
     a.qt = bf16 && c <= 256 && (long long)a.N * a.S * a.H >= 96LL * (a.G < a.N ? a.G : a.N) ? 2 : 1;
     a.qb = 16 * prefix_nw(bf16, c) * a.qt;
     a.units = cus * prefix_per_cu(bf16, c);
-    // no more than there may be tiles
+    // the walks may hold so many tiles
     const int kt = prefix_tile(bf16, c);
-    const long long most = mla_prefix_blocks(a) * (((long long)a.cols * a.page + kt - 1) / kt);
+    const long long rows = (long long)a.S * a.H, cap = ((long long)a.cols * a.page + kt - 1) / kt + PREFIX_START;
+    const long long own_cap = ((long long)a.own_cols * a.page + kt - 1) / kt + PREFIX_START;
+    a.own_blocks = (int)((rows + a.qb - 1) / a.qb);
+    a.own_qb = (int)(rows < a.qb ? rows : a.qb);
+    long long most = mla_prefix_blocks(a) * cap;
+    // Own rows are walked here as well, which saves a launch and its starts (48 sequences of three drafts and 700 rows
+    // of 512 + 64: 105 us with that launch, OWN_GROUPS without; 256 sequences of 128 + 32: 79 and OWN_SERVE), though a sequence's
+    // queries leave waves idle: in bf16, where the rows' bytes take the time even so. In fp32 the products
+    // do: there if they fill the waves, or if the walks may not fill the chip (SMALL).
+    a.own = bf16 || 4 * rows >= 3LL * a.qb || most + a.N * a.own_blocks * own_cap <= a.units;
+    if (a.own) most += a.N * a.own_blocks * own_cap;
     if (most < a.units) a.units = (int)most;
 }
 
@@ -46,16 +56,38 @@ template <bool BF> __global__ __launch_bounds__(256) void mla_shared_join_kernel
     const int cols = a.dl / 4, tid = threadIdx.x, lane = tid & 63, rows = a.S * a.H;
     const int mine = 256 / cols, bpr = (rows + mine - 1) / mine, nq = blockIdx.x / bpr;
     const int q = tid / cols, c = tid % cols * 4, i0 = blockIdx.x % bpr * mine + q;
-    // own rows
-    const Share sh = share_out(a, lane);
-    const int lane_of = nq / sh.per, tiles = seq_tiles(a, nq);
-    int begin = __builtin_amdgcn_readlane(sh.before, lane_of);
-    for (int n = lane_of * sh.per; n < nq; ++n) begin += seq_tiles(a, n);
-    const int w0 = begin / sh.share, own = tiles ? (begin + tiles - 1) / sh.share - w0 + 1 : 0;
-    // the prefix: the group of this sequence, if any
-    long long at0 = 0; // tiles before the first block of the group
-    int block0 = 0, first = 0, ptiles = 0;
     const Line s = line_of(p, lane, kt);
+    // own rows
+    int own, own_slot, own_qb, own_in;
+    if (p.own) {
+        const int g = p.G + nq, l = g / s.per, block = i0 / p.qb;
+        long long at = __shfl(s.tiles0, l, 64);
+        int most = __shfl(s.most, l, 64);
+        Group x = group_of(p, l * s.per, most, kt);
+        for (int i = 1; i <= g - l * s.per; ++i) {
+            at += (long long)x.blocks * x.walk;
+            x = group_of(p, l * s.per + i, most, kt);
+        }
+        at += (long long)block * x.walk + PREFIX_START;
+        own_slot = (int)(at / s.share);
+        own = x.tiles ? (int)((at + x.tiles - 1) / s.share) - own_slot + 1 : 0;
+        own_slot += nq * p.own_blocks + block;
+        own_qb = p.own_qb;
+        own_in = i0 - block * p.qb;
+    } else {
+        const Share sh = share_out(a, lane);
+        const int lane_of = nq / sh.per, tiles = seq_tiles(a, nq);
+        int begin = __builtin_amdgcn_readlane(sh.before, lane_of);
+        for (int n = lane_of * sh.per; n < nq; ++n) begin += seq_tiles(a, n);
+        const int w0 = begin / sh.share;
+        own = tiles ? (begin + tiles - 1) / sh.share - w0 + 1 : 0;
+        own_slot = w0 + nq;
+        own_qb = rows;
+        own_in = i0;
+    }
+    // the prefix: the group of this sequence, if any
+    long long at0 = 0; // the walks before the first block of the group
+    int block0 = 0, first = 0, ptiles = 0, pwalk = 0;
     {
         int most = s.most, end = 0;
         for (int i = 0; i < s.per; ++i) {
@@ -74,18 +106,19 @@ template <bool BF> __global__ __launch_bounds__(256) void mla_shared_join_kernel
                     if (nq >= x.lo) {
                         first = x.lo;
                         ptiles = x.tiles;
+                        pwalk = x.walk;
                     }
                     break;
                 }
                 block0 += x.blocks;
-                at0 += (long long)x.blocks * x.tiles;
+                at0 += (long long)x.blocks * x.walk;
             }
         }
     }
     if (q >= mine || i0 >= rows) return;
     const size_t row = (size_t)nq * rows + i0;
     const int qb = p.qb, in = (nq - first) * rows + i0, block = in / qb;
-    const long long pb = at0 + (long long)block * ptiles;
+    const long long pb = at0 + (long long)block * pwalk + PREFIX_START;
     const int u0 = ptiles ? (int)(pb / s.share) : 0, parts = ptiles ? (int)((pb + ptiles - 1) / s.share) - u0 + 1 : 0;
     const bool real = seq_rows(a, nq) - a.S + i0 / a.H >= 0; // (a token before position 0 is padding)
     float m = -INFINITY, l = 0.f;
@@ -98,10 +131,10 @@ template <bool BF> __global__ __launch_bounds__(256) void mla_shared_join_kernel
 #pragma unroll
             for (int k = 0; k < JB; ++k) { // (past the last: that one again, with weight 0)
                 const int j = min(k0 + k, own + parts - 1);
-                const size_t at = j < own ? (size_t)(w0 + j + nq) * rows + i0
+                const size_t at = j < own ? (size_t)(own_slot + j) * own_qb + own_in
                                           : (size_t)(u0 + (j - own) + block0 + block) * qb + (in - block * qb);
-                st[k] = *reinterpret_cast<const f32x2 *>((j < own ? a.part_ml : p.part_ml) + at * 2);
-                y[k] = *reinterpret_cast<const f32x4 *>((j < own ? a.part : p.part) + at * a.dl + c);
+                st[k] = *reinterpret_cast<const f32x2 *>((j < own ? p.own_part_ml : p.part_ml) + at * 2);
+                y[k] = *reinterpret_cast<const f32x4 *>((j < own ? p.own_part : p.part) + at * a.dl + c);
             }
             float mn = m;
 #pragma unroll

@@ -31,6 +31,12 @@ struct PrefixArgs {
     int units;     // workgroups: shares the blocks' walks are cut into
     float *part;   // workspace [units + blocks][qb][dl]
     float *part_ml; // workspace [units + blocks][qb][2]
+    // 1: the sequences' own rows are walked here too, after the groups; else by mla_step_kernel
+    int own;
+    const int *own_table, *lens; // [N,own_cols], [N]
+    int own_cols, own_blocks, own_qb; // blocks of a sequence's queries, queries of its parts
+    float *own_part;   // workspace [units + N own_blocks][own_qb][dl]
+    float *own_part_ml; // workspace [units + N own_blocks][own_qb][2]
 };
 void mla_prefix_plan(PrefixArgs &a, bool bf16, int cus); // sets qt, qb and units
 long long mla_prefix_blocks(const PrefixArgs &a);        // blocks of queries there may be
