@@ -16,9 +16,10 @@
 // writes them to the front once every segment that still holds rows in their
 // new places has been read. Bytes bound it: each kept row is read and written once, in
 // place. A segment goes by the ticket that its workgroup draws from its
-// sequence's counter and waits for segments of lower tickets alone. Those have
-// been drawn by workgroups that are running, and that set a segment's flag before they wait for
-// anything on its account, so every wait ends.
+// sequence's counter and waits for segments of lower tickets alone. Those were
+// drawn before it, by workgroups that are running, which take their tickets in the order they drew them and
+// set a segment's flag before they wait for anything on its account: a wait
+// leads only to earlier draws, so every wait ends.
 #include "gdn_serve.hpp"
 
 namespace gdn {
@@ -289,86 +290,126 @@ __global__ __launch_bounds__(ET) void evict_chunk_kernel(EvictArgs e, int pass) 
     sum_grains(e, n, (s.n + grain - 1) / grain, want, waves);
 }
 
-// Segment g of sequence n, for all threads of the workgroup.
-__device__ __forceinline__ void move_segment(const EvictArgs &e, int n, int g, const Lot &s, int *from, int *to, int *counts) {
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int row16 = e.row16, seg = evict_segment(row16), grain = evict_grain(row16);
-    const int *tb = e.table + (size_t)n * e.cols;
-    int *done = e.done + (size_t)n * e.segs;
-    const uint32_t bar = e.bar[n];
-    const int spare = e.spare[n];
-    // Which rows stay, and where they go: a thread has a row of the segment, a wave a grain (or two waves'
-    // worth of threads have none).
-    const int p = g * seg + tid;
-    const bool in = tid < seg && p < s.n;
-    const size_t at = (size_t)n * e.grains + (g * seg + (in ? wave * 64 : 0)) / grain;
-    const int first = e.kept[(size_t)n * e.grains + g * seg / grain], before = e.kept[at], ties = e.ties[at];
-    const int slot = in ? slot_in(e, tb[(unsigned)p / (unsigned)e.page], p) : -1;
-    const float weight = slot < 0 ? 0.f : e.weights[slot];
-    const uint32_t key = slot < 0 ? 0u : key_of(weight);
-    const bool mid = in && p >= s.a && p < s.n - s.b, tie = mid && spare > 0 && key == bar;
-    const uint64_t below = (1ull << lane) - 1, eq = __ballot(tie);
-    const bool stay = in && (!mid || (spare > 0 && key > bar) || (tie && ties + __popcll(eq & below) < spare));
-    const uint64_t st = __ballot(stay);
-    const int rank = before - first + __popcll(st & below); // among the segment's
-    int dst = -1;
-    if (stay) {
-        dst = slot_in(e, tb[(unsigned)(first + rank) / (unsigned)e.page], first + rank);
-        from[rank] = slot;
-        to[rank] = dst;
+// A segment of a sequence, as a workgroup's threads see it: each has a row of it, a wave a grain (or two
+// waves' worth of threads have none).
+struct Segment {
+    int n, g, first, before, ties, spare, entry, slot;
+    uint32_t bar;
+    float weight;
+    Lot s;
+    // what the rows' choice hangs on, requested ...
+    __device__ __forceinline__ void ask(const EvictArgs &e, int sequence, int ticket) {
+        const int seg = evict_segment(e.row16), grain = evict_grain(e.row16), tid = threadIdx.x;
+        n = sequence;
+        g = ticket;
+        s = lot_of(e, n);
+        const size_t at = (size_t)n * e.grains;
+        first = e.kept[at + g * seg / grain];
+        const int mine = (g * seg + (row_in(e) ? (int)(tid & ~63u) : 0)) / grain;
+        before = e.kept[at + mine];
+        ties = e.ties[at + mine];
+        bar = e.bar[n];
+        spare = e.spare[n];
+        entry = row_in(e) ? e.table[(size_t)n * e.cols + (unsigned)row(e) / (unsigned)e.page] : -1;
     }
-    if (lane == 0) counts[wave] = __popcll(st);
-    __syncthreads();
-    const int count = (counts[0] + counts[1]) + (counts[2] + counts[3]), pieces = count * row16;
-    // the rows, into registers (a segment whose rows all stay where they are has nothing to read)
-    const bool moves = count > 0 && first < g * seg + min(seg, s.n - g * seg) - count;
-    u32x4 x[EV];
-    u32x4 *pool = (u32x4 *)e.cache;
-    if (moves) {
-#pragma unroll
-        for (int v = 0; v < EV; ++v) {
-            if (v * EM >= pieces) continue;
-            const int i = min(tid + v * EM, pieces - 1), row = (unsigned)i / (unsigned)row16, src = from[row];
-            x[v] = load16(src < 0 ? (const void *)&mla_zeros
-                                  : (const void *)(pool + (size_t)(unsigned)src * row16 + (i - row * row16)));
-        }
+    // ... and the row's weight
+    __device__ __forceinline__ void look(const EvictArgs &e) {
+        slot = slot_in(e, entry, row(e));
+        weight = slot < 0 ? 0.f : e.weights[slot];
     }
-    // All of it is here before the flag says so. (What the flag orders are these reads, done by now, and others'
-    // writes: it has nothing to publish, so it needs no release, which would write back the L2.)
-    wait_vmem();
-    __syncthreads();
-    if (tid == 0) __hip_atomic_store(&done[g], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (!moves) return;
-    // the rows' new places hold rows of at most two segments before this one
-    if (tid == 0) {
-        const int g0 = first / seg, g1 = min((first + count - 1) / seg, g - 1);
-        for (int i = g0; i <= g1; ++i)
-            while (!__hip_atomic_load(&done[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) __builtin_amdgcn_s_sleep(2);
+    __device__ __forceinline__ int row(const EvictArgs &e) const { return g * evict_segment(e.row16) + (int)threadIdx.x; }
+    __device__ __forceinline__ bool row_in(const EvictArgs &e) const {
+        return (int)threadIdx.x < evict_segment(e.row16) && row(e) < s.n;
     }
-    __syncthreads();
-#pragma unroll
-    for (int v = 0; v < EV; ++v) {
-        if (v * EM >= pieces) continue;
-        const int i = tid + v * EM, row = (unsigned)min(i, pieces - 1) / (unsigned)row16;
-        if (i < pieces && from[row] >= 0 && to[row] >= 0) pool[(size_t)(unsigned)to[row] * row16 + (i - row * row16)] = x[v];
-    }
-    if (stay && slot >= 0 && dst >= 0) e.weights[dst] = weight;
-}
+};
 
-__global__ __launch_bounds__(EM) void evict_move_kernel(EvictArgs e) {
-    __shared__ int from[EM], to[EM], counts[EM / 64], drawn;
-    const int tid = threadIdx.x, lane = tid & 63, seg = evict_segment(e.row16);
+__global__ __launch_bounds__(EM, 4) void evict_move_kernel(EvictArgs e) {
+    __shared__ int from[EM], to[EM], counts[EM / 64], drawn[2];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int row16 = e.row16, seg = evict_segment(row16);
     // as many tickets of a sequence are drawn as it has segments
     auto parts = [&](int i) { return move_segments(e, i, seg); };
-    const Pieces pieces = Pieces::of(e.N, parts, lane);
-    for (int b = blockIdx.x; b < pieces.total; b += gridDim.x) {
+    const Pieces all = Pieces::of(e.N, parts, lane);
+    int b = blockIdx.x;
+    if (b >= all.total) return;
+    // A segment's ticket is drawn, and what its rows' choice hangs on requested, while the one before it is moved.
+    Segment c, next;
+    {
         int n, any;
-        pieces.find(parts, b, lane, n, any);
-        if (tid == 0) drawn = atomicAdd(&e.ticket[n], 1);
-        const Lot s = lot_of(e, n);
+        all.find(parts, b, lane, n, any);
+        if (tid == 0) drawn[0] = atomicAdd(&e.ticket[n], 1);
         __syncthreads();
-        move_segment(e, n, __builtin_amdgcn_readfirstlane(drawn), s, from, to, counts);
-        __syncthreads(); // (drawn, from and to are read)
+        c.ask(e, n, __builtin_amdgcn_readfirstlane(drawn[0]));
+        c.look(e);
+    }
+    for (int turn = 1;; turn ^= 1) {
+        b += gridDim.x;
+        const bool more = b < all.total;
+        int n2 = 0, any;
+        if (more) {
+            all.find(parts, b, lane, n2, any);
+            if (tid == 0) drawn[turn] = atomicAdd(&e.ticket[n2], 1);
+        }
+        // which rows stay, and where they go
+        const Lot &s = c.s;
+        const int *tb = e.table + (size_t)c.n * e.cols;
+        int *done = e.done + (size_t)c.n * e.segs;
+        const int p = c.row(e), first = c.first, g = c.g;
+        const uint32_t key = c.slot < 0 ? 0u : key_of(c.weight);
+        const bool in = c.row_in(e), mid = in && p >= s.a && p < s.n - s.b, tie = mid && c.spare > 0 && key == c.bar;
+        const uint64_t below = (1ull << lane) - 1, eq = __ballot(tie);
+        const bool stay = in && (!mid || (c.spare > 0 && key > c.bar) || (tie && c.ties + __popcll(eq & below) < c.spare));
+        const uint64_t st = __ballot(stay);
+        const int rank = c.before - first + __popcll(st & below); // among the segment's
+        int dst = -1;
+        if (stay) {
+            dst = slot_in(e, tb[(unsigned)(first + rank) / (unsigned)e.page], first + rank);
+            from[rank] = c.slot;
+            to[rank] = dst;
+        }
+        if (lane == 0) counts[wave] = __popcll(st);
+        __syncthreads();
+        const int count = (counts[0] + counts[1]) + (counts[2] + counts[3]), pieces = count * row16;
+        // the rows, into registers (a segment whose rows all stay where they are has nothing to read)
+        const bool moves = count > 0 && first < g * seg + min(seg, s.n - g * seg) - count;
+        u32x4 x[EV];
+        u32x4 *pool = (u32x4 *)e.cache;
+        if (moves) {
+#pragma unroll
+            for (int v = 0; v < EV; ++v) {
+                if (v * EM >= pieces) continue;
+                const int i = min(tid + v * EM, pieces - 1), row = (unsigned)i / (unsigned)row16, src = from[row];
+                x[v] = load16(src < 0 ? (const void *)&mla_zeros
+                                      : (const void *)(pool + (size_t)(unsigned)src * row16 + (i - row * row16)));
+            }
+        }
+        if (more) next.ask(e, n2, __builtin_amdgcn_readfirstlane(drawn[turn]));
+        // All of it is here before the flag says so. (What the flag orders are these reads, done by now, and others'
+        // writes: it has nothing to publish, so it needs no release, which would write back the L2.)
+        wait_vmem();
+        __syncthreads();
+        if (tid == 0) __hip_atomic_store(&done[g], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (more) next.look(e);
+        if (moves) {
+            // the rows' new places hold rows of at most two segments before this one
+            if (tid == 0) {
+                const int g0 = first / seg, g1 = min((first + count - 1) / seg, g - 1);
+                for (int i = g0; i <= g1; ++i)
+                    while (!__hip_atomic_load(&done[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) __builtin_amdgcn_s_sleep(2);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int v = 0; v < EV; ++v) {
+                if (v * EM >= pieces) continue;
+                const int i = tid + v * EM, row = (unsigned)min(i, pieces - 1) / (unsigned)row16;
+                if (i < pieces && from[row] >= 0 && to[row] >= 0)
+                    pool[(size_t)(unsigned)to[row] * row16 + (i - row * row16)] = x[v];
+            }
+            if (stay && c.slot >= 0 && dst >= 0) e.weights[dst] = c.weight;
+        }
+        if (!more) break;
+        __syncthreads(); // (from and to are read)
+        c = next;
     }
 }
 
@@ -386,8 +427,8 @@ hipError_t launch_evict_choose(const EvictArgs &a, hipStream_t st) {
     return hipSuccess;
 }
 hipError_t launch_evict_move(const EvictArgs &a, hipStream_t st) {
-    // as many workgroups as the chip holds (five to a CU); how many segments there are is known on the GPU alone
-    const long long most = (long long)a.N * a.segs, held = 5 * MLA_CUS;
+    // as many workgroups as the chip holds (four to a CU); how many segments there are is known on the GPU alone
+    const long long most = (long long)a.N * a.segs, held = 4 * MLA_CUS;
     hipLaunchKernelGGL(evict_move_kernel, dim3((unsigned)(most < held ? most : held)), dim3(EM), 0, st, a);
     return hipGetLastError();
 }
