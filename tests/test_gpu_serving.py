@@ -103,6 +103,62 @@ def test_shared_prefix_of_many_queries(dtype, H, dl):
     within("lse", lse[pick], wl, tl)
 
 
+@pytest.mark.parametrize("dtype,dl", [("bf16", 128), ("bf16", 512), ("fp32", 64), ("fp32", 320)])
+def test_own_rows_of_many_queries(dtype, dl):
+    """More queries in a sequence than a block holds: its own rows are walked once for each block, the last one's mask
+    inside the later blocks."""
+    case = (3, 9, 16, dl, 16, 16, [9, 200, 70], [300], [0, 2])
+    say(f"shared, own blocks {dtype} {dl}")
+    a, f = shared_inputs(case, dtype, 9210)
+    o, lse = gdn.mla_step_shared(*a, scale=0.1)
+    want, to, wl, tl = bound.shared(*f, 0.1, dtype)
+    within("o", o, want, to)
+    within("lse", lse, wl, tl)
+
+
+@pytest.mark.parametrize("H", [1, 4, 16])
+def test_own_rows_apart_in_fp32(H):
+    """Too many own rows for one launch to take both, with queries that leave waves idle, and a prefix of its own."""
+    N = 40
+    case = (N, 1, H, 64, 0, 16, [1 + 23 * n for n in range(N)], [90, 200], [0, 20, N])
+    say(f"shared, own rows apart {H}")
+    a, f = shared_inputs(case, "fp32", 9220)
+    o, lse = gdn.mla_step_shared(*a, scale=0.1)
+    pick = [0, 1, 19, 20, 38, 39]
+    want, to, wl, tl = bound.shared(f[0][pick], f[1], f[2][pick], [case[6][n] for n in pick], 64, f[5], f[6], [0, 3, 6],
+                                    0.1, "fp32")
+    within("o", o[pick], want, to)
+    within("lse", lse[pick], wl, tl)
+
+
+def test_caches_past_32_bits():
+    """Pages whose elements lie past 2^32 of the cache: the same results, bit for bit, as from a small cache."""
+    page, dl, dr, N = 64, 512, 64, 3
+    d, far = dl + dr, 2 ** 32 // (64 * 576) + 40
+    case = (N, 2, 16, dl, dr, page, [130, 2, 64], [200], [0, 2])
+    a, _ = shared_inputs(case, "bf16", 9230)
+    small = a[1]
+    pages = small.shape[0]
+    big = torch.empty((far, page, d), dtype=torch.bfloat16, device="cuda")
+    move = torch.cat([torch.arange(pages // 2), far - pages + torch.arange(pages // 2, pages)]).int().cuda()
+    big[move.long()] = small
+    there = lambda t: torch.where(t >= 0, move[t.clamp(min=0).long()], t).contiguous()  # noqa: E731
+    assert big.numel() > 2 ** 32 and int(there(a[2]).max()) * page * d > 2 ** 32
+    o, lse = gdn.mla_step_shared(*a, scale=0.05)
+    bo, bl = gdn.mla_step_shared(a[0], big, there(a[2]), a[3], dl, there(a[5]), *a[6:], scale=0.05)
+    assert torch.equal(o, bo) and torch.equal(lse, bl)
+    ws, wb = torch.zeros((pages, page), device="cuda"), torch.zeros((far, page), device="cuda")
+    own_o, own_lse = gdn.mla_step(a[0], small, a[2], a[3], dl, scale=0.05)
+    gdn.mla_weights(a[0], small, a[2], a[3], own_lse, ws, scale=0.05)
+    gdn.mla_weights(a[0], big, there(a[2]), a[3], own_lse, wb, scale=0.05)
+    assert float(ws.sum()) > 0 and torch.equal(wb[move.long()], ws)
+    keep = ints([70, 1, 20])
+    out = gdn.mla_evict(ws, small, a[2], a[3], keep, first=2, recent=3)
+    far_out = gdn.mla_evict(wb, big, there(a[2]), a[3], keep, first=2, recent=3)
+    assert torch.equal(out, far_out) and torch.equal(wb[move.long()], ws)
+    assert torch.equal(big[move.long()].view(torch.int16), small.view(torch.int16))
+
+
 def test_shared_prefix_masks():
     """Table entries outside the pool mask their rows, of prefixes too; a prefix that leaves nothing; no groups."""
     case = (3, 1, 4, 32, 8, 4, [5, 2, 1], [9, 8], [0, 2, 3])
