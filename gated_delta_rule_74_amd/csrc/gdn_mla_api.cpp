@@ -159,13 +159,14 @@ gdn_status_t check_shared(const gdn_mla_step_shape_t *s, int32_t G, int32_t pref
     return GDN_OK;
 }
 struct SharedSpace {
-    size_t part, ml, prefix, prefix_ml;
-    size_t all() const { return part + ml + prefix + prefix_ml; }
+    size_t part, ml, prefix, prefix_ml, walks;
+    size_t all() const { return part + ml + prefix + prefix_ml + walks; }
 };
 SharedSpace shared_space(const gdn::MlaStepArgs &a, const gdn::PrefixArgs &p) {
     const size_t own = p.own ? ((size_t)p.units + (size_t)p.N * p.own_blocks) * p.own_qb : ((size_t)a.units + a.N) * a.S * a.H;
     const size_t front = ((size_t)p.units + (size_t)gdn::mla_prefix_blocks(p)) * p.qb;
-    return {align_up(own * a.dl * 4), align_up(own * 8), align_up(front * p.dl * 4), align_up(front * 8)};
+    return {align_up(own * a.dl * 4), align_up(own * 8), align_up(front * p.dl * 4), align_up(front * 8),
+            p.own ? align_up((size_t)p.N * 16) : 0};
 }
 
 constexpr uint32_t ROPE_FLAGS = GDN_ROPE_NORM | GDN_ROPE_INTERLEAVED;
@@ -361,6 +362,7 @@ gdn_status_t gdn_mla_step_shared(const gdn_mla_step_shape_t *s, int32_t G, int32
     p.lens = lens;
     p.part = (float *)(at += z.ml);
     p.part_ml = (float *)(at += z.prefix);
+    p.walks = (long long *)(at += z.prefix_ml);
     p.q = q;
     p.cache = cache;
     p.table = prefix_table;

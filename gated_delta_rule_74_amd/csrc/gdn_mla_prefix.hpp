@@ -38,48 +38,50 @@ template <bool BF, int DLP, int KS, int QT> struct PrefixShape {
 
 __device__ const u32x4 prefix_zeros[576 * 4 / 16] = {}; // a row of them
 
-// The walks, shared out: lane l holds groups l * per .. + per - 1 of the G groups
-// and, behind them, the sequences' own rows (each a group of its own) where they are walked here.
+// A walk's start (the first tile's wait, the queries) counts as so many tiles.
+constexpr int PREFIX_START = 2;
+
+// The groups' walks, end to end: lane l holds groups l * per .. + per - 1. Where the sequences' own
+// rows are walked here too, those walks follow, each sequence as a group of its own.
 struct Line {
     int per, most;           // groups per lane; largest start before this lane's
     int blocks0, blocks;     // blocks of queries before this lane's, in them
     long long tiles0, tiles; // their walks' lengths
-    long long total, share;  // length of all walks, of a workgroup's share
+    long long total;         // length of all groups' walks
 };
 struct Group {
     int lo, hi;                    // its sequences
     int rows, blocks, tiles, walk; // its queries, their blocks, the tiles of its rows, the length of a block's walk
 };
-// A walk's start (the first tile's wait, the queries) counts as so many tiles.
-constexpr int PREFIX_START = 2;
-
-__device__ __forceinline__ int prefix_rows(const PrefixArgs &a, int g) {
+__device__ __forceinline__ int prefix_rows(const PrefixArgs &a, int g) { // g >= G: own rows of sequence g - G
     return g < a.G ? (int)min((long long)max(a.plens[g], 0), (long long)a.cols * a.page)
                    : (int)min((long long)max(a.lens[g - a.G], 0), (long long)a.own_cols * a.page);
 }
-__device__ __forceinline__ int groups_of(const PrefixArgs &a) { return a.G + (a.own ? a.N : 0); }
+__device__ __forceinline__ int tiles_of(const PrefixArgs &a, int g, int kt) {
+    return (int)(((long long)prefix_rows(a, g) + kt - 1) / kt);
+}
+__device__ __forceinline__ int walk_of(int tiles) { return tiles ? tiles + PREFIX_START : 0; }
+// a workgroup's share (a tile at least: where the chip is not full, the longest walk is the call's time, and the
+// parts are few; two prefixes of 700 rows of 64 + 16 in fp32: 15 us with four tiles, 11 with two, 8 with one)
+__device__ __forceinline__ long long share_of(const PrefixArgs &a, long long total) {
+    return max((total + a.units - 1) / a.units, 1LL);
+}
 __device__ __forceinline__ int start_of(const PrefixArgs &a, int g) { return min(max(a.starts[g], 0), a.N); }
 // most: the largest start before (starts that go back count as that)
 __device__ __forceinline__ Group group_of(const PrefixArgs &a, int g, int &most, int kt) {
     Group x;
-    if (g < a.G) {
-        x.lo = max(most, start_of(a, g));
-        x.hi = max(x.lo, start_of(a, g + 1));
-        most = x.lo;
-    } else {
-        x.lo = g - a.G;
-        x.hi = x.lo + 1;
-    }
+    x.lo = max(most, start_of(a, g));
+    x.hi = max(x.lo, start_of(a, g + 1));
+    most = x.lo;
     x.rows = (x.hi - x.lo) * a.S * a.H;
     x.blocks = (x.rows + a.qb - 1) / a.qb;
-    x.tiles = (int)(((long long)prefix_rows(a, g) + kt - 1) / kt);
-    x.walk = x.tiles ? x.tiles + PREFIX_START : 0;
+    x.tiles = tiles_of(a, g, kt);
+    x.walk = walk_of(x.tiles);
     return x;
 }
 __device__ __forceinline__ Line line_of(const PrefixArgs &a, int lane, int kt) {
     Line s;
-    const int all = groups_of(a);
-    s.per = (all + 63) / 64;
+    s.per = (a.G + 63) / 64;
     int m = 0;
     for (int i = 0; i < s.per; ++i)
         if (lane * s.per + i < a.G) m = max(m, start_of(a, lane * s.per + i));
@@ -94,7 +96,7 @@ __device__ __forceinline__ Line line_of(const PrefixArgs &a, int lane, int kt) {
     s.tiles = 0;
     int most = s.most;
     for (int i = 0; i < s.per; ++i) {
-        if (lane * s.per + i >= all) break;
+        if (lane * s.per + i >= a.G) break;
         const Group x = group_of(a, lane * s.per + i, most, kt);
         s.blocks += x.blocks;
         s.tiles += (long long)x.blocks * x.walk;
@@ -113,9 +115,6 @@ __device__ __forceinline__ Line line_of(const PrefixArgs &a, int lane, int kt) {
     s.blocks0 = b - s.blocks;
     s.tiles0 = t - s.tiles;
     s.total = __shfl(t, 63, 64);
-    // (a tile at least: where the chip is not full, the longest walk is the call's time, and the parts are few; two
-    // prefixes of 700 rows of 64 + 16 in fp32: 15 us with four tiles, 11 with two, 8 with one)
-    s.share = max((s.total + a.units - 1) / a.units, 1LL);
     return s;
 }
 
@@ -123,14 +122,6 @@ __device__ __forceinline__ Line line_of(const PrefixArgs &a, int lane, int kt) {
 template <bool BF, int DLP, int KS, int QT>
 __device__ __forceinline__ void prefix_piece(const PrefixArgs a, int g, int lo, int rows, int row0, int t0, int t1,
                                              int slot, u32x4 *T0, float *bias0) {
-    // (the same for all lanes)
-    g = __builtin_amdgcn_readfirstlane(g);
-    lo = __builtin_amdgcn_readfirstlane(lo);
-    rows = __builtin_amdgcn_readfirstlane(rows);
-    row0 = __builtin_amdgcn_readfirstlane(row0);
-    t0 = __builtin_amdgcn_readfirstlane(t0);
-    t1 = __builtin_amdgcn_readfirstlane(t1);
-    slot = __builtin_amdgcn_readfirstlane(slot);
     using P = PrefixShape<BF, DLP, KS, QT>;
     using S = typename P::S;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15,
@@ -359,6 +350,12 @@ __device__ __forceinline__ void prefix_piece(const PrefixArgs a, int g, int lo, 
 // workgroups a CU holds, by registers and LDS
 __host__ __device__ constexpr int prefix_per_cu(bool bf, int dlp) { return bf ? dlp <= 256 ? 2 : 1 : dlp <= 128 ? 2 : 1; }
 
+// a value that is the same in all lanes, as one that needs no vector register
+__device__ __forceinline__ int one(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ long long one(long long x) {
+    return (long long)(((uint64_t)(uint32_t)one((int)(x >> 32)) << 32) | (uint32_t)one((int)x));
+}
+
 template <bool BF, int DLP, int KS, int QT>
 __global__ __launch_bounds__(64 * prefix_nw(BF, DLP), prefix_per_cu(BF, DLP) * prefix_nw(BF, DLP) / 4) void mla_prefix_kernel(PrefixArgs a) {
     using P = PrefixShape<BF, DLP, KS, QT>;
@@ -368,18 +365,46 @@ __global__ __launch_bounds__(64 * prefix_nw(BF, DLP), prefix_per_cu(BF, DLP) * p
     if ((a.dl + a.dr) / P::V < P::RU) // units that no row fills
         for (int i = threadIdx.x; i < 2 * P::TILE; i += P::NT) T[i] = u32x4{0u, 0u, 0u, 0u};
     const Line s = line_of(a, lane, P::KT);
-    const long long from = unit * s.share, to = min(from + s.share, s.total);
+    Pieces own = {};
+    auto walks = [&](int n) { return walk_of(tiles_of(a, a.G + n, P::KT)); };
+    if (a.own) own = Pieces::of(a.N, walks, lane);
+    const long long groups = one(s.total), all = groups + (long long)one(own.total) * a.own_blocks;
+    const long long share = one(share_of(a, all)), from = unit * share, to = min(from + share, all);
     if (from >= to) return;
-    // the group the share begins in
-    int owner = __builtin_ctzll(__ballot(s.tiles0 + s.tiles > from));
-    int g = owner * s.per, most = __shfl(s.most, owner, 64), block0 = __shfl(s.blocks0, owner, 64);
-    long long begin = __shfl(s.tiles0, owner, 64);
-    Group x = group_of(a, g, most, P::KT);
+    auto own_group = [&](int n) {
+        const int tiles = tiles_of(a, a.G + n, P::KT);
+        return Group{n, n + 1, a.S * a.H, a.own_blocks, tiles, walk_of(tiles)};
+    };
+    // the group, or the sequence's own rows, that the share begins in
+    int g, most = 0, block0 = 0;
+    long long begin;
+    Group x;
+    if (from < groups) {
+        const int owner = __builtin_ctzll(__ballot(s.tiles0 + s.tiles > from));
+        g = owner * s.per;
+        most = one(__shfl(s.most, owner, 64));
+        block0 = one(__shfl(s.blocks0, owner, 64));
+        begin = one(__shfl(s.tiles0, owner, 64));
+        x = group_of(a, g, most, P::KT);
+    } else { // (each of a sequence's blocks has a walk: found by their number)
+        int n, in;
+        const int number = (int)((from - groups) / a.own_blocks);
+        own.find(walks, number, lane, n, in);
+        n = one(n);
+        g = a.G + n;
+        begin = groups + (long long)(number - one(in)) * a.own_blocks;
+        x = own_group(n);
+    }
     for (long long at = from; at < to;) {
         while (begin + (long long)x.blocks * x.walk <= at) {
             begin += (long long)x.blocks * x.walk;
             block0 += x.blocks;
-            x = group_of(a, ++g, most, P::KT);
+            ++g;
+            x = g < a.G ? group_of(a, g, most, P::KT) : own_group(g - a.G);
+        }
+        if (g >= a.G && at == begin && threadIdx.x == 0) { // (for the join)
+            a.walks[2 * x.lo] = begin;
+            a.walks[2 * x.lo + 1] = share;
         }
         const int block = (int)((at - begin) / x.walk);
         const long long first = begin + (long long)block * x.walk, stop = min(first + x.walk, to);

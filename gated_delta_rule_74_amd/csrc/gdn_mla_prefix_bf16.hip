@@ -59,22 +59,18 @@ template <bool BF> __global__ __launch_bounds__(256) void mla_shared_join_kernel
     const Line s = line_of(p, lane, kt);
     // own rows
     int own, own_slot, own_qb, own_in;
-    if (p.own) {
-        const int g = p.G + nq, l = g / s.per, block = i0 / p.qb;
-        long long at = __shfl(s.tiles0, l, 64);
-        int most = __shfl(s.most, l, 64);
-        Group x = group_of(p, l * s.per, most, kt);
-        for (int i = 1; i <= g - l * s.per; ++i) {
-            at += (long long)x.blocks * x.walk;
-            x = group_of(p, l * s.per + i, most, kt);
-        }
-        at += (long long)block * x.walk + PREFIX_START;
-        own_slot = (int)(at / s.share);
-        own = x.tiles ? (int)((at + x.tiles - 1) / s.share) - own_slot + 1 : 0;
+    long long share;
+    if (p.own) { // (a token that is no padding has rows, so its sequence's walk was noted)
+        const int tiles = tiles_of(p, p.G + nq, kt), block = i0 / p.qb;
+        const long long at = p.walks[2 * nq] + (long long)block * walk_of(tiles) + PREFIX_START;
+        share = max(p.walks[2 * nq + 1], 1LL);
+        own_slot = (int)(at / share);
+        own = tiles ? (int)((at + tiles - 1) / share) - own_slot + 1 : 0;
         own_slot += nq * p.own_blocks + block;
         own_qb = p.own_qb;
         own_in = i0 - block * p.qb;
     } else {
+        share = share_of(p, s.total);
         const Share sh = share_out(a, lane);
         const int lane_of = nq / sh.per, tiles = seq_tiles(a, nq);
         int begin = __builtin_amdgcn_readlane(sh.before, lane_of);
@@ -119,7 +115,7 @@ template <bool BF> __global__ __launch_bounds__(256) void mla_shared_join_kernel
     const size_t row = (size_t)nq * rows + i0;
     const int qb = p.qb, in = (nq - first) * rows + i0, block = in / qb;
     const long long pb = at0 + (long long)block * pwalk + PREFIX_START;
-    const int u0 = ptiles ? (int)(pb / s.share) : 0, parts = ptiles ? (int)((pb + ptiles - 1) / s.share) - u0 + 1 : 0;
+    const int u0 = ptiles ? (int)(pb / share) : 0, parts = ptiles ? (int)((pb + ptiles - 1) / share) - u0 + 1 : 0;
     const bool real = seq_rows(a, nq) - a.S + i0 / a.H >= 0; // (a token before position 0 is padding)
     float m = -INFINITY, l = 0.f;
     f32x4 x = zero4();

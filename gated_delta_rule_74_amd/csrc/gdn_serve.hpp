@@ -37,6 +37,7 @@ struct PrefixArgs {
     int own_cols, own_blocks, own_qb; // blocks of a sequence's queries, queries of its parts
     float *own_part;   // workspace [units + N own_blocks][own_qb][dl]
     float *own_part_ml; // workspace [units + N own_blocks][own_qb][2]
+    long long *walks;  // workspace [N][2]: where a sequence's walk begins, the share (of sequences with rows)
 };
 void mla_prefix_plan(PrefixArgs &a, bool bf16, int cus); // sets qt, qb and units
 long long mla_prefix_blocks(const PrefixArgs &a);        // blocks of queries there may be
@@ -149,6 +150,7 @@ struct Pieces {
     template <class F> __device__ __forceinline__ static Pieces of(int N, F &&parts, int lane) {
         Pieces s = {N, (N + 63) / 64, 0, 0, 0};
         const int from = min(lane * s.per, N), to = min(from + s.per, N);
+#pragma unroll 4
         for (int i = from; i < to; ++i) s.mine += parts(i);
         s.sum(lane);
         return s;
