@@ -7,7 +7,9 @@
 // Bound by the state, read and written once: a wave holds 64 columns of one
 // head's state in registers, four columns of every fourth row in a lane, so a
 // row of the state is read in 16-byte pieces and the sum over the keys ends in
-// two exchanges between the wave's quarters.
+// two exchanges between the wave's quarters. 256 sequences, 16 heads of 56 x 56, up
+// to three tokens: 19 us, 5.4 TB/s; 33 sequences, 8 heads of 64 x 64, up to seven: 10 us,
+// the chain of the tokens.
 #include "gdn_common.hpp"
 #include "gdn_serve.hpp"
 

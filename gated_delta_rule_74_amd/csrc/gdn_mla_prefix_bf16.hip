@@ -40,9 +40,9 @@ void mla_prefix_plan(PrefixArgs &a, bool bf16, int cus) {
     a.own_qb = (int)(rows < a.qb ? rows : a.qb);
     long long most = mla_prefix_blocks(a) * cap;
     // Own rows are walked here as well, which saves a launch and its starts (48 sequences of three drafts and 700 rows
-    // of 512 + 64: 105 us with that launch, OWN_GROUPS without; 256 sequences of 128 + 32: 79 and OWN_SERVE), though a sequence's
-    // queries leave waves idle: in bf16, where the rows' bytes take the time even so. In fp32 the products
-    // do: there if they fill the waves, or if the walks may not fill the chip (SMALL).
+    // of 512 + 64: 105 us with a launch of their own, 88 without; 256 sequences of 1024 rows of 128 + 32: 79 and 76; five
+    // short ones in fp32: 21 and 18), though a sequence's queries leave waves idle: in bf16, where the rows' bytes take
+    // the time even so. In fp32 the products do: there if they fill the waves, or if all walks may not fill the chip.
     a.own = bf16 || 4 * rows >= 3LL * a.qb || most + a.N * a.own_blocks * own_cap <= a.units;
     if (a.own) most += a.N * a.own_blocks * own_cap;
     if (most < a.units) a.units = (int)most;

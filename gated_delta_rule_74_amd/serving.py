@@ -97,7 +97,8 @@ def mla_evict(weights, cache, block_table, lens, keep, *, first=0, recent=0, len
     first `first`, the last `recent` and those of the highest weights, moved to
     the front of its pages in their order, in cache [pages, page_size, d] and
     weights [pages, page_size] alike. block_table [N, max_pages], lens, keep
-    [N] int32. Returns the new lengths (page_trim gives the pages back)."""
+    [N] int32. Sequences that share a page with another must not be evicted.
+    Returns the new lengths (page_trim gives the pages back)."""
     _tensors(weights=weights, cache=cache, block_table=block_table, lens=lens, keep=keep)
     if cache.dim() != 3 or block_table.dim() != 2:
         raise ValueError("cache must be [pages, page_size, d], block_table [N, max_pages]")

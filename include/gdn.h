@@ -415,7 +415,9 @@ gdn_status_t gdn_mla_weights(const gdn_mla_step_shape_t *s, float decay, const v
  * front in their order, rows of cache [pages,page_size,d] and weights
  * [pages,page_size] fp32 alike, in place, and lens_out[n] = k; what stands
  * behind them in the sequence's pages stays as it was. Sequences with keep[n]
- * >= lens[n] are not touched. Pages are not given back here (several layers
+ * >= lens[n] are not touched. A page in use may stand in one sequence's table row
+ * alone (of two that hold it, each would move its rows: what then stands there
+ * is not defined). Pages are not given back here (several layers
  * may share a table): gdn_page_trim does that. Rows whose table entry lies outside
  * [0, pages) count as lighter than any other and are neither read nor written.
  * A page may be in use by one sequence only. row_bytes: bytes of a cache row, a
@@ -434,7 +436,8 @@ gdn_status_t gdn_mla_evict(int32_t N, int32_t max_pages, int32_t pages, int32_t 
  * free_pages [n_pages], of which n_free are free before and n_free_out
  * afterwards (may be the same). Lengths are clamped to what a row holds,
  * new_lens to [0, lens]; pages for which the stack has no room are lost. The
- * table is not changed (entries behind a length are not in use). All int32. */
+ * table is not changed (entries behind a length are not in use). A page that
+ * stands in two of those places is pushed twice. All int32. */
 gdn_status_t gdn_page_trim(int32_t N, int32_t max_pages, int32_t n_pages, int32_t page_size, const int32_t *lens,
                            const int32_t *new_lens, const int32_t *block_table, int32_t *free_pages,
                            const int32_t *n_free, int32_t *n_free_out, void *stream);
