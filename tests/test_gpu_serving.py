@@ -473,6 +473,28 @@ def test_verify_unusual_numbers():
     assert (wa[19:22] == 2).all() and wa[7] == 0
 
 
+@pytest.mark.parametrize("V", [2 ** 20 + 5, 2 ** 26 - 3])
+def test_verify_large_vocabularies(V):
+    """Equal logits: the token of u is floor(u V), whatever the number of pieces. (A term passes fewer than 2^11
+    additions, a lane's, a wave's and the pieces': a border is off by less than 2^11 2^-53 V < 2^-16 of a place; and by
+    2048 places times the exponential's 2^-34, 2^-23, inside a piece. u V is kept 0.01 away from borders.) Greedy: the
+    first largest, in the last piece."""
+    say(f"verify, V {V}")
+    z = torch.zeros((2, 1, V), dtype=torch.bfloat16, device="cuda")
+    z[1, 0, V - 2] = 1.0
+    z[1, 0, V - 1] = 1.0
+    draft, heat = torch.zeros((2, 0), dtype=torch.int32, device="cuda"), torch.tensor([0.7, 0.0], device="cuda")
+    for place in (0, 1, 2047, 2048, V // 3, V - 2049, V - 1):
+        # the fp32 number nearest the middle of the place, and the place that this one lies in
+        u = torch.tensor([[(place + 0.5) / V], [0.5]], dtype=torch.float32)
+        x = float(u[0, 0]) * V
+        if abs(x - round(x)) < 0.01:
+            continue
+        accepted, tokens, logprobs = gdn.draft_verify(z, draft, u.cuda(), temperature=heat)
+        assert accepted.tolist() == [0, 0] and tokens[:, 0].tolist() == [min(int(x), V - 1), V - 2]
+        assert abs(float(logprobs[0, 0]) + np.log(V)) < 2 ** -20 * np.log(V)
+
+
 def test_verify_ties_and_steps():
     """Two tokens that share all of the mass, exactly: borders that a rounding would move."""
     z = np.full((4, 1, 9000), -np.inf)

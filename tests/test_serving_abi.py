@@ -149,6 +149,14 @@ def commit(L, **over):  # noqa: F811
                                               "counts", "hin", "hout")], None)
 
 
+def test_verification_takes_vocabularies_up_to_a_limit(L):  # noqa: F811
+    for dtype in (0, 1):
+        assert L.gdn_draft_verify_workspace_size(1, 0, 2 ** 26, dtype) > 0
+        assert L.gdn_draft_verify_workspace_size(1, 0, 2 ** 26 + 1, dtype) == 0
+        assert L.gdn_draft_verify_workspace_size(31, 0, 2 ** 26, dtype) > 0
+        assert L.gdn_draft_verify_workspace_size(33, 0, 2 ** 26, dtype) == 0  # (2^31 elements and more)
+
+
 def test_commit_rejects_bad_arguments(L):  # noqa: F811
     for over in (dict(N=-1), dict(S=-1), dict(H=0), dict(dk=0), dict(dk=129), dict(dv=129), dict(dtype=3), dict(flags=8),
                  dict(N=1 << 20, H=64, dk=128, dv=128)):
