@@ -633,6 +633,33 @@ def test_two_streams_at_once():
     assert all(same(x, want[i % 2]) for i, x in enumerate(got))
 
 
+def test_two_evictions_at_once():
+    """Moves of more segments than the chip holds workgroups, on two streams together: every wait ends, each is as alone."""
+    page, N, n, d = 64, 96, 2048, 160
+    cols, streams, runs = n // page, [torch.cuda.Stream() for _ in range(2)], []
+    for i in range(2):
+        g = torch.Generator(device="cuda").manual_seed(9700 + i)
+        table = torch.randperm(N * cols, generator=g, device="cuda").int().view(N, cols)
+        cache = torch.randn((N * cols, page, d), generator=g, device="cuda").bfloat16()
+        w = torch.randn((N * cols, page), generator=g, device="cuda")
+        lens = torch.randint(1, n + 1, (N,), generator=g, device="cuda").int()
+        keep = lens // 2
+        alone = (w.clone(), cache.clone())
+        out = gdn.mla_evict(*alone, table, lens, keep, first=4, recent=16)
+        runs.append((w, cache, table, lens, keep, alone, out))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        copies = [(w.clone(), cache.clone()) for w, cache, *_ in runs]
+        torch.cuda.synchronize()
+        outs = []
+        for s, c, r in zip(streams, copies, runs):
+            with torch.cuda.stream(s):
+                outs.append(gdn.mla_evict(*c, *r[2:5], first=4, recent=16))
+        torch.cuda.synchronize()
+        for c, r, o in zip(copies, runs, outs):
+            assert torch.equal(o, r[6]) and torch.equal(c[0], r[5][0]) and torch.equal(bits(c[1]), bits(r[5][1]))
+
+
 def test_workspaces_of_the_callers():
     say("workspaces")
     a, _ = shared_inputs(SHARED[4], "bf16", 11)
