@@ -20,10 +20,10 @@
 // only grow from one piece to the next, and one of them does. The join adds up a query's parts.
 //
 // Measured: 256 sequences of up to 1024 rows behind a prefix of 16384, 16 heads of 128 + 32
-// bf16: 73 us and 10 us for the join. The vector instructions beside the products
+// bf16: 70 us and 9 us for the join. The vector instructions beside the products
 // (exponentials, sums, conversions: 140 for 36 products) bound it; the loads of a tile took
 // as many again before rows' addresses went through the wave and the walk lost its divisions.
-// 48 sequences of three drafts, four prefixes of 4096 to 8191 rows, 512 + 64 bf16: 73 and 15 us; LDS reads bound
+// 48 sequences of three drafts, four prefixes of 4096 to 8191 rows, 512 + 64 bf16: 70 and 15 us; LDS reads bound
 // it (a wave reads all of a tile for 16 queries, which is what its registers hold beside 512
 // columns of sums: 1.1 MB a tile and CU, 3.6 us of its 6), and the parts' 65 MB, written and read again.
 #pragma once
@@ -277,10 +277,8 @@ __device__ __forceinline__ void prefix_piece(const PrefixArgs a, int g, int lo, 
             }
             // What a token does not see is taken out behind the product, as its rows may hold anything. (The products'
             // results are waited for by hand: the compiler, ROCm 7.2, leaves the wait out behind a conditional block.)
-#pragma unroll
-            for (int t = 0; t < QT; ++t)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) asm volatile("s_nop 15" : "+v"(X[t][j]));
+            if constexpr (QT == 2) asm volatile("s_nop 15" : "+v"(X[0][0]), "+v"(X[0][1]), "+v"(X[1][0]), "+v"(X[1][1]));
+            else asm volatile("s_nop 15" : "+v"(X[0][0]), "+v"(X[0][1]));
             const int from = tile * P::KT + 32 * u;
             if (from + 32 > all_see) {
 #pragma unroll
