@@ -4,7 +4,7 @@
 namespace gdn {
 
 template <int DLP, int KS> static hipError_t rows_bf16(const PrefixArgs &a, hipStream_t st) {
-    if constexpr (DLP > 256) return prefix_run<true, DLP, KS, 1>(a, st);
+    if constexpr (DLP > 192) return prefix_run<true, DLP, KS, 1>(a, st);
     else return a.qt == 2 ? prefix_run<true, DLP, KS, 2>(a, st) : prefix_run<true, DLP, KS, 1>(a, st);
 }
 // (a rotary part of 32 columns or less needs one step of the product less)
@@ -28,8 +28,10 @@ long long mla_prefix_blocks(const PrefixArgs &a) {
 }
 void mla_prefix_plan(PrefixArgs &a, bool bf16, int cus) {
     const int c = step_class(a.dl);
-    // two blocks of queries a wave where a group has them: each tile read from LDS then serves twice as many products
-    a.qt = bf16 && c <= 256 && (long long)a.N * a.S * a.H >= 96LL * (a.G < a.N ? a.G : a.N) ? 2 : 1;
+    // Two blocks of queries a wave where a group fills them: each tile read from LDS then serves twice as many products
+    // (256 sequences, 16 heads, behind one prefix of 8192 rows: 64 columns 41 us with one, 37 with two, 128: 51 and 48, 192:
+    // 67 and 61; 256, where two spill, 75 and 130; eight groups of 96 queries, 128 columns: 21 and 22).
+    a.qt = bf16 && c <= 192 && (long long)a.N * a.S * a.H >= 256LL * (a.G < a.N ? a.G : a.N) ? 2 : 1;
     a.qb = 16 * prefix_nw(bf16, c) * a.qt;
     a.units = cus * prefix_per_cu(bf16, c);
     // the walks may hold so many tiles
