@@ -103,6 +103,20 @@ def test_shared_prefix_of_many_queries(dtype, H, dl):
     within("lse", lse[pick], wl, tl)
 
 
+@pytest.mark.parametrize("dl,dr", [(64, 32), (48, 48), (112, 16), (128, 64), (192, 32), (176, 56), (256, 64), (384, 32)])
+def test_shared_prefix_of_full_blocks(dl, dr):
+    """Every width's kernel for groups that fill blocks of queries, the last one in part; an odd page."""
+    case = (20, 1, 32, dl, dr, 24, [1 + 7 * n for n in range(20)], [450, 131], [0, 11, 20])
+    say(f"shared, full blocks {dl} {dr}")
+    a, f = shared_inputs(case, "bf16", 9240)
+    o, lse = gdn.mla_step_shared(*a, scale=0.1)
+    pick = [0, 10, 11, 19]
+    want, to, wl, tl = bound.shared(f[0][pick], f[1], f[2][pick], [case[6][n] for n in pick], dl, f[5], f[6], [0, 2, 4],
+                                    0.1, "bf16")
+    within("o", o[pick], want, to)
+    within("lse", lse[pick], wl, tl)
+
+
 @pytest.mark.parametrize("dtype,dl", [("bf16", 128), ("bf16", 512), ("fp32", 64), ("fp32", 320)])
 def test_own_rows_of_many_queries(dtype, dl):
     """More queries in a sequence than a block holds: its own rows are walked once for each block, the last one's mask
