@@ -336,6 +336,10 @@ template <bool BF> struct Source {
     double c;
     Dist p, q;
     const S *zp, *zq;
+    __device__ __forceinline__ void whole_row() { // p, whatever was rejected
+        mode = MODE_ROW;
+        x = -1;
+    }
     __device__ __forceinline__ Source(const VerifyArgs &a, int n, int how) : mode(how) {
         const double *pick = a.pick + (size_t)n * VERIFY_PICK;
         row = (int)pick[PICK_ROW];
@@ -387,14 +391,18 @@ template <bool BF> __global__ __launch_bounds__(VT) void verify_left_kernel(Veri
     if (threadIdx.x == 0) a.left[(size_t)n * a.nch + piece] = (ws[0] + ws[1]) + (ws[2] + ws[3]);
 }
 
+// A rejected draft that leaves less than this (of 1) had the same distribution as the target, as far as the
+// exponentials tell: of both their errors, 2^-33 of each probability, no more than 2^-32 can be left.
+constexpr double LEFT_LEAST = 0x1p-30;
+
 template <bool BF> __global__ __launch_bounds__(DT) void verify_draw_kernel(VerifyArgs a) {
     constexpr int G = Op<BF>::VEC, PER = VPIECE / DT, NG = PER / G; // places of a thread, in a row
     __shared__ double ws[DT / 64], rest;
-    __shared__ int where, first, last;
+    __shared__ int how, where, first, last;
     const int n = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
-    const int mode = (int)a.pick[(size_t)n * VERIFY_PICK + PICK_MODE];
-    if (mode == MODE_NONE || mode == MODE_TOKEN) return;
-    const Source<BF> src(a, n, mode);
+    const int decided = (int)a.pick[(size_t)n * VERIFY_PICK + PICK_MODE];
+    if (decided == MODE_NONE || decided == MODE_TOKEN) return;
+    Source<BF> src(a, n, decided);
     const size_t out = (size_t)n * (a.S + 1) + src.row;
     auto emit = [&](int v, float z) {
         a.tokens[out] = v;
@@ -402,17 +410,25 @@ template <bool BF> __global__ __launch_bounds__(DT) void verify_draw_kernel(Veri
     };
     // the piece: the first whose end passes u times the whole (should none, the last with anything), by one wave
     if (tid < 64) {
-        const size_t at = (mode == MODE_ROW ? out : (size_t)n) * a.nch;
         auto part = [&](int k) {
             if (k >= a.nch) return 0.0;
-            if (mode != MODE_ROW) return a.left[at + k];
-            return a.refs[at + k] > -INFINITY ? a.sums[at + k] * exp2_f64<10>(log2_p((double)a.refs[at + k], src.p, src.c))
-                                              : 0.0;
+            if (src.mode != MODE_ROW) return a.left[(size_t)n * a.nch + k];
+            const size_t at = out * a.nch + k;
+            return a.refs[at] > -INFINITY ? a.sums[at] * exp2_f64<10>(log2_p((double)a.refs[at], src.p, src.c)) : 0.0;
         };
-        const double u = uniform_of(a.uniforms[(size_t)n * (a.S + 1) + a.S]), here = part(lane);
-        double all = here;
-        for (int k = 64 + lane; k < a.nch; k += 64) all += part(k);
-        const double aim = u * wave_sum_d(all);
+        double here;
+        auto whole = [&] {
+            double all = here = part(lane);
+            for (int k = 64 + lane; k < a.nch; k += 64) all += part(k);
+            return wave_sum_d(all);
+        };
+        const double u = uniform_of(a.uniforms[(size_t)n * (a.S + 1) + a.S]);
+        double aim = whole();
+        if (src.mode != MODE_ROW && aim < LEFT_LEAST) {
+            src.whole_row();
+            aim = whole();
+        }
+        aim *= u;
         double before = 0.0, start = 0.0;
         int piece = -1;
         for (int k0 = 0; k0 < a.nch; k0 += 64) {
@@ -433,6 +449,7 @@ template <bool BF> __global__ __launch_bounds__(DT) void verify_draw_kernel(Veri
             before += __shfl(s, 63, 64);
         }
         if (tid == 0) {
+            how = src.mode;
             where = piece;
             rest = aim - start; // to be passed within the piece
             first = 2147483647;
@@ -441,7 +458,8 @@ template <bool BF> __global__ __launch_bounds__(DT) void verify_draw_kernel(Veri
     }
     __syncthreads();
     const int piece = where;
-    if (piece < 0) { // (nothing left: not with finite numbers)
+    if (how == MODE_ROW) src.whole_row();
+    if (piece < 0) { // (not where p has a distribution)
         if (tid == 0) emit(-1, 0.f);
         return;
     }
@@ -454,7 +472,7 @@ template <bool BF> __global__ __launch_bounds__(DT) void verify_draw_kernel(Veri
         Group<BF> gp[NG], gq[NG];
 #pragma unroll
         for (int k = 0; k < NG; ++k) gp[k].load(src.zp, a.V, v0 + k * G);
-        if (mode == MODE_DIFF) {
+        if (src.mode == MODE_DIFF) {
 #pragma unroll
             for (int k = 0; k < NG; ++k) gq[k].load(src.zq, a.V, v0 + k * G);
         }
@@ -463,7 +481,7 @@ template <bool BF> __global__ __launch_bounds__(DT) void verify_draw_kernel(Veri
             const int at = Group<BF>::place(a.V, v0 + k * G);
             float w[G] = {};
             gp[k].get(a.V, v0 + k * G, tail, z[k]);
-            if (mode == MODE_DIFF) gq[k].get(a.V, v0 + k * G, tail, w);
+            if (src.mode == MODE_DIFF) gq[k].get(a.V, v0 + k * G, tail, w);
 #pragma unroll
             for (int e = 0; e < G; ++e) {
                 r[k][e] = at + e == src.x ? 0.0 : src.weight(z[k][e], w[e]);

@@ -454,6 +454,8 @@ gdn_status_t gdn_page_trim(int32_t N, int32_t max_pages, int32_t n_pages, int32_
  * accepted while uniforms[n,i] q_i(x) < p_i(x). At the first one that is not,
  * a token is drawn from max(p_i - q_i, 0); after the last one from p_i of the
  * next row: the lowest v with C(v) > uniforms[n,S] C(V-1), C the running sum.
+ * Where max(p_i - q_i, 0) sums to less than 2^-30 (a draft that neither gives
+ * any probability, before equal distributions), the token is drawn from p_i.
  * Greedy: a draft is accepted when it is the row's first largest logit, which is
  * also the token drawn. Logits of -inf have probability 0.
  *   accepted [N] int32   drafts accepted

@@ -163,6 +163,8 @@ def draft_verify(z, draft, u, zq, lens, temp):
                     break
                 if not un[i] * q[x] < p[x]:
                     last = np.maximum(p - q, 0.0)
+                    if last.sum() < 2.0 ** -30:  # (as good as nothing: the distributions are the same)
+                        last = p
                     break
             tokens[n, i], lp[n, i] = x, np.log(p[x])
             i += 1

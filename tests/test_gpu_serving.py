@@ -487,6 +487,29 @@ def test_verify_unusual_numbers():
     assert (wa[19:22] == 2).all() and wa[7] == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("V", [9, 5000])
+def test_verify_where_a_rejected_draft_leaves_nothing(V, dtype):
+    """Drafts that neither model gives any probability, masked or far below at a low temperature, before equal
+    distributions: rejected, and the token is drawn from p. Equal with the same logits, with others a constant apart
+    (1, which both types hold beside multiples of 1/16 below 8), and as one token alone."""
+    say(f"verify, nothing left {V} {dtype}")
+    g, N = rng(9991), 24
+    z = np.round(16 * g.standard_normal((N, 2, V)).clip(-4, 4)) / 16
+    z[:, :, 5] = -np.inf
+    draft, temp = np.full((N, 1), 5, np.int32), np.ones(N, np.float32)
+    zq = z[:, :1] + np.where(np.arange(N) % 2, 1.0, 0.0)[:, None, None]
+    z[12:, :, 5], zq[12:, :, 5] = -4, -4  # p = q = 0 only as numbers: e^-4000 and less
+    z[12:, :, 3] += 8
+    zq[12:, :, 3] += 8 + np.where(np.arange(12, N) % 2, 1 / 16, 0)[:, None]
+    temp[12:] = 1e-3
+    u = g.random((N, 2)).astype(np.float32)
+    u[::5, 1], u[1::5, 1] = 0.0, 1.0
+    a = dict(logits=dev(z, dtype)[0], draft=draft, uniforms=u, draft_logits=dev(zq, dtype)[0], draft_lens=None, temperature=temp)
+    wa = check_verify(a, (dev(z, dtype)[1], draft, u, dev(zq, dtype)[1], None, temp))
+    assert not wa.any()
+
+
 @pytest.mark.parametrize("V", [2 ** 20 + 5, 2 ** 26 - 3])
 def test_verify_large_vocabularies(V):
     """Equal logits: the token of u is floor(u V), whatever the number of pieces. (A term passes fewer than 2^11

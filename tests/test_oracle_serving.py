@@ -112,6 +112,18 @@ def test_verified_drafts_are_distributed_as_the_target():
         np.testing.assert_allclose(chance, np.exp(z), atol=3e-3)  # (two grids of a thousand points)
 
 
+def test_a_rejected_draft_that_leaves_nothing_draws_from_the_target():
+    """Equal distributions, and a draft to which they give nothing: masked, or below what fp64 holds."""
+    for z, t in (([0., 1, -np.inf], 1.0), ([0., 0.5, -9], 1e-3), ([0., 1, -23], 1.0)):
+        z = np.array(z)
+        p = serving.distribution(z, t)
+        for u in (0.0, 0.2, 0.9):
+            a, tok, lp = serving.draft_verify(np.tile(z, (1, 2, 1)), np.array([[2]]), np.array([[1.0, u]]), z[None, None] + 3,
+                                              None, [t])
+            want = 2 if p[2] else int(u >= p[0])  # (as long as the draft has a chance, it stands)
+            assert a[0] == (p[2] > 0) and tok[0, 0] == want and abs(lp[0, 0] - np.log(p[want])) < 1e-12
+
+
 def test_greedy_verification_follows_the_largest_logit():
     z = np.array([[[1., 3, 3, 0], [0, 0, 5, 0], [2, 1, 0, 0]]])
     a, t, _ = serving.draft_verify(z, np.array([[1, 3]]), np.ones((1, 3)), None, None, [0.0])
