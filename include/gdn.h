@@ -435,7 +435,8 @@ gdn_status_t gdn_mla_evict(int32_t N, int32_t max_pages, int32_t pages, int32_t 
  * ceil(lens[n] / page_size) - 1 of block_table [N,max_pages] are pushed on
  * free_pages [n_pages], of which n_free are free before and n_free_out
  * afterwards (may be the same). Lengths are clamped to what a row holds,
- * new_lens to [0, lens]; pages for which the stack has no room are lost. The
+ * new_lens to [0, lens]; pages for which the stack has no room are lost,
+ * entries below 0 (no page) are left out. The
  * table is not changed (entries behind a length are not in use). A page that
  * stands in two of those places is pushed twice. All int32. */
 gdn_status_t gdn_page_trim(int32_t N, int32_t max_pages, int32_t n_pages, int32_t page_size, const int32_t *lens,

@@ -118,7 +118,7 @@ def page_trim(lens, new, table, stack, n_free, page):
         L = min(max(int(lens[n]), 0), table.shape[1] * page)
         m = min(max(int(new[n]), 0), L)
         for c in range(-(-m // page), -(-L // page)):
-            if top < F:
+            if top < F and table[n, c] >= 0:  # (below 0: no page)
                 stack[top] = table[n, c]
                 top += 1
     return stack, top

@@ -408,6 +408,26 @@ def test_page_trim(N, page, most, room):
     assert int(f) == top and (s.cpu().numpy() == want).all()
 
 
+@pytest.mark.parametrize("N,page,most,room", [(1, 1, 3, 9), (3, 16, 100, 50), (1025, 16, 200, 10 ** 5), (2500, 3, 40, 7000),
+                                              (4, 64, 60000, 3500), (300, 16, 700, 10 ** 5)])
+@pytest.mark.parametrize("share", [0.001, 0.3, 1.0])
+def test_page_trim_leaves_out_entries_that_are_no_page(N, page, most, room, share):
+    """Entries below 0, which page_plan would hand out again: the others are pushed in their order."""
+    say(f"trim, no pages {N} {page} {most} {share}")
+    g = rng(9961)
+    lens, new, cols = g.integers(-2, most + 3, N), g.integers(-5, most // 2, N), -(-most // page)
+    t = g.integers(0, 10 ** 6, (N, cols)).astype(np.int32)
+    none = g.random(t.shape) < share
+    t[none] = g.choice([-1, -5, -2 ** 31], none.sum())
+    stack = np.full(5 + room + 1, -9, np.int32)
+    stack[:5] = np.arange(5) + 7
+    want, top = ref.page_trim(lens, new, t, stack, 5, page)
+    assert (want[:top] >= 0).all()
+    s = ints(stack)
+    out = gdn.page_trim(ints(lens), ints(new), ints(t), s, ints([5]), page)
+    assert int(out) == top and (s.cpu().numpy() == want).all()
+
+
 # ---------------------------------------------------------------- draft verification
 
 def drafts(N, S, V, dtype, seed, with_q, ragged, heat, close=0.7):

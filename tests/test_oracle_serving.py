@@ -90,6 +90,12 @@ def test_page_trim_gives_back_what_a_plan_would_take_again():
     assert list(stack) == [70, 71, 1, 2, 9] and top == 5  # (10 found no room)
 
 
+def test_page_trim_gives_back_pages_alone():
+    stack, top = serving.page_trim([12, 8, 12], [0, 4, 5], np.array([[3, -1, 7], [5, -4, 6], [-1, 1, -2]]),
+                                   np.array([70, 71, -9, -9, -9, -9]), 2, 4)
+    assert list(stack) == [70, 71, 3, 7, -9, -9] and top == 4  # (the others hold 1, and no pages, behind their lengths)
+
+
 def test_verified_drafts_are_distributed_as_the_target():
     """Chance of each emitted token over a fine grid of both random numbers: the target's own."""
     z, zq = np.log(np.array([0.5, 0.2, 0.2, 0.1])), np.log(np.array([0.1, 0.6, 0.2, 0.1]))
