@@ -127,9 +127,9 @@ template <bool BF, int RI, bool VEC> __global__ __launch_bounds__(CW * 64) void 
     }
 }
 
+long long step_commit_groups(int N, int H, int dv) { return ((long long)N * H * ((dv + 63) / 64) + CW - 1) / CW; }
 template <bool BF, int RI> static hipError_t commit_run(const CommitArgs &a, hipStream_t st) {
-    const long long items = (long long)a.N * a.H * ((a.dv + 63) / 64);
-    const dim3 grid((unsigned)((items + CW - 1) / CW));
+    const dim3 grid((unsigned)step_commit_groups(a.N, a.H, a.dv));
     // 16-byte pieces where every row of the state and of v begins on one
     const auto on = [](const void *p, size_t n) { return (uintptr_t)p % n == 0; };
     if (a.dv % 4 == 0 && on(a.h_in, 16) && on(a.h_out, 16) && on(a.v, BF ? 8 : 16))

@@ -54,6 +54,7 @@ struct CommitArgs {
     float *h_out;
     int N, S, H, dk, dv, additive, logits, l2k;
 };
+long long step_commit_groups(int N, int H, int dv); // workgroups of 256 threads
 hipError_t launch_step_commit(const CommitArgs &a, bool bf16, hipStream_t st);
 
 struct PageTrimArgs {

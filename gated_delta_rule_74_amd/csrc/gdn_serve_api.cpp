@@ -101,6 +101,8 @@ gdn_status_t gdn_step_commit(int32_t N, int32_t S, int32_t H, int32_t dk, int32_
     if (flags & ~STEP_FLAGS) return fail(GDN_EINVAL, "unknown flag bits 0x%x", flags);
     if ((double)N * H * dk * dv >= LIMIT || (double)N * S * H * (dk > dv ? dk : dv) >= LIMIT)
         return fail(GDN_EINVAL, "state or tokens too large");
+    if (S > 0 && (double)gdn::step_commit_groups(N, H, dv) * 256 >= THREADS)
+        return fail(GDN_EINVAL, "too many states for a launch");
     const size_t e = esize(dtype), n = (size_t)N * S * H, state = (size_t)N * H * dk * dv * 4;
     const Buf b[] = {{k, n * dk * e, "k", 4, false, true},
                      {v, n * dv * e, "v", 4, false, true},

@@ -226,7 +226,7 @@ gdn_status_t gdn_step_tokens(int32_t N, int32_t S, int32_t H, int32_t dk, int32_
  * flags and h_in / h_out (NULL: zero state; the same buffer: in place) as in
  * gdn_step_tokens; k [N,S,H,dk], v [N,S,H,dv], g, beta [N,S,H], counts [N]
  * int32. Tokens past a count are not read. The state is read and written once;
- * a sequence whose count is 0 keeps its state. */
+ * a sequence whose count is 0 keeps its state. With S > 0, N * H is at most 2^26 - 4. */
 gdn_status_t gdn_step_commit(int32_t N, int32_t S, int32_t H, int32_t dk, int32_t dv, int32_t dtype, uint32_t flags,
                              const void *k, const void *v, const float *g, const float *beta, const float *A_log,
                              const int32_t *counts, const float *h_in, float *h_out, void *stream);

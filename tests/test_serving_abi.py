@@ -169,6 +169,15 @@ def test_commit_rejects_bad_arguments(L):  # noqa: F811
     assert commit(L, S=0, k=None, v=None, g=None, beta=None, A=None, counts=None, hout=fake(7)) == 0  # in place: nothing to do
 
 
+def test_commit_rejects_more_states_than_a_launch_has_threads_for(L):  # noqa: F811
+    """A wave takes 64 columns of a state, a launch has fewer than 2^32 threads."""
+    far = dict(k=fake(1), v=fake(20), g=fake(40), beta=fake(60), A=fake(80), counts=fake(100), hin=fake(120), hout=fake(140))
+    for N, H, dk, dv in ((1 << 26, 1, 1, 1), (1 << 27, 1, 1, 1), (1 << 20, 64, 1, 1), ((1 << 26) - 3, 1, 1, 1), (1 << 22, 16, 5, 6),
+                         (1 << 26, 1, 1, 31), (1 << 25, 2, 31, 1)):
+        assert commit(L, N=N, S=1, H=H, dk=dk, dv=dv, **far) == EINVAL, (N, H, dk, dv)
+        assert b"launch" in L.gdn_last_error_detail()
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes():
     z, i = torch.zeros, lambda *s: torch.zeros(s, dtype=torch.int32)
     with pytest.raises(ValueError):
