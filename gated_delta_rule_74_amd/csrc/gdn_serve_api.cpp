@@ -37,7 +37,8 @@ gdn_status_t check_evict(int32_t N, int32_t max_pages, int32_t page_size, int32_
     if (row_bytes < 16 || row_bytes % 16) return fail(GDN_EINVAL, "row_bytes must be a multiple of 16");
     if (row_bytes > 16 * gdn::EVICT_ROW16)
         return fail(GDN_EUNSUPPORTED, "row_bytes must be at most %d", 16 * gdn::EVICT_ROW16);
-    if ((double)max_pages * page_size > LIMIT - AHEAD || (double)N * max_pages >= LIMIT)
+    // (the end of a sequence's last chunk stays in int32)
+    if ((double)max_pages * page_size > LIMIT - gdn::EVICT_CHUNK || (double)N * max_pages >= LIMIT)
         return fail(GDN_EINVAL, "table too large");
     // (segments are counted in int32; one workgroup of 1024 threads for every chunk)
     const double rows = (double)max_pages * page_size;

@@ -421,7 +421,8 @@ gdn_status_t gdn_mla_weights(const gdn_mla_step_shape_t *s, float decay, const v
  * may share a table): gdn_page_trim does that. Rows whose table entry lies outside
  * [0, pages) count as lighter than any other and are neither read nor written.
  * A page may be in use by one sequence only. row_bytes: bytes of a cache row, a
- * multiple of 16 up to 2304; first, recent >= 0. ws:
+ * multiple of 16 up to 2304; first, recent >= 0; max_pages * page_size at most
+ * 2^31 - 8192, N * max_pages and pages * page_size below 2^31. ws:
  * gdn_mla_evict_workspace_size() bytes, 256-byte aligned. */
 size_t gdn_mla_evict_workspace_size(int32_t N, int32_t max_pages, int32_t page_size, int32_t row_bytes);
 gdn_status_t gdn_mla_evict(int32_t N, int32_t max_pages, int32_t pages, int32_t page_size, int32_t row_bytes,

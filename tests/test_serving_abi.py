@@ -104,6 +104,15 @@ def test_eviction_rejects_bad_arguments(L):  # noqa: F811
     assert evict(L, N=0, table=None, lens=None, keep=None, w=None, cache=None, out=None, ws=None, ws_bytes=0) == 0
 
 
+def test_eviction_rejects_tables_that_hold_nearly_2_31_rows(L):  # noqa: F811
+    """Such a sequence's chunks of 8192 rows cannot be counted in int32 (the last one's end passes it)."""
+    for cols, page in ((2 ** 31 - 2048, 1), ((2 ** 31 - 4096) // 64, 64), ((2 ** 31 - 8128) // 64, 64)):
+        assert L.gdn_mla_evict_workspace_size(1, cols, page, 16) == 0, (cols, page)
+        assert evict(L, N=1, cols=cols, pages=10, page=page, row=16, ws_bytes=1 << 40) == EINVAL, (cols, page)
+        assert b"table" in L.gdn_last_error_detail()
+    assert L.gdn_mla_evict_workspace_size(1, (2 ** 31 - 8192) // 64, 64, 16) > 0
+
+
 def trim(L, **over):  # noqa: F811
     a = dict(N=3, cols=5, F=10, page=4, lens=fake(1), new=fake(2), table=fake(3), stack=fake(4), free=fake(5), out=fake(6))
     a.update(over)
