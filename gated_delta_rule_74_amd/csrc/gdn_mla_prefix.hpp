@@ -275,8 +275,10 @@ __device__ __forceinline__ void prefix_piece(const PrefixArgs a, int g, int lo, 
                             if (i * KG + k < KS) X[t][j] = mma8(kf[i & 1][k][j], Q[t][i * KG + k], X[t][j]);
                 in_flight();
             }
-            // What a token does not see is taken out behind the product, as its rows may hold anything. (The products'
-            // results are waited for by hand: the compiler, ROCm 7.2, leaves the wait out behind a conditional block.)
+            // What a token does not see is taken out behind the product, whatever its rows' scores came to. (In the
+            // product with the values such a row still has its place, with probability 0: finite values leave no
+            // trace, a NaN or infinity reaches the sequence's other tokens, as in the step.) The products'
+            // results are waited for by hand: the compiler, ROCm 7.2, leaves the wait out behind a conditional block.
             if constexpr (QT == 2) asm volatile("s_nop 15" : "+v"(X[0][0]), "+v"(X[0][1]), "+v"(X[1][0]), "+v"(X[1][1]));
             else asm volatile("s_nop 15" : "+v"(X[0][0]), "+v"(X[0][1]));
             const int from = tile * P::KT + 32 * u;

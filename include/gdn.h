@@ -374,7 +374,12 @@ gdn_status_t gdn_page_plan(int32_t N, int32_t max_pages, int32_t n_pages, int32_
 
 /* ---------------------------------------------------------------------------
  * Serving beside the plain step: prefixes that a batch shares, caches that may
- * not grow, drafts. The rules at the top of this file hold.
+ * not grow, drafts. The rules at the top of this file hold, and those of
+ * gdn_mla_step for what a call rounds and how far a NaN reaches: gdn_mla_step_shared
+ * in bf16 rounds the probabilities for their product with the rows, and a NaN or
+ * infinity in one of a sequence's own rows may reach o of all S tokens of that
+ * sequence, those before the row among them (their lse stays right). In
+ * gdn_mla_weights a row reaches its own weight alone.
  */
 
 /* gdn_mla_step for sequences that share long prefixes: sequences starts[g] ..
@@ -466,7 +471,8 @@ gdn_status_t gdn_page_trim(int32_t N, int32_t max_pages, int32_t n_pages, int32_
  * A target row without a distribution (a NaN, +inf, nothing above -inf)
  * accepts nothing and draws -1 (with logprob 0). A draft outside [0, V), or whose row of
  * draft_logits has no distribution, is not accepted and the token is drawn from p_i.
- * Sums run in fp64. N, S >= 0, 1 <= V <= 2^26; each tensor below 2^31 elements; ws:
+ * Sums run in fp64, of exponentials that are off by up to 2^-34 of their value.
+ * N, S >= 0, 1 <= V <= 2^26; each tensor below 2^31 elements; ws:
  * gdn_draft_verify_workspace_size() bytes, 256-byte aligned. */
 size_t gdn_draft_verify_workspace_size(int32_t N, int32_t S, int32_t V, int32_t dtype);
 gdn_status_t gdn_draft_verify(int32_t N, int32_t S, int32_t V, int32_t dtype, const void *logits, const int32_t *draft,

@@ -237,6 +237,25 @@ def test_nan_in_a_prefix_reaches_its_group_alone():
     assert o2[:2].isnan().any() and torch.equal(o2[2:], o[2:])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("dl", [64, 128, 512])
+def test_nan_in_an_own_row_reaches_its_sequence_alone(dl, dtype):
+    """The last draft's row: the sequence's other tokens do not see it, but share its tile (as in mla_step). Their lse,
+    and all of other sequences, stay as they were."""
+    case = (4, 3, 4, dl, 16, 16, [3, 20, 9, 70], [100, 70], [0, 2, 4])
+    a, f = shared_inputs(case, dtype, 9610)
+    o, lse = gdn.mla_step_shared(*a, scale=0.2)
+    for bad in (float("nan"), float("inf")):
+        row = a[1][f[2][1, 19 // 16], 19 % 16]
+        was = row.clone()
+        row[5] = bad
+        o2, lse2 = gdn.mla_step_shared(*a, scale=0.2)
+        others = [0, 2, 3]
+        assert torch.equal(o2[others], o[others]) and torch.equal(lse2[others], lse[others])
+        assert torch.equal(lse2[1, :2], lse[1, :2]) and o2[1, 2].isnan().any()
+        row.copy_(was)
+
+
 # ---------------------------------------------------------------- weights of cached rows
 
 WEIGHTS = [
