@@ -305,7 +305,8 @@ def page_plan(lens, new_lens, block_table, free_pages, n_free, page_size, max_to
     in place, new_lens[i] < 0 ends sequence i. Returns a dict with starts
     [N + 1], granted [N], lens [N], n_free [1], slots and positions
     [max_tokens], block_table and free_pages. lens_out=lens and
-    n_free_out=n_free update those in place too."""
+    n_free_out=n_free update those in place too. positions count the rows that
+    a sequence holds, without a shared prefix's and those an eviction dropped."""
     _tensors(lens=lens, new_lens=new_lens, block_table=block_table, free_pages=free_pages, n_free=n_free)
     if block_table.dim() != 2 or free_pages.dim() != 1:
         raise ValueError("block_table must be [N, max_pages], free_pages [n_pages]")

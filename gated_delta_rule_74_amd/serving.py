@@ -44,7 +44,9 @@ def mla_step_shared(q, cache, block_table, lens, dl, prefix_table, prefix_lens, 
     starts[g + 1] - 1 see the prefix_lens[g] cached rows of prefix_table[g]
     before their own. q, cache, block_table, lens as in mla_step (lens counts
     own rows only, the new tokens' included); prefix_table [G, prefix_pages],
-    prefix_lens [G], starts [G + 1], all int32. Returns (o [..., dl], lse)."""
+    prefix_lens [G], starts [G + 1], all int32. page_plan's positions of the new
+    tokens lack the prefix's length: add it before rows and queries are turned by
+    them. Returns (o [..., dl], lse)."""
     s, lead = _paged(q, cache, block_table, lens, dl, scale)
     _tensors(prefix_table=prefix_table, prefix_lens=prefix_lens, starts=starts)
     if prefix_table.dim() != 2:
@@ -98,7 +100,10 @@ def mla_evict(weights, cache, block_table, lens, keep, *, first=0, recent=0, len
     the front of its pages in their order, in cache [pages, page_size, d] and
     weights [pages, page_size] alike. block_table [N, max_pages], lens, keep
     [N] int32. Sequences that share a page with another must not be evicted.
-    Returns the new lengths (page_trim gives the pages back)."""
+    Kept rows stay turned as they are, and page_plan's positions of later tokens
+    lack the rows dropped: add lens less the result, from every eviction, before
+    rows and queries are turned by them. Returns the new lengths (page_trim gives
+    the pages back)."""
     _tensors(weights=weights, cache=cache, block_table=block_table, lens=lens, keep=keep)
     if cache.dim() != 3 or block_table.dim() != 2:
         raise ValueError("cache must be [pages, page_size, d], block_table [N, max_pages]")

@@ -361,7 +361,11 @@ gdn_status_t gdn_mla_write(int64_t n, int32_t dl, int32_t dr, int32_t dtype, uin
  *   starts [N+1]       their prefix sums: where a sequence's new tokens begin
  *   slots [max_tokens] page * page_size + offset of every new token; -1 past
  *                      the last one
- *   positions [max_tokens]  its position in its sequence; 0 past the last one
+ *   positions [max_tokens]  its position in its sequence, the rows that the
+ *                      sequence holds before it; 0 past the last one. Rows of a
+ *                      prefix (gdn_mla_step_shared) and rows that an eviction
+ *                      dropped (gdn_mla_evict) are not in it: a caller who turns
+ *                      queries and keys by position adds their number first
  *   lens_out [N]       lengths afterwards (may be lens)
  *   n_free_out [1]     free pages afterwards (may be n_free)
  * block_table and free_pages are updated in place; with separate lens_out and
@@ -388,7 +392,8 @@ gdn_status_t gdn_page_plan(int32_t N, int32_t max_pages, int32_t n_pages, int32_
  * pages of the same cache) before their own, so that token s of sequence n
  * sees those rows and its own rows j <= lens[n] - S + s (block_table, lens).
  * Sequences of no group have no prefix. A token at a position before 0
- * (lens[n] - S + s < 0: padding) sees nothing: o = 0, lse = -inf. The prefix's
+ * (lens[n] - S + s < 0: padding) sees nothing: o = 0, lse = -inf. Own rows and
+ * queries that are turned by position stand at prefix_lens[g] + j. The prefix's
  * rows are read once for many of the group's queries instead of once for each
  * sequence. s->N, max_pages and the limits of gdn_mla_step; prefix_pages *
  * page_size at most 2^31 - 2048, G * prefix_pages below 2^31. G = 0: no prefix
@@ -419,7 +424,9 @@ gdn_status_t gdn_mla_weights(const gdn_mla_step_shape_t *s, float decay, const v
  * the lowest positions; a NaN counts as the highest, -0 as 0). They move to the
  * front in their order, rows of cache [pages,page_size,d] and weights
  * [pages,page_size] fp32 alike, in place, and lens_out[n] = k; what stands
- * behind them in the sequence's pages stays as it was. Sequences with keep[n]
+ * behind them in the sequence's pages stays as it was. Rotary keys keep the
+ * position they were turned to; of the tokens that follow, gdn_page_plan's
+ * positions are lens[n] - k too low. Sequences with keep[n]
  * >= lens[n] are not touched. A page in use may stand in one sequence's table row
  * alone (of two that hold it, each would move its rows: what then stands there
  * is not defined). Pages are not given back here (several layers

@@ -844,3 +844,61 @@ def test_a_serving_loop():
         held = [int(p) for n, r in enumerate(rows) for p in tb[n, :-(-len(r) // page)]]
         free = stack[:int(n_free)].tolist()
         assert sorted(held + free) == sorted(int(x) for x in rest)
+
+
+def test_positions_behind_a_prefix_and_after_evictions():
+    """page_plan counts the rows a sequence holds. With what it has in front and what it has lost added, every cached
+    rotary key is turned by its token's place in the whole text, prefix, evicted rows and sequences that end included."""
+    say("positions")
+    g = rng(78)
+    N, P, dl, dr, page, pages, cols, cap = 5, 6, 16, 8, 4, 80, 12, 16
+    stack, n_free, table = ints(g.permutation(pages)), ints([pages]), ints(np.full((N, cols), -1))
+    lens, weights, front = ints(np.zeros(N)), torch.zeros((pages, page), device="cuda"), ints([P, 0, P, 0, P])
+    cache, away = torch.full((pages, page, dl + dr), float("nan"), device="cuda"), front.clone()
+    freqs = 100.0 ** (-np.arange(dr // 2) / (dr // 2))
+    fr = torch.tensor(freqs, device="cuda")
+    held = [[] for _ in range(N)]  # the rows of each sequence: key before its turn, place in the text
+    told = [int(x) for x in front]  # tokens of the text so far
+    for step in range(12):
+        new = g.integers(0, 5, N)
+        if step in (5, 9):
+            new[step % N] = -1
+            away[step % N], held[step % N], told[step % N] = front[step % N], [], int(front[step % N])
+        plan = gdn.page_plan(lens, ints(new), table, stack, n_free, page, cap, lens_out=lens, n_free_out=n_free)
+        seq = torch.searchsorted(plan["starts"], torch.arange(cap, dtype=torch.int32, device="cuda"), right=True) - 1
+        positions = plan["positions"] + away[seq.clamp(max=N - 1)]
+        c, kr = torch.zeros((cap, dl), device="cuda"), dev(g.standard_normal((cap, dr)), "fp32")
+        gdn.mla_write(c, kr[0], plan["slots"], cache, None, positions, fr, norm=False)
+        t = 0
+        for n, k in enumerate(plan["granted"].tolist()):
+            for _ in range(k):
+                held[n].append((kr[1][t], told[n]))
+                told[n] += 1
+                t += 1
+        # some new tokens are taken back (their places are given again), then rows are dropped (theirs are not)
+        back = np.minimum(g.integers(0, 3, N), np.maximum(plan["granted"].cpu().numpy(), 0))
+        kept = lens - ints(back)
+        gdn.page_trim(lens, kept, table, stack, n_free, page, n_free_out=n_free)
+        for n, k in enumerate(back):
+            held[n] = held[n][:len(held[n]) - k]
+            told[n] -= k
+        weights.copy_(torch.rand((pages, page), generator=torch.Generator("cuda").manual_seed(step), device="cuda"))
+        w, tb = host(weights), table.cpu().numpy()
+        fewer = gdn.mla_evict(weights, cache, table, kept, ints([7] * N), first=1, recent=2)
+        away += kept - fewer
+        gdn.page_trim(kept, fewer, table, stack, n_free, page, n_free_out=n_free)
+        lens = fewer
+        for n, rows in enumerate(held):
+            m = len(rows)
+            if m > 7:
+                best = sorted(range(1, m - 2), key=lambda j: (-w[tb[n, j // page], j % page], j))[:4]
+                held[n] = [rows[j] for j in [0] + sorted(best) + [m - 2, m - 1]]
+        assert lens.tolist() == [len(r) for r in held]
+        got, tb = host(cache), table.cpu().numpy()
+        for n, rows in enumerate(held):
+            for j, (k, place) in enumerate(rows):
+                want = latent.turn(k[None, None], np.array([place]), freqs, False)[0, 0]
+                x = got[tb[n, j // page], j % page, dl:]
+                # two products with a sine or cosine, each off by 2^-21 and ten roundings
+                assert (np.abs(x - want) <= 2 * (2.0 ** -21 + 10 * U) * np.abs(k).max()).all(), (step, n, j, place)
+    assert max(told) > P + 14 and int((away - front).max()) > 0
