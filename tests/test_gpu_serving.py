@@ -145,6 +145,26 @@ def test_own_rows_apart_in_fp32(H):
     within("lse", lse[pick], wl, tl)
 
 
+@pytest.mark.parametrize("dtype,H,dl,N,G", [("bf16", 4, 64, 150, 70), ("fp32", 1, 64, 150, 70), ("fp32", 16, 32, 150, 70),
+                                            ("bf16", 16, 256, 150, 100), ("bf16", 1, 16, 4500, 300), ("fp32", 2, 16, 4500, 300)])
+def test_shared_prefixes_of_many_groups(dtype, H, dl, N, G):
+    """More groups and sequences than a wave has lanes; groups of none and of one among them, prefixes of nothing."""
+    say(f"shared, many groups {dtype} {H} {dl} {N} {G}")
+    g = rng(9250)
+    starts = np.sort(g.integers(1, N - 1, G + 1))
+    plens = [int(x) for x in g.integers(0, 150, G)]
+    plens[::7] = [0] * len(plens[::7])
+    lens = [int(x) for x in g.integers(0, 60, N)]
+    case = (N, 2, H, dl, 16, 8, lens, plens, [int(x) for x in starts])
+    a, f = shared_inputs(case, dtype, 9251)
+    o, lse = gdn.mla_step_shared(*a, scale=0.1)
+    pick = sorted({0, 1, int(starts[0]), int(starts[0]) - 1, N // 2, N // 3, int(starts[-1]) - 1, int(starts[-1]), N - 1})
+    want, to, wl, tl = bound.shared(f[0][pick], f[1], f[2][pick], [lens[n] for n in pick], dl, f[5], f[6],
+                                    [sum(p < s for p in pick) for s in case[8]], 0.1, dtype)
+    within("o", o[pick], want, to)
+    within("lse", lse[pick], wl, tl)
+
+
 def test_caches_past_32_bits():
     """Pages whose elements lie past 2^32 of the cache: the same results, bit for bit, as from a small cache."""
     page, dl, dr, N = 64, 512, 64, 3
@@ -317,6 +337,61 @@ def test_weights_of_the_unusual():
     within("weights", got, want, tol)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("N,d", [(100, 40), (150, 88), (256, 160)])
+def test_weights_of_many_sequences(N, d, dtype):
+    """Waves that walk 32, 64 and 128 rows, the next sixteen requested while these are used; picked sequences."""
+    say(f"weights, many sequences {N} {d} {dtype}")
+    g, page, scale = rng(9710), 64, d ** -0.5
+    S, H, lens = 2, 3, [int(x) for x in g.integers(0, 2113, N)]
+    lens[:9] = [2112, 0, 1, 2, 511, 512, 513, 16, 1056]
+    t, order, _ = tables(g, lens, page)
+    q, qf = dev(g.standard_normal((N, S, H, d)), dtype)
+    cache, cf = pool(g, dtype, len(order), page, d, [(t, lens)])
+    pick = [0, 1, 2, 3, 4, 5, 6, 7, 8, N - 2, N - 1]
+    sub = (qf[pick], cf, t[pick], [lens[n] for n in pick])
+    some = latent.step(*sub, d, scale)[1]
+    lse = np.zeros((N, S, H))
+    lse[pick] = some
+    lse, lsef = dev(lse, "fp32")
+    old, oldf = dev(g.random((len(order), page)), "fp32")
+    known = [max(0, n - 40) for n in lens]
+    before = old.clone()
+    gdn.mla_weights(q, cache, ints(t), ints(lens), lse, old, ints(known), scale=scale, decay=0.5)
+    want, tol = bound.weights(*sub, lsef[pick], oldf, [known[n] for n in pick], scale, 0.5)
+    at = np.zeros(want.shape, bool)
+    held = np.zeros(want.shape, bool)
+    for n, m in enumerate(lens):
+        j = np.arange(m)
+        held[t[n, j // page], j % page] = True
+        if n in pick:
+            at[t[n, j // page], j % page] = True
+    assert at.sum() == sum(lens[n] for n in pick)
+    rows = torch.from_numpy(at).cuda()
+    within("weights", old[rows], want[at], tol[at])
+    rows = torch.from_numpy(~held).cuda()
+    assert torch.equal(old[rows], before[rows])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("d", [24, 64, 88, 128, 152, 184, 224, 248, 320, 360, 448, 488, 512, 576])
+def test_weights_of_every_width(d, many, dtype):
+    """Every number of column steps, with queries that stay in LDS and with more of them."""
+    say(f"weights, width {d} {many} {dtype}")
+    g, page, lens = rng(9720), 16, [37]
+    S, H = (33, 24) if many else (2, 5)
+    t, order, _ = tables(g, lens, page)
+    scale = d ** -0.5
+    q, qf = dev(g.standard_normal((1, S, H, d)), dtype)
+    cache, cf = pool(g, dtype, len(order), page, d, [(t, lens)])
+    lse, lsef = dev(latent.step(qf, cf, t, lens, d, scale)[1], "fp32")
+    old, oldf = dev(g.random((len(order), page)), "fp32")
+    gdn.mla_weights(q, cache, ints(t), ints(lens), lse, old, ints([20]), scale=scale, decay=0.5)
+    want, tol = bound.weights(qf, cf, t, lens, lsef, oldf, [20], scale, 0.5)
+    within("weights", old, want, tol)
+
+
 # ---------------------------------------------------------------- eviction
 
 EVICT = [
@@ -403,6 +478,29 @@ def test_eviction_with_entries_outside_the_pool():
     at = torch.from_numpy(at[..., 0].astype(np.int64).ravel()).cuda()
     assert torch.equal(bits(a[1]).flatten(0, 1), bits(c0).flatten(0, 1)[at])
     assert torch.equal(bits(a[0]).flatten(), bits(w0).flatten()[at])
+
+
+# table rows of more than 8192 rows, and of more than one workgroup of the choice takes
+EVICT_WIDE = [
+    (8, 64, [20000, 0, 9000, 3], [12345, 0, 8999, 2], 4, 300),
+    (40, 24, [32760, 8193], [1, 4000], 0, 0),
+    (8, 64, [40000, 5000, 0, 33001, 8192], [30000, 1200, 0, 17, 8191], 4, 64),
+    (16, 16, [33000, 16385, 40016], [32999, 16384, 3], 0, 2),
+]
+
+
+@pytest.mark.parametrize("ties", [False, True])
+@pytest.mark.parametrize("case", EVICT_WIDE, ids=lambda c: f"{c[0]}-{c[1]}-{max(c[2])}")
+def test_eviction_of_several_long_sequences(case, ties):
+    test_eviction(case, "bf16", ties)
+
+
+def test_eviction_of_thousands_of_sequences():
+    """More sequences than a wave has lanes, many times over: which of them a workgroup works on is found in two steps."""
+    g, N = rng(9962), 4500
+    lens = [int(x) for x in g.integers(0, 9, N)]
+    keep = [int(x) for x in g.integers(-1, 10, N)]
+    test_eviction((8, 4, lens, keep, 1, 1), "bf16", True)
 
 
 # ---------------------------------------------------------------- pages given back
@@ -569,6 +667,25 @@ def test_verify_large_vocabularies(V):
         accepted, tokens, logprobs = gdn.draft_verify(z, draft, u.cuda(), temperature=heat)
         assert accepted.tolist() == [0, 0] and tokens[:, 0].tolist() == [min(int(x), V - 1), V - 2]
         assert abs(float(logprobs[0, 0]) + np.log(V)) < 2 ** -20 * np.log(V)
+
+
+@pytest.mark.parametrize("V", [2 ** 20 + 5, 2 ** 26 - 20001])
+def test_verify_every_part_of_a_large_vocabulary(V):
+    """Equal logits, as above: places at both ends, between, and in the last piece, none of them skipped: u goes up by
+    single steps until u V lies at least 0.1 from a border."""
+    say(f"verify, all of V {V}")
+    z = torch.zeros((1, 1, V), dtype=torch.bfloat16, device="cuda")
+    none, ran = torch.zeros((1, 0), dtype=torch.int32, device="cuda"), 0
+    for place in (0, 2047, 2048, 64 * 2048 - 1, 64 * 2048, V // 3, V // 2, V - V // 5, V - 5000, (V - 1) // 2048 * 2048):
+        u = np.float32((place + 0.5) / V)
+        while float(u) * V < place or not 0.1 <= float(u) * V % 1 <= 0.9:
+            u = np.nextafter(u, np.float32(1))
+        x = int(float(u) * V)
+        assert place <= x < V and u < 1 and x // 2048 == place // 2048, (place, x)
+        _, tokens, _ = gdn.draft_verify(z, none, torch.tensor([[float(u)]], device="cuda"))
+        assert tokens.tolist() == [[x]], (place, tokens)
+        ran += x // 2048 == (V - 1) // 2048
+    assert ran >= 1
 
 
 def test_verify_ties_and_steps():
