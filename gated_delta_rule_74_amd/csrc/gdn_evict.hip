@@ -21,7 +21,7 @@
 // set a segment's flag before they wait for anything on its account: a wait
 // leads only to earlier draws, so every wait ends. The next segment's ticket and choice are requested
 // while this one's rows are on their way (256 sequences of up to 4096 rows of 160 bf16: 57 us one after the other, 45
-// so, 2.9 TB/s read and written; one of 131072 rows of 576: 53 us, 2.8 TB/s; a large copy makes 4.8).
+// so, 3.8 TB/s read and written; one of 131072 rows of 576: 53 us, 2.8 TB/s; a large copy makes 4.8).
 #include "gdn_serve.hpp"
 
 namespace gdn {

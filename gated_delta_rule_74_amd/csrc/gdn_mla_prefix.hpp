@@ -6,8 +6,10 @@
 // A prefix's rows are seen by every query of its group, thousands of them, so
 // this is a matrix product as in the attention of a prompt, without a mask: S^T =
 // K Q^T and O^T = V^T P^T over tiles of cached rows in LDS, a lane owning one
-// query, the probabilities at once the operand of the second product (in bf16
-// rounded to it, as in the step), V read from the same tile by transposing reads. A
+// query, the probabilities at once the operand of the second product, V read from the same tile by transposing
+// reads. (In bf16 they are rounded to it, as in the step: against 64 bits o is off by 0.0017 to 0.0020 of its size
+// where 32-bit probabilities leave the 0.0017 of its own rounding; two operands for their two halves would be half as
+// many products again.) A
 // wave takes 16 * QT queries of a group, which stay in registers; the waves of a
 // workgroup walk tiles of rows that they share, two tiles in LDS, the next one
 // requested before this one is used, straight from memory (through registers a
@@ -20,12 +22,14 @@
 // only grow from one piece to the next, and one of them does. The join adds up a query's parts.
 //
 // Measured: 256 sequences of up to 1024 rows behind a prefix of 16384, 16 heads of 128 + 32
-// bf16: 70 us and 9 us for the join. The vector instructions beside the products
-// (exponentials, sums, conversions: 140 for 36 products) bound it; the loads of a tile took
-// as many again before rows' addresses went through the wave and the walk lost its divisions.
-// 48 sequences of three drafts, four prefixes of 4096 to 8191 rows, 512 + 64 bf16: 70 and 15 us; LDS reads bound
-// it (a wave reads all of a tile for 16 queries, which is what its registers hold beside 512
-// columns of sums: 1.1 MB a tile and CU, 3.6 us of its 6), and the parts' 65 MB, written and read again.
+// bf16: 71 us and 10 us for the join; 48 sequences of three drafts, four prefixes of 4096 to 8191
+// rows, 512 + 64 bf16: 78 and 15 us. No unit is half busy (matrix products 23 and 19 % of the time,
+// vector instructions 29 and 17, LDS 18 and 23, which reads 256 bytes a cycle): of the waves' time
+// 41 and 42 % go by in waits for a tile or an operand, 25 and 32 % in waits to issue. A SIMD's two
+// waves go through scores, exponentials and values between the same barriers. 512 columns: a wave
+// reads all of a tile for 16 queries, which is what its registers hold beside their sums; the parts'
+// 61 MB are written and read again. (Loads of a tile took as many vector instructions again before
+// rows' addresses went through the wave and the walk lost its divisions.)
 #pragma once
 
 #include "gdn_lds_tile.hpp"
