@@ -222,8 +222,10 @@ hipError_t launch_page_fill(const PagePlanArgs &a, hipStream_t st) {
 
 // Pages behind shortened sequences, pushed on the stack: page_plan's first
 // half, with the columns between two lengths. One workgroup, bound by its chain
-// of sums (256 sequences of up to 130 tokens: 4.4 us, of up to 4096 7.7); the pages are spread over the threads, found by a binary search. Entries below 0 are
-// no pages (tables that an eviction takes may have them): where there are some, a prefix sum closes up the others.
+// of sums (256 sequences of up to 130 tokens: 4.4 us, of up to 4096: 7.7); the
+// pages are spread over the threads, found by a binary search. Entries below 0
+// are no pages (tables that an eviction takes may have them): where there are
+// some, a prefix sum closes up the others.
 constexpr unsigned TRIM = 8 * PL; // pages that are looked at together
 __global__ __launch_bounds__(PL) void page_trim_kernel(PageTrimArgs a) {
     __shared__ int ends[PL], from_s[PL];

@@ -133,7 +133,8 @@ def page_trim(lens, new_lens, block_table, free_pages, n_free, page_size, *, n_f
     """Pages behind sequences that became shorter (rejected drafts, evicted
     rows) back on the stack of free pages, without leaving the GPU: block_table
     [N, max_pages], lens and new_lens [N], free_pages [n_pages] (updated in
-    place), n_free [1], all int32. Returns the number of free pages afterwards
+    place), n_free [1], all int32; table entries below 0 are no pages and are
+    left out. Returns the number of free pages afterwards
     [1] (n_free_out=n_free updates it in place)."""
     _tensors(lens=lens, new_lens=new_lens, block_table=block_table, free_pages=free_pages, n_free=n_free)
     if block_table.dim() != 2 or free_pages.dim() != 1:
